@@ -1,4 +1,4 @@
-"""ctypes binding of libgqa_av.so (include/gqa_av.h).
+"""ctypes binding of libgqa_av.so (include/gqa_*.h).
 
 Argument marshalling only: every step of the reduction runs in the CUDA
 library. Import fails loudly when the library has not been built; there is no
@@ -91,6 +91,14 @@ def _load() -> ctypes.CDLL:
     lib.gqa_attn_device_status.argtypes = [P, I]
     lib.gqa_attn_last_error.argtypes = []
     lib.gqa_attn_last_error.restype = ctypes.c_char_p
+    L, F = ctypes.c_int64, ctypes.c_float
+    lib.gqa_kv_tables.argtypes = [P] * 11 + [I] * 6 + [P]
+    lib.gqa_kv_norm_rope_append.argtypes = [P, P, P, L, L, L, P, ctypes.POINTER(I), I, P, P, P, F,
+                                            F, I, P, P, I, P, P, *[I] * 8, P]
+    lib.gqa_kv_last_error.argtypes = []
+    lib.gqa_kv_last_error.restype = ctypes.c_char_p
+    for f in ("gqa_kv_tables", "gqa_kv_norm_rope_append"):
+        getattr(lib, f).restype = I
     for f in ("gqa_attn_decode", "gqa_attn_decode_tuned", "gqa_attn_plan", "gqa_attn_device_status"):
         getattr(lib, f).restype = I
     for f in ("gqa_av_decode", "gqa_av_decode_per_head", "gqa_av_decode_tuned", "gqa_av_decode_paged",
@@ -349,3 +357,111 @@ def gqa_attn_plan(B, Cmax, Hq, Hkv, D, kv_dtype=GQA_AV_BF16, mode=MODE_AUTO, con
 
 def gqa_attn_device_status(stream=None, clear: bool = True) -> None:
     _check_attn(lib.gqa_attn_device_status(_stream_handle(stream), 1 if clear else 0))
+
+
+# --------------------------------------------- block tables and cache write
+GQA_KV_F32 = 2
+
+
+def _check_kv(status: int) -> None:
+    if status != GQA_AV_OK:
+        name = lib.gqa_av_status_string(status).decode()
+        raise GqaAvError(status, f"{name}: {lib.gqa_kv_last_error().decode()}")
+
+
+def _int32(name: str, t, *shape) -> None:
+    """A contiguous CUDA int32 tensor of this shape (None: any size)."""
+    if (not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape)
+            or any(n is not None and n != m for n, m in zip(shape, t.shape))):
+        want = "[" + ", ".join("*" if n is None else str(n) for n in shape) + "]"
+        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of shape {want}, not "
+                         f"{t.dtype} {tuple(t.shape)}")
+
+
+def _pools(k_pool: torch.Tensor, v_pool: torch.Tensor):
+    if k_pool.dim() != 4 or tuple(v_pool.shape) != tuple(k_pool.shape):
+        raise ValueError("k_pool and v_pool must both be [num_blocks, block_size, Hkv, D], not "
+                         f"{tuple(k_pool.shape)} and {tuple(v_pool.shape)}")
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if k_pool.dtype not in _V_DTYPE or v_pool.dtype != k_pool.dtype:
+        raise ValueError("k_pool and v_pool must both be bfloat16 or both float16")
+    return tuple(k_pool.shape)
+
+
+def gqa_kv_tables(cached_lens, new_lens, free_list, free_count, block_table, seq_lens, token_start,
+                  slots, positions, free_left, block_size: int, num_blocks: int, pos_base=None,
+                  stream=None) -> None:
+    """Block-table entries, slots and positions of a step's new tokens: blocks come off the end
+    of ``free_list[:free_count]`` in request order and ``block_table`` is updated in place;
+    ``seq_lens``, ``token_start``, ``slots``, ``positions`` and ``free_left`` are written.
+    Requests that find no blocks keep their length and get slots of -1."""
+    _int32("block_table", block_table, None, None)
+    B, max_blocks = block_table.shape
+    for name, t in (("cached_lens", cached_lens), ("new_lens", new_lens), ("seq_lens", seq_lens)):
+        _int32(name, t, B)
+    if pos_base is not None:
+        _int32("pos_base", pos_base, B)
+    _int32("free_list", free_list, None)
+    _int32("free_count", free_count, 1)
+    _int32("free_left", free_left, 1)
+    _int32("token_start", token_start, B + 1)
+    _int32("slots", slots, None)
+    _int32("positions", positions, slots.shape[0])
+    _check_kv(lib.gqa_kv_tables(_ptr(cached_lens), _ptr(new_lens), _ptr(pos_base), _ptr(free_list),
+                                _ptr(free_count), _ptr(block_table), _ptr(seq_lens),
+                                _ptr(token_start), _ptr(slots), _ptr(positions), _ptr(free_left),
+                                B, slots.shape[0], max_blocks, free_list.shape[0], int(block_size),
+                                int(num_blocks), _stream_handle(stream)))
+
+
+def gqa_kv_norm_rope_append(q, k, v, positions, slots, inv_freq, q_out, k_pool, v_pool,
+                            q_weight=None, k_weight=None, eps: float = 1e-6,
+                            weight_offset: float = 0.0, sections=None, interleaved: bool = False,
+                            stream=None) -> torch.Tensor:
+    """Per-head RMS norm of q [T,Hq,D] and k [T,Hkv,D] (where a weight is given), rotation by
+    ``positions`` ([T], or [axes,T] with ``sections`` pairs an axis) times ``inv_freq``, queries to
+    ``q_out`` (float32 or the input type), keys and values to rows ``slots`` of the pools. q, k and
+    v may be views of one packed projection. Returns ``q_out``."""
+    num_blocks, block_size, Hkv, D = _pools(k_pool, v_pool)
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q must be [T,Hq,D], k and v [T,Hkv,D]")
+    T, Hq = q.shape[:2]
+    if (q.shape[2] != D or tuple(k.shape) != (T, Hkv, D) or tuple(v.shape) != (T, Hkv, D)
+            or tuple(q_out.shape) != (T, Hq, D)):
+        raise ValueError(f"inconsistent shapes: q {tuple(q.shape)}, k {tuple(k.shape)}, v "
+                         f"{tuple(v.shape)}, q_out {tuple(q_out.shape)}, pools "
+                         f"{tuple(k_pool.shape)}")
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        if not t.is_cuda or t.dtype != k_pool.dtype:
+            raise ValueError(f"{name} must be a CUDA tensor of the pools' type")
+        if T and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D)):
+            raise ValueError(f"a token's heads must be contiguous in {name}")
+    if not q_out.is_cuda or not q_out.is_contiguous() or q_out.dtype not in (torch.float32,
+                                                                             k_pool.dtype):
+        raise ValueError("q_out must be a contiguous CUDA tensor, float32 or of the pools' type")
+    _int32("slots", slots, T)
+    if positions.dim() == 1:
+        _int32("positions", positions, T)
+    else:
+        _int32("positions", positions, None, T)
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if (not inv_freq.is_cuda or inv_freq.dtype != torch.float32 or inv_freq.dim() != 1
+            or not inv_freq.is_contiguous()):
+        raise ValueError("inv_freq must be a contiguous CUDA float32 tensor of one dimension")
+    if sections is not None and len(sections) != axes:
+        raise ValueError(f"{len(sections)} sections for {axes} position axes")
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None and (not t.is_cuda or t.dtype != k_pool.dtype or tuple(t.shape) != (D,)
+                              or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous CUDA tensor [D] of the pools' type")
+    sec = None if sections is None else (ctypes.c_int * axes)(*[int(n) for n in sections])
+    od = GQA_KV_F32 if q_out.dtype == torch.float32 else _V_DTYPE[k_pool.dtype]
+    _check_kv(lib.gqa_kv_norm_rope_append(
+        _ptr(q), _ptr(k), _ptr(v), q.stride(0), k.stride(0), v.stride(0), _ptr(positions), sec,
+        axes, _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), float(eps), float(weight_offset),
+        1 if interleaved else 0, _ptr(slots), _ptr(q_out), od, _ptr(k_pool), _ptr(v_pool), T, Hq,
+        Hkv, D, 2 * inv_freq.shape[0], _V_DTYPE[k_pool.dtype], block_size, num_blocks,
+        _stream_handle(stream)))
+    return q_out
