@@ -9,7 +9,8 @@ the decode score step before it (include/gqa_qk.h):
 
 and both fused in one pass over the KV cache (include/gqa_attn.h). Around them
 for a paged cache: block tables, slots, and the norm, rotation and cache write of
-a step's tokens (include/gqa_kv.h).
+a step's tokens (include/gqa_kv.h), and decode attention over the paged cache for
+sequences that share prefixes (include/gqa_prefix.h).
 
 ``workloads`` (seeded inputs) imports without the CUDA library; the binding
 functions below need the built library and raise ImportError without it.
@@ -23,7 +24,8 @@ _BINDING = ("gqa_av_decode", "gqa_av_decode_per_head", "gqa_av_decode_tuned",
             "MODE_PER_HEAD", "MODE_GQA", "GQA_AV_BF16", "GQA_AV_FP16",
             "gqa_qk_softmax_decode", "gqa_qk_device_status", "gqa_av_decode_paged",
             "gqa_attn_decode", "gqa_attn_plan", "gqa_attn_device_status",
-            "gqa_kv_tables", "gqa_kv_norm_rope_append", "GQA_KV_F32")
+            "gqa_kv_tables", "gqa_kv_norm_rope_append", "GQA_KV_F32",
+            "gqa_prefix_attn_decode", "gqa_prefix_device_status")
 
 
 def __getattr__(name):

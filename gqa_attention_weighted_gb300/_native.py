@@ -97,7 +97,12 @@ def _load() -> ctypes.CDLL:
                                             F, I, P, P, I, P, P, *[I] * 8, P]
     lib.gqa_kv_last_error.argtypes = []
     lib.gqa_kv_last_error.restype = ctypes.c_char_p
-    for f in ("gqa_kv_tables", "gqa_kv_norm_rope_append"):
+    lib.gqa_prefix_attn_decode.argtypes = [P] * 9 + [I] * 10 + [F, P]
+    lib.gqa_prefix_device_status.argtypes = [P, I]
+    lib.gqa_prefix_last_error.argtypes = []
+    lib.gqa_prefix_last_error.restype = ctypes.c_char_p
+    for f in ("gqa_kv_tables", "gqa_kv_norm_rope_append", "gqa_prefix_attn_decode",
+              "gqa_prefix_device_status"):
         getattr(lib, f).restype = I
     for f in ("gqa_attn_decode", "gqa_attn_decode_tuned", "gqa_attn_plan", "gqa_attn_device_status"):
         getattr(lib, f).restype = I
@@ -465,3 +470,50 @@ def gqa_kv_norm_rope_append(q, k, v, positions, slots, inv_freq, q_out, k_pool, 
         Hkv, D, 2 * inv_freq.shape[0], _V_DTYPE[k_pool.dtype], block_size, num_blocks,
         _stream_handle(stream)))
     return q_out
+
+
+# ------------------------------------------- attention with shared prefixes
+def _check_prefix(status: int) -> None:
+    if status != GQA_AV_OK:
+        name = lib.gqa_av_status_string(status).decode()
+        raise GqaAvError(status, f"{name}: {lib.gqa_prefix_last_error().decode()}")
+
+
+def gqa_prefix_attn_decode(q, k_pool, v_pool, prefix_table, prefix_lens, group_start, block_table,
+                           seq_lens, out, scale=None, stream=None) -> torch.Tensor:
+    """Decode attention over a paged cache: sequence b attends to the ``prefix_lens[p]`` rows of its
+    group's ``prefix_table[p]`` (group p: ``group_start[p] <= b < group_start[p + 1]``; None: one
+    group of all) and to its own ``seq_lens[b]`` rows of ``block_table[b]``. ``prefix_table`` None:
+    no shared prefixes; ``block_table`` None: no own rows. q and out are [B,Hq,D] of the pools' type
+    (scale defaults to 1/sqrt(D)); writes and returns ``out``."""
+    num_blocks, block_size, Hkv, D = _pools(k_pool, v_pool)
+    if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape:
+        raise ValueError(f"q and out must be [B,Hq,{D}], not {tuple(q.shape)} and "
+                         f"{tuple(out.shape)}")
+    B, Hq = q.shape[:2]
+    for name, t in (("q", q), ("out", out)):
+        if not t.is_cuda or not t.is_contiguous() or t.dtype != k_pool.dtype:
+            raise ValueError(f"{name} must be a contiguous CUDA tensor of the pools' type")
+    P = max_pblocks = max_blocks = 0
+    if prefix_table is not None:
+        _int32("prefix_table", prefix_table, None, None)
+        P, max_pblocks = prefix_table.shape
+        _int32("prefix_lens", prefix_lens, P)
+        if group_start is not None:
+            _int32("group_start", group_start, P + 1)
+    if block_table is not None:
+        _int32("block_table", block_table, B, None)
+        max_blocks = block_table.shape[1]
+    if seq_lens is not None:
+        _int32("seq_lens", seq_lens, B)
+    sc = float(D) ** -0.5 if scale is None else float(scale)
+    _check_prefix(lib.gqa_prefix_attn_decode(
+        _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(prefix_table) if P else None,
+        _ptr(prefix_lens) if P else None, _ptr(group_start) if P else None, _ptr(block_table),
+        _ptr(seq_lens), _ptr(out), B, P, Hq, Hkv, D, _V_DTYPE[k_pool.dtype], block_size, num_blocks,
+        max_pblocks, max_blocks, sc, _stream_handle(stream)))
+    return out
+
+
+def gqa_prefix_device_status(stream=None, clear: bool = True) -> None:
+    _check_prefix(lib.gqa_prefix_device_status(_stream_handle(stream), 1 if clear else 0))

@@ -11,6 +11,7 @@
 #include <type_traits>
 
 #include "gqa_av_kernel.cuh"
+#include "gqa_pack.cuh"
 
 namespace gqa_av {
 
@@ -185,17 +186,6 @@ __device__ __forceinline__ void pair_rotation(unsigned long long turn64, int pos
   const unsigned long long x = turn64 * static_cast<unsigned long long>(static_cast<long long>(pos));
   const float half_turns = static_cast<float>(static_cast<int32_t>(x >> 32)) * 4.656612873077393e-10f;
   sincospif(half_turns, s, c);
-}
-
-template <typename Tag>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (std::is_same<Tag, Bf16Tag>::value) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
 }
 
 // A warp takes part of a token's heads, 32 / L heads a step: a lane owns 8

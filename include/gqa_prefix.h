@@ -1,0 +1,83 @@
+/*
+ * gqa_prefix.h -- C ABI of the GB300 (sm_103a) decode attention over a paged
+ * KV cache for a batch whose sequences share prefixes: each shared prefix is
+ * read and multiplied once for all sequences behind it.
+ *
+ * The sequences of the batch lie in groups: group p holds the sequences
+ * group_start[p] <= b < group_start[p + 1], which share the prefix_lens[p]
+ * rows that row p of prefix_table lists. Behind its group's prefix every
+ * sequence has seq_lens[b] rows of its own, in the blocks of row b of
+ * block_table. With K_b and V_b the prefix rows followed by the own rows,
+ *
+ *     out[b, q_h, :] = sum_c softmax_c(scale * q[b, q_h, :] . K_b[c, kv_h, :]) * V_b[c, kv_h, :],
+ *     kv_h = q_h / G,   G = Hq / Hkv.
+ *
+ * A sequence in no group has no prefix; P = 0 means that none has, which is
+ * plain decode attention over a paged cache. A sequence with no rows at all
+ * gives out = 0.
+ *
+ *     q, out             [B, Hq, D]                          kv_dtype (bf16 or fp16)
+ *     k_pool, v_pool     [num_blocks, block_size, Hkv, D]    kv_dtype
+ *     prefix_table       [P, max_prefix_blocks] int32
+ *     prefix_lens        [P] int32
+ *     group_start        [P + 1] int32, not decreasing; NULL with P = 1: all
+ *                        sequences share the one prefix
+ *     block_table        [B, max_blocks] int32, or NULL with max_blocks = 0:
+ *                        no sequence has rows of its own
+ *     seq_lens           [B] int32, or NULL meaning max_blocks * block_size
+ * (all contiguous device memory). Lengths are clamped to what their table row
+ * can hold, group starts to [0, B] and to their predecessors. Row c is in
+ * block table[c / block_size] at c % block_size; a table entry outside
+ * [0, num_blocks) reads rows of zeros. Entries of blocks past a length, and
+ * rows past a length inside a block, may hold anything.
+ *
+ * Numerics: products on the tensor cores with fp32 accumulation; the running
+ * maximum and sum of the softmax and the output sums are fp32; the weights
+ * exp(s - m) are rounded once to kv_dtype before they multiply V (their fp32
+ * values make the sum), out once at the end. Repeated calls with the same
+ * shapes and lengths give bitwise-identical out.
+ *
+ * Limits: D 64, 128 or 256; G <= 128; block_size a multiple of 8; q, out and
+ * the pools 16-byte aligned; B <= 4096, P <= 128; num_blocks * block_size and
+ * what one table row can hold below 2^31 rows.
+ *
+ * Execution: asynchronous on `stream`, no host synchronisation; the lengths
+ * and groups are read on the device, so a captured graph follows them. The
+ * call keeps its own per-device workspace, grown on demand with cudaMalloc
+ * outside stream capture (a buffer that it outgrows is kept until the process
+ * ends, since captured graphs may hold it); calls that may overlap on the GPU
+ * must not be issued concurrently. Errors: a status code from gqa_av.h; on
+ * error nothing is launched and gqa_prefix_last_error() holds a message.
+ */
+#ifndef GQA_PREFIX_H
+#define GQA_PREFIX_H
+
+#include <stddef.h>
+#include <stdint.h>
+
+#include "gqa_av.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+int gqa_prefix_attn_decode(const void *q, const void *k_pool, const void *v_pool,
+                           const int32_t *prefix_table, const int32_t *prefix_lens,
+                           const int32_t *group_start, const int32_t *block_table,
+                           const int32_t *seq_lens, void *out, int B, int P, int Hq, int Hkv,
+                           int D, int kv_dtype, int block_size, int num_blocks,
+                           int max_prefix_blocks, int max_blocks, float scale, void *stream);
+
+/* Synchronise `stream`, then read the call's device status word (set when a
+ * bounded wait inside a kernel runs out): GQA_AV_OK or
+ * GQA_AV_ERR_DEVICE_TIMEOUT; with clear != 0 the word is reset. */
+int gqa_prefix_device_status(void *stream, int clear);
+
+/* Message of the calling thread's last error of these calls ("" if none). */
+const char *gqa_prefix_last_error(void);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* GQA_PREFIX_H */
