@@ -1,11 +1,17 @@
-// Host side of the C ABI declared in include/gqa_prefix.h: argument checks and
-// dispatch.
+// Host side of the C ABI declared in include/gqa_prefix.h: argument checks, the
+// call's workspace, tensor maps and dispatch to the attention and combine
+// kernels.
+#include <cuda.h>
 #include <cuda_runtime.h>
+#include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
+#include <map>
+#include <mutex>
 #include <string>
 
 #include "gqa_prefix.h"
@@ -13,6 +19,8 @@
 
 namespace gqa_av {
 namespace {
+
+constexpr long long kPxTimeoutNs = 2000000000LL;   // 2 s bound on every mbarrier wait
 
 thread_local std::string g_px_error;
 
@@ -73,13 +81,124 @@ int check_args(const void* q, const void* k_pool, const void* v_pool, const int3
   return GQA_AV_OK;
 }
 
-using SimpleKernel = void (*)(PrefixParams);
+using PrefixKernel = void (*)(PrefixParams);
 
 template <typename Tag>
-SimpleKernel pick_simple(int D) {
-  return D == 64 ? gqa_prefix_simple_kernel<Tag, 64>
-                 : D == 128 ? gqa_prefix_simple_kernel<Tag, 128> : gqa_prefix_simple_kernel<Tag, 256>;
+PrefixKernel pick_main(int D) {
+  return D == 64 ? gqa_prefix_kernel<Tag, 64>
+                 : D == 128 ? gqa_prefix_kernel<Tag, 128> : gqa_prefix_kernel<Tag, 256>;
 }
+template <typename Tag>
+PrefixKernel pick_combine(int D) {
+  return D == 64 ? gqa_prefix_combine_kernel<Tag, 64>
+                 : D == 128 ? gqa_prefix_combine_kernel<Tag, 128>
+                            : gqa_prefix_combine_kernel<Tag, 256>;
+}
+int smem_bytes(int D) {
+  return D == 64 ? PxShape<64>::SMEM : D == 128 ? PxShape<128>::SMEM : PxShape<256>::SMEM;
+}
+
+struct Ws {
+  char* base = nullptr;
+  size_t bytes = 0;
+};
+std::mutex g_px_mu;
+std::map<int, Ws> g_px_ws;
+
+// The device's workspace, grown to `need` bytes. Outgrown buffers are kept: a
+// captured graph may hold their addresses.
+int workspace(int dev, size_t need, cudaStream_t stream, char** out) {
+  std::lock_guard<std::mutex> lk(g_px_mu);
+  Ws& w = g_px_ws[dev];
+  if (w.bytes < need) {
+    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream, &cs);
+    if (e != cudaSuccess) return pfail_cuda(e, "cudaStreamIsCapturing");
+    if (cs != cudaStreamCaptureStatusNone)
+      return pfail(GQA_AV_ERR_NOMEM,
+                   "workspace must grow to %zu B but the stream is capturing; make one call with "
+                   "the largest shape before capture",
+                   need);
+    const size_t bytes = std::max(need, w.bytes + w.bytes / 2);
+    void* p = nullptr;
+    e = cudaMalloc(&p, bytes);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      return pfail(GQA_AV_ERR_NOMEM, "cudaMalloc(%zu) failed: %s", bytes, cudaGetErrorString(e));
+    }
+    e = cudaMemset(p, 0, sizeof(PxHeader));
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+    if (e != cudaSuccess) {
+      cudaFree(p);
+      return pfail_cuda(e, "zeroing the workspace header");
+    }
+    w.base = static_cast<char*>(p);
+    w.bytes = bytes;
+  }
+  *out = w.base;
+  return GQA_AV_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 g_px_encode = nullptr;
+
+// A map over 16-bit elements: `rank` dimensions, boxes 64 elements wide in the
+// 128-byte swizzle. What lies outside reads as zeros.
+int encode(CUtensorMap* m, const void* x, int rank, const cuuint64_t* dims,
+           const cuuint64_t* strides, const cuuint32_t* box, const char* what) {
+  {
+    std::lock_guard<std::mutex> lk(g_px_mu);
+    if (!g_px_encode) {
+      void* f = nullptr;
+      cudaDriverEntryPointQueryResult q;
+      cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                       cudaEnableDefault, &q);
+      if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !f)
+        return pfail(GQA_AV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+      g_px_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }
+  }
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_px_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(x), dims,
+                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return pfail(GQA_AV_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled (%s) failed (%d)", what, (int)r);
+  return GQA_AV_OK;
+}
+
+int encode_maps(PrefixParams* p, const void* q, const void* k_pool, const void* v_pool, int D) {
+  const cuuint64_t d = D, G = p->G, Hkv = p->Hkv, rows = static_cast<cuuint64_t>(p->bs) * p->num_blocks;
+  const cuuint64_t qd[4] = {d, G, Hkv, static_cast<cuuint64_t>(p->B)};
+  const cuuint64_t qs[3] = {d * 2, G * d * 2, Hkv * G * d * 2};
+  const cuuint32_t tile[4] = {64, static_cast<cuuint32_t>(p->G), 1, static_cast<cuuint32_t>(p->TB)};
+  const cuuint32_t one[4] = {64, static_cast<cuuint32_t>(p->G), 1, 1};
+  const cuuint64_t kd[3] = {d, Hkv, rows};
+  const cuuint64_t ks[2] = {d * 2, Hkv * d * 2};
+  const cuuint32_t kb[3] = {64, 1, static_cast<cuuint32_t>(p->R)};
+  int rc = encode(&p->q_tile_map, q, 4, qd, qs, tile, "q");
+  if (!rc) rc = encode(&p->q_one_map, q, 4, qd, qs, one, "q");
+  if (!rc) rc = encode(&p->k_map, k_pool, 3, kd, ks, kb, "K");
+  if (!rc) rc = encode(&p->v_map, v_pool, 3, kd, ks, kb, "V");
+  return rc;
+}
+
+cudaError_t launch_pdl(const void* fn, int grid, int block, size_t smem, cudaStream_t stream,
+                       void** args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 }  // namespace gqa_av
@@ -97,27 +216,95 @@ extern "C" int gqa_prefix_attn_decode(
                       seq_lens, out, B, P, Hq, Hkv, D, kv_dtype, block_size, num_blocks,
                       max_prefix_blocks, max_blocks, scale);
   if (rc) return rc;
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return pfail_cuda(e, "cudaGetDevice");
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+
   PrefixParams p;
-  p.q = q; p.k_pool = k_pool; p.v_pool = v_pool;
   p.prefix_table = prefix_table; p.prefix_lens = prefix_lens; p.group_start = group_start;
   p.block_table = block_table; p.seq_lens = seq_lens; p.out = out;
-  p.B = B; p.P = P; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv;
+  p.B = B; p.P = P; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.TB = 128 / p.G;
   p.bs = block_size; p.num_blocks = num_blocks;
   p.max_pblocks = max_prefix_blocks; p.max_blocks = max_blocks;
-  p.qscale = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);  // log2(e)
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  SimpleKernel k = kv_dtype == GQA_AV_BF16 ? pick_simple<Bf16Tag>(D) : pick_simple<Fp16Tag>(D);
-  k<<<B * Hq, 128, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
+  const int keys = D == 256 ? PxShape<256>::KEYS : PxShape<128>::KEYS;
+  for (p.R = 8; p.R < keys && block_size % (2 * p.R) == 0;) p.R *= 2;
+  // log2(e) in the scale; a scale of 0 becomes the smallest normal number, which
+  // leaves every finite score at 0 and keeps masked ones at -inf.
+  const double s2 = std::fabs(static_cast<double>(scale)) * 1.4426950408889634;
+  if (s2 > FLT_MAX) return pfail(GQA_AV_ERR_UNSUPPORTED, "scale=%g is too large", (double)scale);
+  p.qscale = std::max(static_cast<float>(s2), FLT_MIN);
+  p.negate = scale < 0.0f;
+  // Cost model of the plan, in SM cycles: a key tile of 64 KiB streams from
+  // HBM in about 2800 (all SMs together); its products take 1024 a query tile
+  // at D >= 128 (the softmax as long at D = 64) and a little more measured.
+  p.c_pair = D == 64 ? 1200.0f : 2300.0f;
+  p.c_tile = D == 64 ? 700.0f : 1300.0f;
+  p.c_own = D == 64 ? 1400.0f : 2800.0f;
+  p.c_unit = 4000.0f;
+  p.timeout_ns = kPxTimeoutNs;
+
+  const int ns = D == 256 ? 1 : 2;
+  const size_t q_tiles = static_cast<size_t>((B + p.TB - 1) / p.TB + std::min(P, B)) * Hkv;
+  const size_t prefix_slots = P ? q_tiles + 2 * static_cast<size_t>(sms) : 0;
+  const size_t own_slots = max_blocks ? static_cast<size_t>(B) * Hkv + 4 * static_cast<size_t>(sms) : 0;
+  if (prefix_slots + own_slots > 0x3fffffffu)
+    return pfail(GQA_AV_ERR_UNSUPPORTED, "too many units of work");
+  p.prefix_slots = static_cast<int>(prefix_slots);
+  const size_t at_po = up256(sizeof(PxHeader));
+  const size_t at_pm = at_po + prefix_slots * ns * 128 * D * 4;
+  const size_t at_oo = at_pm + prefix_slots * ns * 128 * 8;
+  const size_t at_om = at_oo + up256(own_slots * p.G * D * 4);
+  char* base = nullptr;
+  if ((rc = workspace(dev, at_om + own_slots * p.G * 8, stream, &base))) return rc;
+  p.head = reinterpret_cast<PxHeader*>(base);
+  p.prefix_o = reinterpret_cast<float*>(base + at_po);
+  p.prefix_ml = reinterpret_cast<float2*>(base + at_pm);
+  p.own_o = reinterpret_cast<float*>(base + at_oo);
+  p.own_ml = reinterpret_cast<float2*>(base + at_om);
+  if ((rc = encode_maps(&p, q, k_pool, v_pool, D))) return rc;
+
+  const bool bf = kv_dtype == GQA_AV_BF16;
+  const void* k = reinterpret_cast<const void*>(bf ? pick_main<Bf16Tag>(D) : pick_main<Fp16Tag>(D));
+  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(D));
+  if (e != cudaSuccess) return pfail_cuda(e, "cudaFuncSetAttribute");
+  void* args[] = {&p};
+  e = launch_pdl(k, sms, kPxThreads, smem_bytes(D), stream, args);
   if (e != cudaSuccess) return pfail_cuda(e, "attention kernel launch");
+  k = reinterpret_cast<const void*>(bf ? pick_combine<Bf16Tag>(D) : pick_combine<Fp16Tag>(D));
+  e = launch_pdl(k, B * Hkv, kPxCombineThreads, 0, stream, args);
+  if (e != cudaSuccess) {
+    cudaMemsetAsync(&p.head->next, 0, sizeof p.head->next, stream);   // the combine's job
+    return pfail_cuda(e, "combine kernel launch");
+  }
   return GQA_AV_OK;
 }
 
 extern "C" int gqa_prefix_device_status(void* stream_, int clear) {
-  (void)clear;
   g_px_error.clear();
-  cudaError_t e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream_));
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return pfail_cuda(e, "cudaGetDevice");
+  e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream_));
   if (e != cudaSuccess) return pfail_cuda(e, "cudaStreamSynchronize");
+  char* base = nullptr;
+  {
+    std::lock_guard<std::mutex> lk(g_px_mu);
+    auto it = g_px_ws.find(dev);
+    if (it != g_px_ws.end()) base = it->second.base;
+  }
+  if (!base) return GQA_AV_OK;
+  unsigned word = 0;
+  e = cudaMemcpy(&word, base, sizeof word, cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess) return pfail_cuda(e, "reading the status word");
+  if (word && clear) {
+    e = cudaMemset(base, 0, sizeof word);
+    if (e != cudaSuccess) return pfail_cuda(e, "clearing the status word");
+  }
+  if (word)
+    return pfail(GQA_AV_ERR_DEVICE_TIMEOUT, "a bounded wait in the attention kernel ran out (0x%x)",
+                 word);
   return GQA_AV_OK;
 }
 

@@ -1,97 +1,989 @@
 // Decode attention over a paged KV cache with shared prefixes, sm_103a. The
 // operation is stated in include/gqa_prefix.h.
+//
+// Rows. For one KV head the G query heads of every sequence behind a prefix
+// form the rows of one matrix: a query tile is TB = 128 / G sequences (TB * G
+// <= 128 rows), so a prefix key that is read once meets 128 rows, or 256 where
+// two tiles run together. A sequence's own keys meet its G rows only.
+//
+// Units. The work is cut into units: prefix units (group, KV head, split of
+// the prefix, query tile or pair of tiles; tiles fastest, so the CTAs that
+// need the same keys take them at the same time) and then the sequences' own
+// units (sequence, KV head, split). A persistent CTA takes unit blockIdx.x
+// first and then the next free one from a counter. A unit writes its
+// unnormalised output, maximum and sum to a slot of its own, and the combine
+// kernel adds a row's slots in split order: who computed a unit does not
+// matter for the result.
+//
+// A unit runs an online softmax over tiles of KEYS keys:
+//   S = Q K^T     tcgen05.mma, M = 128 rows, N = KEYS, Q and K from shared
+//                 memory (K-major, 128-byte swizzle), S in tensor memory;
+//   P = 2^(S' - m) by one softmax warpgroup, a row a thread, S' = S * scale *
+//                 log2 e; P goes back to tensor memory over S as 16 bits;
+//   O += P V      tcgen05.mma with P as the A operand from tensor memory and V
+//                 from shared memory (MN-major), O in tensor memory.
+// m moves only when a row's maximum has grown by more than 2^8 (then O and l
+// are rescaled), so O is rarely touched; weights stay below 2^8.
+//
+// D <= 128: two streams (S, O and a softmax warpgroup each) work in turn, so
+// the tensor core multiplies for one while the other makes weights. The
+// streams take the two query tiles of a pair and share every K and V stage, or
+// the even and odd key tiles of a single query tile, merged at the unit's end.
+// D = 256: O fills half of the tensor memory, so there is one stream with two
+// S buffers and key tiles of 64.
+//
+// Warps: 0-3 and 4-7 softmax warpgroups (and the units' ends), 8 issues the
+// MMAs from one thread, 9 makes the plan, hands out units and issues the TMA
+// loads, one box a lane. Every wait is bounded (2 s): on expiry the role sets
+// the status word and leaves, the others run out in turn, copies and MMAs in
+// flight are waited for and tensor memory is freed.
 #pragma once
 
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
-#include "gqa_av_kernel.cuh"
+#include "gqa_av_mma.cuh"
 #include "gqa_pack.cuh"
 
 namespace gqa_av {
 
-struct PrefixParams {
-  const void *q, *k_pool, *v_pool;
-  const int32_t *prefix_table, *prefix_lens, *group_start, *block_table, *seq_lens;
-  void* out;
-  int B, P, Hq, Hkv, G;
-  int bs, num_blocks, max_pblocks, max_blocks;
-  float qscale;                 // scale * log2(e)
+constexpr int kPxThreads = 320;
+constexpr int kPxMmaWarp = 8, kPxLoadWarp = 9;
+constexpr int kPxMaxGroups = 128;
+constexpr int kPxMaxB = 4096;
+constexpr int kPxSegs = 4;             // unit descriptors in flight
+constexpr int kPxMaxStages = 12;
+constexpr float kPxGrow = 8.0f;        // log2 of the growth of a maximum that is tolerated
+constexpr unsigned kErrPxLoad = 16u, kErrPxMma = 32u, kErrPxSoftmax = 64u;
+
+template <int D>
+struct PxShape {
+  static constexpr int NS = D == 256 ? 1 : 2;          // streams
+  static constexpr int KEYS = D == 256 ? 64 : 128;     // keys of a tile
+  static constexpr int PARTS = D / 64;                 // 64-column parts of a row
+  static constexpr int STAGE = KEYS * D * 2;           // bytes of a K or V stage
+  static constexpr int QBYTES = 128 * D * 2;
+  static constexpr int QBUF = NS;                      // query buffers
+  static constexpr int STAGES = D == 64 ? 11 : 5;
+  static constexpr int TILES_BYTES = QBUF * QBYTES + STAGES * STAGE;
+  static constexpr int SMEM = TILES_BYTES + 3072;
+  static constexpr uint32_t S_COL = KEYS;              // tensor-memory columns of an S buffer
+  static constexpr uint32_t O_COL0 = 256;
 };
 
-// One CTA per (sequence, query head): its warps take every fourth key, a lane
-// D / 32 elements of it, with a running maximum and sum; the warps' results
-// are merged at the end. fp32 throughout, the weights not rounded.
+// A group's part of the plan, as the combine kernel reads it.
+struct PxGroup {
+  int begin, end;     // sequences
+  int splits;         // 0: no prefix rows
+  int nq;             // units a split and KV head: query tiles, or pairs of them
+  int pair;           // two query tiles a unit
+  int base;           // its first unit
+};
+struct PxHeader {
+  unsigned status;
+  int next;                       // units handed out past the first of each CTA
+  int own_tiles;                  // key tiles of a sequence's own unit
+  int pad[61];
+  PxGroup group[kPxMaxGroups];
+  int own_base[kPxMaxB];          // first own unit (slot) of each sequence
+};
+
+struct alignas(64) PrefixParams {
+  CUtensorMap q_tile_map;         // q as {D, G, Hkv, B}; box {64, G, 1, TB}
+  CUtensorMap q_one_map;          // box {64, G, 1, 1}
+  CUtensorMap k_map, v_map;       // pools as {D, Hkv, rows}; box {64, 1, R}
+  const int32_t *prefix_table, *prefix_lens, *group_start, *block_table, *seq_lens;
+  void* out;
+  PxHeader* head;
+  float* prefix_o;                // prefix slots [units][NS][D / 4][128][4]
+  float2* prefix_ml;              // [units][NS][128] (maximum in log2 units, sum)
+  float* own_o;                   // own slots [units][D / 4][G][4]
+  float2* own_ml;                 // [units][G]
+  int B, P, Hq, Hkv, G, TB;
+  int bs, num_blocks, max_pblocks, max_blocks;
+  int R;                          // rows of a K or V box: gcd(bs, KEYS)
+  float qscale;                   // |scale| * log2(e)
+  int negate;                     // scale < 0
+  int prefix_slots;               // bound on the prefix units
+  float c_pair, c_tile, c_own, c_unit;   // plan: cost of a key tile of each kind and of a unit
+  long long timeout_ns;
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands of one type.
+__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// kind::f16 with fp32 D, M = 128, N = n; b_mn: B is MN-major.
+template <typename Tag>
+__host__ __device__ constexpr uint32_t px_idesc(int n, bool b_mn) {
+  return (1u << 4) | (std::is_same<Tag, Bf16Tag>::value ? ((1u << 7) | (1u << 10)) : 0u) |
+         (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// A wait by a whole warp; the lanes agree on whether it ran out, so that they
+// leave together.
+__device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity, long long timeout_ns) {
+  return __all_sync(0xffffffffu, mbar_poll(bar, parity, timeout_ns));
+}
+
+// Keeps uses of values that tcgen05.ld delivers behind its wait.
+template <int N>
+__device__ __forceinline__ void hold(float* v) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
+}
+
+// What the consumers of a unit need to know.
+struct PxUnit {
+  int tiles;          // key tiles; 0: no more units
+  int pair;           // two query tiles, each with all key tiles
+  int rows[2];        // rows of the query tiles
+  int last_valid;     // keys of the last tile
+  int slot;           // its slot
+  int own;            // a sequence's own unit
+};
+
+// Positions of a unit's K and V tiles in its run of 2 * tiles stages, in the
+// order of their first use: K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
+__device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
+__device__ __forceinline__ int v_pos(int i, int n) { return min(2 * i + 2, 2 * n - 1); }
+
+__device__ __forceinline__ int warp_sum(int x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ int warp_incl_sum(int x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// The plan, made by a whole warp from the lengths: lane l holds groups 32 j + l
+// and the unit sums of the blocks 32 j + l of 32 sequences.
+template <int D>
+struct PxPlan {
+  using Shape = PxShape<D>;
+  static constexpr int J = kPxMaxGroups / 32;
+  int begin[J], end[J], len[J], tiles[J], splits[J], nq[J], pair[J], upto[J];
+  int prefix_units, own_tiles, own_units;
+  int own_upto[J];
+
+  static __device__ __forceinline__ int own_len(const PrefixParams& p, int b) {
+    const int cap = p.max_blocks * p.bs;
+    return b < p.B ? (p.seq_lens ? min(max(p.seq_lens[b], 0), cap) : cap) : 0;
+  }
+  static __device__ __forceinline__ int tiles_of(int len) {
+    return len / Shape::KEYS + (len % Shape::KEYS != 0);
+  }
+
+  __device__ void make(const PrefixParams& p) {
+    const int lane = threadIdx.x & 31;
+    const int n = gridDim.x;
+    // Own tiles of the batch, and how many of them a unit takes: about four
+    // units a CTA, so that the last ones to end are short.
+    const int blocks = (p.B + 31) / 32;
+    long long own = 0;
+    int seqs = 0;
+    if (p.max_blocks > 0)
+      for (int k = 0; k < blocks; ++k) {
+        const int t = tiles_of(own_len(p, 32 * k + lane));
+        own += t;
+        seqs += t > 0;
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
+    own *= p.Hkv;
+    own_tiles = static_cast<int>(max(1LL, (own + 4LL * n - 1) / (4LL * n)));
+    // Groups.
+    int carry = 0, carry_n = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      begin[j] = end[j] = len[j] = tiles[j] = splits[j] = nq[j] = pair[j] = 0;
+      upto[j] = 0;
+      if (32 * j < p.P) {
+        const int g = 32 * j + lane;
+        int a = 0, e = 0;
+        if (g < p.P) {
+          a = p.group_start ? min(max(p.group_start[g], 0), p.B) : 0;
+          e = p.group_start ? min(max(p.group_start[g + 1], 0), p.B) : p.B;
+          len[j] = min(max(p.prefix_lens[g], 0), p.max_pblocks * p.bs);
+        }
+        a = max(a, carry);
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, a, o);
+          if (lane >= o) a = max(a, y);
+        }
+        carry = __shfl_sync(0xffffffffu, a, 31);
+        begin[j] = a;
+        end[j] = max(a, e);
+        tiles[j] = end[j] > begin[j] && len[j] > 0 ? tiles_of(len[j]) : 0;
+      }
+    }
+    // How to cut the prefixes: each lane costs one choice of pairs or single
+    // tiles and of the tiles a split takes (1 to 8 units a CTA), from the
+    // time that the units take if all CTAs stay busy, own units included, and
+    // from the CTA with the most prefix units.
+    const bool pairs = Shape::NS == 2 && (lane & 1);
+    double cost[2] = {0.0, 0.0};     // prefix key tiles x query tiles, single and paired
+    long long items[2] = {0, 0};
+    int longest = 0;
+    for (int g = 0; g < p.P; ++g) {
+      int t = 0, m = 0;
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (g / 32 == j) {
+          t = __shfl_sync(0xffffffffu, tiles[j], g % 32);
+          m = __shfl_sync(0xffffffffu, end[j] - begin[j], g % 32);
+        }
+      if (t == 0) continue;
+      const int q = (m + p.TB - 1) / p.TB;
+      cost[0] += static_cast<double>(t) * q;
+      cost[1] += static_cast<double>(t) * ((q + 1) / 2);
+      items[0] += q;
+      items[1] += (q + 1) / 2;
+      longest = max(longest, t);
+    }
+    prefix_units = 0;
+    int cut = 1;
+    bool use_pairs = false;
+    if (longest > 0) {
+      const int r = (lane >> 2) + 1;
+      const double w = cost[pairs] * p.Hkv;
+      long long chunk = static_cast<long long>(ceil(w / (static_cast<double>(r) * n))) + ((lane >> 1) & 1);
+      if (lane >= 30) chunk = longest;   // no cut: always within the slots
+      chunk = max(1LL, min(chunk, static_cast<long long>(longest)));
+      long long units = 0;
+      for (int g = 0; g < p.P; ++g) {
+        int t = 0, m = 0;
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+          if (g / 32 == j) {
+            t = __shfl_sync(0xffffffffu, tiles[j], g % 32);
+            m = __shfl_sync(0xffffffffu, end[j] - begin[j], g % 32);
+          }
+        const int q = (m + p.TB - 1) / p.TB;
+        units += (t + chunk - 1) / chunk * (pairs ? (q + 1) / 2 : q);
+      }
+      units *= p.Hkv;
+      const float c = pairs ? p.c_pair : p.c_tile;
+      const float one = static_cast<float>(chunk) * c + p.c_unit;
+      const float all = (static_cast<float>(w) * c + static_cast<float>(units) * p.c_unit +
+                         static_cast<float>(own) * p.c_own) / static_cast<float>(n);
+      float est = fmaxf(all, static_cast<float>((units + n - 1) / n) * one);
+      if (units > p.prefix_slots) est = INFINITY;
+      float best = est;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
+      const int src = __ffs(__ballot_sync(0xffffffffu, est == best)) - 1;
+      cut = __shfl_sync(0xffffffffu, static_cast<int>(chunk), src);
+      use_pairs = __shfl_sync(0xffffffffu, static_cast<int>(pairs), src);
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if (32 * j < p.P) {
+        if (tiles[j] > 0) {
+          const int q = (end[j] - begin[j] + p.TB - 1) / p.TB;
+          pair[j] = use_pairs && q > 1;
+          nq[j] = pair[j] ? (q + 1) / 2 : q;
+          splits[j] = (tiles[j] + cut - 1) / cut;
+        }
+        upto[j] = carry_n + warp_incl_sum(nq[j] * splits[j] * p.Hkv);
+        carry_n = __shfl_sync(0xffffffffu, upto[j], 31);
+      }
+    }
+    prefix_units = carry_n;
+    // Unit sums of the blocks of 32 sequences.
+    own_units = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) own_upto[j] = 0;
+    if (p.max_blocks > 0) {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        for (int k = 32 * j; k < min(blocks, 32 * (j + 1)); ++k) {
+          const int t = tiles_of(own_len(p, 32 * k + lane));
+          const int s = warp_sum((t + own_tiles - 1) / own_tiles) * p.Hkv;
+          if (k % 32 == lane) own_upto[j] = s;
+        }
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+        if (32 * j < blocks) {
+          own_upto[j] = own_units + warp_incl_sum(own_upto[j]);
+          own_units = __shfl_sync(0xffffffffu, own_upto[j], 31);
+        }
+    }
+  }
+
+  // The group and KV head ... of prefix unit u, or the sequence of an own one.
+  struct Where {
+    PxUnit unit;
+    const int32_t* table;   // the table row of its keys
+    int len;                // rows that the table row lists
+    int t0;                 // first key tile
+    int kv;                 // KV head
+    int q0;                 // first sequence
+  };
+  __device__ Where find(const PrefixParams& p, int u) const {
+    const int lane = threadIdx.x & 31;
+    Where w;
+    w.unit.own = u >= prefix_units;
+    if (!w.unit.own) {
+      int g = 0, a = 0, e = 0, len_g = 0, t = 0, s = 1, q = 1, pr = 0, last = 0;
+      bool found = false;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        if (32 * j < p.P && !found) {
+          const unsigned hit = __ballot_sync(0xffffffffu, u < upto[j]);
+          if (hit) {
+            const int src = __ffs(hit) - 1;
+            found = true;
+            g = 32 * j + src;
+            a = __shfl_sync(0xffffffffu, begin[j], src);
+            e = __shfl_sync(0xffffffffu, end[j], src);
+            len_g = __shfl_sync(0xffffffffu, len[j], src);
+            t = __shfl_sync(0xffffffffu, tiles[j], src);
+            s = __shfl_sync(0xffffffffu, splits[j], src);
+            q = __shfl_sync(0xffffffffu, nq[j], src);
+            pr = __shfl_sync(0xffffffffu, pair[j], src);
+            last = __shfl_sync(0xffffffffu, upto[j], src);
+          }
+        }
+      }
+      const int local = u - (last - q * s * p.Hkv);
+      const int i = local % q, split = local / q % s;
+      w.kv = local / q / s;
+      w.t0 = static_cast<int>(static_cast<long long>(split) * t / s);
+      const int t1 = static_cast<int>(static_cast<long long>(split + 1) * t / s);
+      w.q0 = a + i * (pr ? 2 : 1) * p.TB;
+      w.unit.rows[0] = min(p.TB, e - w.q0) * p.G;
+      w.unit.rows[1] = pr ? max(0, min(p.TB, e - w.q0 - p.TB)) * p.G : 0;
+      w.unit.pair = w.unit.rows[1] > 0;
+      w.unit.tiles = t1 - w.t0;
+      w.unit.last_valid = t1 == t ? len_g - (t - 1) * Shape::KEYS : Shape::KEYS;
+      w.unit.slot = u;
+      w.table = p.prefix_table + static_cast<size_t>(g) * p.max_pblocks;
+      w.len = len_g;
+      return w;
+    }
+    const int v = u - prefix_units;
+    int block = 0, before = 0;
+    bool found = false;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      if (!found) {
+        const unsigned hit = __ballot_sync(0xffffffffu, v < own_upto[j]);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          found = true;
+          block = 32 * j + src;
+          before = src > 0 ? __shfl_sync(0xffffffffu, own_upto[j], src > 0 ? src - 1 : 0)
+                           : before;
+        } else {
+          before = __shfl_sync(0xffffffffu, own_upto[j], 31);
+        }
+      }
+    }
+    const int my_len = own_len(p, 32 * block + lane);
+    const int my_splits = (tiles_of(my_len) + own_tiles - 1) / own_tiles;
+    const int incl = warp_incl_sum(my_splits * p.Hkv);
+    const unsigned hit = __ballot_sync(0xffffffffu, v - before < incl);
+    const int src = hit ? __ffs(hit) - 1 : 31;
+    const int s = max(1, __shfl_sync(0xffffffffu, my_splits, src));
+    const int len_b = __shfl_sync(0xffffffffu, my_len, src);
+    const int local = v - before - (__shfl_sync(0xffffffffu, incl, src) - s * p.Hkv);
+    const int t = tiles_of(len_b), split = local % s;
+    w.kv = local / s;
+    w.t0 = static_cast<int>(static_cast<long long>(split) * t / s);
+    const int t1 = static_cast<int>(static_cast<long long>(split + 1) * t / s);
+    w.q0 = 32 * block + src;
+    w.unit.rows[0] = p.G;
+    w.unit.rows[1] = 0;
+    w.unit.pair = 0;
+    w.unit.tiles = t1 - w.t0;
+    w.unit.last_valid = t1 == t ? len_b - (t - 1) * Shape::KEYS : Shape::KEYS;
+    w.unit.slot = v;
+    w.table = p.block_table + static_cast<size_t>(w.q0) * p.max_blocks;
+    w.len = len_b;
+    return w;
+  }
+
+  // For the combine kernel (one warp of one CTA).
+  __device__ void write(const PrefixParams& p) const {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) p.head->own_tiles = own_tiles;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (32 * j + lane < p.P)
+        p.head->group[32 * j + lane] = {begin[j], end[j], splits[j], nq[j], pair[j],
+                                        upto[j] - nq[j] * splits[j] * p.Hkv};
+    int base = 0;
+    if (p.max_blocks > 0)
+      for (int k = 0; 32 * k < p.B; ++k) {
+        const int n = (tiles_of(own_len(p, 32 * k + lane)) + own_tiles - 1) / own_tiles * p.Hkv;
+        const int incl = warp_incl_sum(n);
+        if (32 * k + lane < p.B) p.head->own_base[32 * k + lane] = base + incl - n;
+        base += __shfl_sync(0xffffffffu, incl, 31);
+      }
+  }
+};
+
 template <typename Tag, int D>
-__global__ void __launch_bounds__(128) gqa_prefix_simple_kernel(const PrefixParams p) {
-  constexpr int E = D / 32;
-  __shared__ float s_m[4], s_l[4], s_o[4][D];
-  const int b = blockIdx.x / p.Hq, h = blockIdx.x % p.Hq, kv = h / p.G;
+__global__ void __launch_bounds__(kPxThreads, 1)
+    gqa_prefix_kernel(const __grid_constant__ PrefixParams p) {
+  using Shape = PxShape<D>;
+  constexpr int NS = Shape::NS, KEYS = Shape::KEYS, STAGES = Shape::STAGES, PARTS = Shape::PARTS;
+  // fp16 weights are scaled by 2^6 (at most 2^14 with the growth allowance), so
+  // that small ones keep their bits; the sum carries the same factor.
+  constexpr float kOff = std::is_same<Tag, Fp16Tag>::value ? 6.0f : 0.0f;
+  extern __shared__ __align__(1024) uint8_t px_smem[];
+  uint8_t* smem = px_smem;
+  const uint32_t base_s = smem_addr(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Shape::TILES_BYTES);
+  const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * kPxMaxStages;
+  const uint32_t qfull0 = empty0 + 8 * kPxMaxStages, qempty0 = qfull0 + 16;
+  const uint32_t sfull0 = qempty0 + 16, pfull0 = sfull0 + 16;   // a stream's, or an S buffer's
+  const uint32_t ofull0 = pfull0 + 16, ofree = ofull0 + 16, pvdone = ofree + 8;
+  const uint32_t meet = pvdone + 8, drain = meet + 8;
+  const uint32_t ufull0 = drain + 8, uempty0 = ufull0 + 8 * kPxSegs;
+  constexpr int kBars = 2 * kPxMaxStages + 15 + 2 * kPxSegs;
+  PxUnit* units = reinterpret_cast<PxUnit*>(bars + kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(units + kPxSegs);
+  float2* ml = reinterpret_cast<float2*>(smem + Shape::TILES_BYTES + 1024);   // [2][128]
+  static_assert(8 * kBars + sizeof(PxUnit) * kPxSegs + 4 <= 1024, "misc shared memory");
+
+  if (warp == kPxMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(tmem_slot)),
+                 "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(full0 + 8 * i, 1);
+      mbar_init(empty0 + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(qfull0 + 8 * i, 1);
+      mbar_init(qempty0 + 8 * i, 1);
+      mbar_init(sfull0 + 8 * i, 1);
+      mbar_init(pfull0 + 8 * i, 4);
+      mbar_init(ofull0 + 8 * i, 1);
+    }
+    mbar_init(ofree, 8);
+    mbar_init(pvdone, 1);
+    mbar_init(meet, 8);
+    mbar_init(drain, 1);
+    for (int i = 0; i < kPxSegs; ++i) {
+      mbar_init(ufull0 + 8 * i, 1);
+      mbar_init(uempty0 + 8 * i, 9);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kPxLoadWarp && lane < 4) {
+    const CUtensorMap* m = lane == 0 ? &p.k_map : lane == 1 ? &p.v_map : lane == 2 ? &p.q_tile_map
+                                                                                   : &p.q_one_map;
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const uint32_t qbuf_s = base_s, ring_s = base_s + Shape::QBUF * Shape::QBYTES;
   grid_dependency_wait();
   grid_launch_dependents();
-  auto load = [&](const void* base, size_t at, float (&x)[E]) {
-    const uint16_t* src = static_cast<const uint16_t*>(base) + at + E * lane;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const uint16_t v = src[e];
-      if constexpr (std::is_same<Tag, Bf16Tag>::value) x[e] = __uint_as_float(uint32_t(v) << 16);
-      else x[e] = __half2float(__ushort_as_half(v));
+  const bool aligned = (base_s & 1023u) == 0;   // the tiles need it; dynamic memory starts so
+  if (!aligned && threadIdx.x == 0) atomicOr(&p.head->status, kErrPxLoad);
+
+  if (aligned && warp == kPxLoadWarp) {
+    // ------------------------------------------------------- plan and loads
+    PxPlan<D> plan;
+    plan.make(p);
+    const int total = plan.prefix_units + plan.own_units;
+    uint64_t keep, once = evict_first_policy();
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+    const int nch = KEYS / p.R;              // boxes of one 64-column part of a tile
+    const int chunk = lane % nch, part = lane / nch;
+    const bool boxed = part < PARTS;
+    const int oob = p.num_blocks * p.bs;
+    unsigned pos = 0, fills = 0, unit_no = 0;
+    bool ok = true;
+    int u = blockIdx.x;
+    while (true) {
+      int next = 0;
+      typename PxPlan<D>::Where w;
+      w.unit.tiles = 0;
+      if (u < total) {
+        w = plan.find(p, u);
+        if (lane == 0) next = atomicAdd(&p.head->next, 1) + gridDim.x;
+      }
+      const int seg = unit_no % kPxSegs;
+      if (!(ok = warp_poll(uempty0 + 8 * seg, ((unit_no / kPxSegs) & 1) ^ 1, p.timeout_ns))) break;
+      if (lane == 0) {
+        units[seg] = w.unit;
+        mbar_arrive(ufull0 + 8 * seg);
+      }
+      __syncwarp();
+      ++unit_no;
+      if (w.unit.tiles == 0) break;
+      const int n = w.unit.tiles;
+      for (int i = 0; i <= w.unit.pair && ok; ++i) {
+        const int buf = fills % Shape::QBUF;
+        ok = warp_poll(qempty0 + 8 * buf, ((fills / Shape::QBUF) & 1) ^ 1, p.timeout_ns);
+        if (!ok) break;
+        const int rows = w.unit.own ? p.G : p.TB * p.G;
+        if (lane == 0) mbar_arrive_expect_tx(qfull0 + 8 * buf, rows * 128 * PARTS);
+        __syncwarp();
+        if (lane < PARTS)
+          tma_load_4d(qbuf_s + buf * Shape::QBYTES + lane * 128 * 128,
+                      w.unit.own ? &p.q_one_map : &p.q_tile_map, 64 * lane, 0, w.kv,
+                      w.q0 + i * p.TB, qfull0 + 8 * buf, keep);
+        ++fills;
+      }
+      if (!ok) break;
+      // The row of tile i's box of this lane; rows past the length read zeros.
+      auto row_of = [&](int i) {
+        const int c = (w.t0 + i) * KEYS + chunk * p.R;
+        if (!boxed || i >= n || c >= w.len) return oob;
+        const int col = c / p.bs, block = w.table[col];
+        return block >= 0 && block < p.num_blocks ? block * p.bs + (c - col * p.bs) : oob;
+      };
+      const uint64_t policy = w.unit.own ? once : keep;
+      auto load = [&](const CUtensorMap* map, int row) {
+        const unsigned stage = pos % STAGES;
+        if (!warp_poll(empty0 + 8 * stage, ((pos / STAGES) & 1) ^ 1, p.timeout_ns)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * stage, Shape::STAGE);
+        __syncwarp();
+        if (boxed)
+          tma_load_3d(ring_s + stage * Shape::STAGE + part * KEYS * 128 + chunk * p.R * 128, map,
+                      64 * part, w.kv, row, full0 + 8 * stage, policy);
+        ++pos;
+        return true;
+      };
+      int r0 = row_of(0), r1 = row_of(1), r2 = row_of(2);
+      ok = load(&p.k_map, r0) && (n == 1 || load(&p.k_map, r1));
+      for (int i = 0; i < n && ok; ++i) {
+        const int r3 = row_of(i + 3);
+        ok = load(&p.v_map, r0) && (i + 2 >= n || load(&p.k_map, r2));
+        r0 = r1;
+        r1 = r2;
+        r2 = r3;
+      }
+      if (!ok) break;
+      u = __shfl_sync(0xffffffffu, next, 0);
     }
-  };
-  int group = -1, first = 0;
-  for (int g = 0; g < p.P; ++g) {
-    const int a = max(first, p.group_start ? min(max(p.group_start[g], 0), p.B) : 0);
-    const int e = max(a, p.group_start ? min(max(p.group_start[g + 1], 0), p.B) : p.B);
-    if (b >= a && b < e) group = g;
-    first = a;
+    if (!ok) {
+      if (lane == 0) atomicOr(&p.head->status, kErrPxLoad);
+      for (unsigned i = pos > STAGES ? pos - STAGES : 0; i < pos; ++i)
+        mbar_wait(full0 + 8 * (i % STAGES), (i / STAGES) & 1, p.timeout_ns);
+      for (unsigned i = fills > Shape::QBUF ? fills - Shape::QBUF : 0; i < fills; ++i)
+        mbar_wait(qfull0 + 8 * (i % Shape::QBUF), (i / Shape::QBUF) & 1, p.timeout_ns);
+    }
+  } else if (aligned && warp == kPxMmaWarp) {
+    // ------------------------------------------------------------ MMA issue
+    if (lane == 0) {
+      constexpr uint32_t qk_idesc = px_idesc<Tag>(KEYS, false), pv_idesc = px_idesc<Tag>(D, true);
+      unsigned base = 0, fills = 0, done[2] = {0, 0};   // stages, fills, tiles of each stream
+      bool ok = true;
+      for (unsigned unit_no = 0; ok; ++unit_no) {
+        const int seg = unit_no % kPxSegs;
+        if (!(ok = mbar_poll(ufull0 + 8 * seg, (unit_no / kPxSegs) & 1, p.timeout_ns))) break;
+        const int n = units[seg].tiles, pair = units[seg].pair;
+        mbar_arrive(uempty0 + 8 * seg);
+        if (n == 0) break;
+        const int cnt[2] = {NS == 1 || pair ? n : (n + 1) / 2, NS == 1 ? 0 : pair ? n : n / 2};
+        auto tile_of = [&](int w, int j) { return NS == 1 || pair ? j : 2 * j + w; };
+        auto s_of = [&](int w, unsigned tile_no) {
+          return tmem + Shape::S_COL * (NS == 2 ? w : tile_no & 1);
+        };
+        auto qk = [&](int w, int j) {
+          const int i = tile_of(w, j);
+          const unsigned at = base + k_pos(i), stage = at % STAGES;
+          const unsigned fill = fills + (pair ? w : 0), buf = fill % Shape::QBUF;
+          if (j == 0) ok = ok && mbar_poll(qfull0 + 8 * buf, (fill / Shape::QBUF) & 1, p.timeout_ns);
+          ok = ok && mbar_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns);
+          if (!ok) return;
+          tc_fence_after();
+          const unsigned no = done[w] + j;
+          const uint64_t a = smem_desc(qbuf_s + buf * Shape::QBYTES, 16, 1024, 2);
+          const uint64_t b = smem_desc(ring_s + stage * Shape::STAGE, 16, 1024, 2);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_f16(s_of(w, no), a + (uint64_t)((kk / 4 * 128 * 128 + kk % 4 * 32) >> 4),
+                    b + (uint64_t)((kk / 4 * KEYS * 128 + kk % 4 * 32) >> 4), qk_idesc, kk > 0);
+          if (!pair || w == 1) mma_commit(empty0 + 8 * stage);
+          if (pair ? j == n - 1 : i == n - 1) mma_commit(qempty0 + 8 * buf);
+          mma_commit(sfull0 + 8 * (NS == 2 ? w : no & 1));
+        };
+        auto pv = [&](int w, int j) {
+          const int i = tile_of(w, j);
+          const unsigned at = base + v_pos(i, n), stage = at % STAGES;
+          const unsigned no = done[w] + j;
+          ok = ok && mbar_poll(pfull0 + 8 * (NS == 2 ? w : no & 1), (NS == 2 ? no : no >> 1) & 1,
+                               p.timeout_ns);
+          if (j == 0 && unit_no > 0) ok = ok && mbar_poll(ofree, (unit_no - 1) & 1, p.timeout_ns);
+          ok = ok && mbar_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns);
+          if (!ok) return;
+          tc_fence_after();
+          const uint64_t b = smem_desc(ring_s + stage * Shape::STAGE, KEYS * 128, 1024, 2);
+#pragma unroll
+          for (int kk = 0; kk < KEYS / 16; ++kk)
+            mma_f16_ta(tmem + Shape::O_COL0 + w * D, s_of(w, no) + 8 * kk,
+                       b + (uint64_t)(kk * (2048 >> 4)), pv_idesc, j > 0 || kk > 0);
+          if (!pair || w == 1) mma_commit(empty0 + 8 * stage);
+          if (NS == 1) mma_commit(pvdone);
+          if (j == cnt[w] - 1) mma_commit(ofull0 + 8 * w);
+        };
+        if constexpr (NS == 1) {
+          qk(0, 0);
+          for (int j = 0; j < n && ok; ++j) {
+            if (j + 1 < n) qk(0, j + 1);
+            pv(0, j);
+          }
+        } else {
+          qk(0, 0);
+          if (cnt[1] > 0) qk(1, 0);
+          for (int j = 0; j < cnt[0] && ok; ++j)
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+              if (j < cnt[w]) {
+                pv(w, j);
+                if (j + 1 < cnt[w]) qk(w, j + 1);
+              }
+        }
+        base += 2 * n;
+        fills += 1 + pair;
+        done[0] += cnt[0];
+        done[1] += cnt[1];
+      }
+      if (!ok) {
+        atomicOr(&p.head->status, kErrPxMma);
+        mma_commit(drain);
+        mbar_wait(drain, 0, p.timeout_ns);
+      }
+    }
+    __syncwarp();
+  } else if (aligned) {
+    // ------------------------------------------------- softmax, units' ends
+    const int w = warp >> 2;                  // stream
+    const int r = threadIdx.x & 127;          // row of the query tile, tensor-memory lane
+    const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    if (blockIdx.x == 0 && warp == 4) {
+      PxPlan<D> plan;
+      plan.make(p);
+      plan.write(p);
+    }
+    unsigned base = 0, done = 0, ends[2] = {0, 0}, meets = 0;
+    bool ok = true;
+    for (unsigned unit_no = 0; ok; ++unit_no) {
+      const int seg = unit_no % kPxSegs;
+      if (!(ok = warp_poll(ufull0 + 8 * seg, (unit_no / kPxSegs) & 1, p.timeout_ns))) break;
+      const PxUnit un = units[seg];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(uempty0 + 8 * seg);
+      const int n = un.tiles;
+      if (n == 0) break;
+      const int cnt[2] = {NS == 1 || un.pair ? n : (n + 1) / 2,
+                          NS == 1 ? 0 : un.pair ? n : n / 2};
+      const int mine = cnt[w];
+      const int rows = un.pair && w == 1 ? un.rows[1] : un.rows[0];
+      const bool active = 32 * (warp & 3) < rows;   // warps without rows only keep step
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < mine; ++j) {
+        const unsigned no = done + j;
+        const int sb = NS == 2 ? w : no & 1;
+        if (!(ok = warp_poll(sfull0 + 8 * sb, (NS == 2 ? no : no >> 1) & 1, p.timeout_ns))) break;
+        tc_fence_after();
+        const int i = NS == 1 || un.pair ? j : 2 * j + w;
+        const int valid = i == n - 1 ? un.last_valid : KEYS;
+        if (valid < KEYS && (w == 0 || !un.pair)) {
+          // V rows past the length may hold NaN: zeroed before the product.
+          const unsigned at = base + v_pos(i, n), stage = at % STAGES;
+          if (!(ok = warp_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns))) break;
+          uint8_t* v = smem + Shape::QBUF * Shape::QBYTES + stage * Shape::STAGE;
+          const int line = (KEYS - valid) * 8;   // 16-byte pieces of one part
+          for (int t = r; t < line * PARTS; t += 128) {
+            const int part = t / line, c = t - part * line;
+            *reinterpret_cast<uint4*>(v + part * KEYS * 128 + valid * 128 + c * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        if (active) {
+          const uint32_t s_addr = tmem + lane_addr + Shape::S_COL * sb;
+          float s[KEYS];
+#pragma unroll
+          for (int c = 0; c < KEYS; c += 32) tmem_ld32(s_addr + c, s + c);
+          tmem_wait_ld();
+          hold<KEYS>(s);
+          if (p.negate) {
+#pragma unroll
+            for (int c = 0; c < KEYS; ++c) s[c] = -s[c];
+          }
+          if (valid < KEYS) {
+#pragma unroll
+            for (int c = 0; c < KEYS; ++c) s[c] = c < valid ? s[c] : -INFINITY;
+          }
+          float mx[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mx[c] = s[c];
+#pragma unroll
+          for (int c = 4; c < KEYS; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
+          if (j == 0) {
+            m = top == -INFINITY ? -1e30f : top;   // nothing finite yet: weights of 0
+          } else if (__any_sync(0xffffffffu, top > m + kPxGrow)) {
+            // The previous tiles' products are done: S of this tile was
+            // multiplied after them, or (one stream) the wait below.
+            if (NS == 1) {
+              if (!(ok = warp_poll(pvdone, (no - 1) & 1, p.timeout_ns))) break;
+              tc_fence_after();
+            }
+            const float now = fmaxf(m, top), a = ex2(m - now);
+            m = now;
+            l *= a;
+            const uint32_t o_addr = tmem + lane_addr + Shape::O_COL0 + w * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_ld32(o_addr + c, o);
+              tmem_wait_ld();
+              hold<32>(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= a;
+              tmem_st32(o_addr + c, reinterpret_cast<const uint32_t*>(o));
+            }
+          }
+          const float shift = kOff - m;
+          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int c0 = 0; c0 < KEYS; c0 += 64) {
+            uint32_t w16[32];
+#pragma unroll
+            for (int c = 0; c < 64; c += 2) {
+              const float x = ex2(fmaf(s[c0 + c], p.qscale, shift));
+              const float y = ex2(fmaf(s[c0 + c + 1], p.qscale, shift));
+              sum[c & 2] += x;
+              sum[(c & 2) + 1] += y;
+              w16[c / 2] = pack2<Tag>(x, y);
+            }
+            tmem_st32(s_addr + c0 / 2, w16);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pfull0 + 8 * sb);
+      }
+      if (!ok) break;
+      done += mine;
+      // The unit's end: O, m and l to its slot.
+      const bool both = NS == 2 && !un.pair;        // one query tile, merged here
+      for (int x = 0; x < 2 && ok; ++x)
+        if (cnt[x] > 0 && (both || NS == 1 || x == w))
+          ok = warp_poll(ofull0 + 8 * x, ends[x] & 1, p.timeout_ns);
+      if (!ok) break;
+      for (int x = 0; x < 2; ++x) ends[x] += cnt[x] > 0;
+      tc_fence_after();
+      float a0 = 1.0f, a1 = 0.0f;
+      if (both) {
+        if (mine > 0) ml[128 * w + r] = make_float2(m, l);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(meet);
+        if (!(ok = warp_poll(meet, meets & 1, p.timeout_ns))) break;
+        ++meets;
+        if (cnt[1] > 0) {
+          const float2 x = ml[r], y = ml[128 + r];
+          const float top = fmaxf(x.x, y.x);
+          a0 = ex2(x.x - top);
+          a1 = ex2(y.x - top);
+          m = top;
+          l = x.y * a0 + y.y * a1;
+        }
+      }
+      if (active) {
+        const int stride = un.own ? p.G : 128;
+        const int sub = un.pair ? w : 0;
+        float4* dst;
+        float2* dst_ml;
+        if (un.own) {
+          dst = reinterpret_cast<float4*>(p.own_o) + static_cast<size_t>(un.slot) * (D / 4) * p.G;
+          dst_ml = p.own_ml + static_cast<size_t>(un.slot) * p.G;
+        } else {
+          const size_t tile = static_cast<size_t>(un.slot) * NS + sub;
+          dst = reinterpret_cast<float4*>(p.prefix_o) + tile * (D / 4) * 128;
+          dst_ml = p.prefix_ml + tile * 128;
+        }
+        // A pair's streams write their own tiles; else the warpgroups share
+        // the columns of the one tile.
+        const int c_begin = un.pair ? 0 : w * (D / 2), c_end = un.pair ? D : c_begin + D / 2;
+        const uint32_t o_addr = tmem + lane_addr + Shape::O_COL0 + (un.pair ? w * D : 0);
+#pragma unroll 1
+        for (int c = c_begin; c < c_end; c += 32) {
+          float o[32];
+          tmem_ld32(o_addr + c, o);
+          if (both && cnt[1] > 0) {
+            float o1[32];
+            tmem_ld32(o_addr + D + c, o1);
+            tmem_wait_ld();
+            hold<32>(o);
+            hold<32>(o1);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = o[e] * a0 + o1[e] * a1;
+          } else {
+            tmem_wait_ld();
+            hold<32>(o);
+          }
+          if (r < rows) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              __stcg(dst + static_cast<size_t>((c + e) / 4) * stride + r,
+                     make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+          }
+        }
+        if (r < rows && (un.pair || w == 0)) __stcg(dst_ml + r, make_float2(m, l));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(ofree);
+      base += 2 * n;
+    }
+    if (!ok && lane == 0) atomicOr(&p.head->status, kErrPxSoftmax);
   }
-  const int plen = group < 0 ? 0 : min(max(p.prefix_lens[group], 0), p.max_pblocks * p.bs);
-  const int cap = p.max_blocks * p.bs;
-  const int len = p.seq_lens ? min(max(p.seq_lens[b], 0), cap) : cap;
-  float q[E], o[E], m = -INFINITY, l = 0.0f;
-  load(p.q, (static_cast<size_t>(b) * p.Hq + h) * D, q);
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.0f;
-  for (int c = warp; c < plen + len; c += 4) {
-    const int row = c < plen ? c : c - plen;
-    const int block = c < plen ? p.prefix_table[static_cast<size_t>(group) * p.max_pblocks + row / p.bs]
-                               : p.block_table[static_cast<size_t>(b) * p.max_blocks + row / p.bs];
-    const bool in = block >= 0 && block < p.num_blocks;
-    const size_t at = ((static_cast<size_t>(in ? block : 0) * p.bs + row % p.bs) * p.Hkv + kv) * D;
-    float k[E], v[E], s = 0.0f;
-    load(p.k_pool, at, k);
-    load(p.v_pool, at, v);
-#pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], in ? k[e] : 0.0f, s);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.qscale;
-    const float top = fmaxf(m, s), a = m == top ? 1.0f : exp2f(m - top), w = exp2f(s - top);
-    l = l * a + w;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * a + w * (in ? v[e] : 0.0f);
-    m = top;
-  }
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][E * lane + e] = o[e];
+  __syncwarp();
+  tc_fence_before();
   __syncthreads();
-  for (int d = threadIdx.x; d < D; d += 128) {
-    const float top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-    float sum = 0.0f, x = 0.0f;
-    for (int w = 0; w < 4; ++w) {
-      const float a = s_m[w] == -INFINITY ? 0.0f : exp2f(s_m[w] - top);
-      sum += a * s_l[w];
-      x += a == 0.0f ? 0.0f : a * s_o[w][d];
+  if (warp == kPxMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512)
+                 : "memory");
+  }
+}
+
+// out row = sum over its slots of 2^(m_s - M) O_s / sum of 2^(m_s - M) l_s, the
+// prefix's splits first, then the sequence's own. One CTA a (sequence, KV
+// head), a thread a row and 4 columns.
+constexpr int kPxCombineThreads = 128;
+
+template <typename Tag, int D>
+__global__ void __launch_bounds__(kPxCombineThreads)
+    gqa_prefix_combine_kernel(const __grid_constant__ PrefixParams p) {
+  using Shape = PxShape<D>;
+  const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, lane = threadIdx.x & 31;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.head->next = 0;   // for the next call
+  int group = -1;
+  for (int j = 0; j < p.P; j += 32) {
+    bool in = false;
+    if (j + lane < p.P) {
+      const PxGroup& g = p.head->group[j + lane];
+      in = b >= g.begin && b < g.end && g.splits > 0;
     }
-    const float y = sum == 0.0f ? 0.0f : x / sum;
-    static_cast<uint16_t*>(p.out)[(static_cast<size_t>(b) * p.Hq + h) * D + d] =
-        static_cast<uint16_t>(pack2<Tag>(y, 0.0f) & 0xffffu);
+    const unsigned hit = __ballot_sync(0xffffffffu, in);
+    if (hit) group = j + __ffs(hit) - 1;
+  }
+  int n0 = 0, row0 = 0;
+  size_t tile0 = 0, step0 = 0;     // prefix: first tile of slots, tiles between splits
+  if (group >= 0) {
+    const PxGroup g = p.head->group[group];
+    const int t = (b - g.begin) / p.TB;
+    const int i = g.pair ? t / 2 : t;
+    n0 = g.splits;
+    row0 = (b - g.begin - t * p.TB) * p.G;
+    tile0 = (static_cast<size_t>(g.base) + static_cast<size_t>(h) * g.splits * g.nq + i) * Shape::NS +
+            (g.pair ? t & 1 : 0);
+    step0 = static_cast<size_t>(g.nq) * Shape::NS;
+  }
+  int n1 = 0;
+  size_t slot1 = 0;
+  if (p.max_blocks > 0) {
+    const int tiles = PxPlan<D>::tiles_of(PxPlan<D>::own_len(p, b));
+    n1 = (tiles + p.head->own_tiles - 1) / p.head->own_tiles;
+    slot1 = static_cast<size_t>(p.head->own_base[b]) + static_cast<size_t>(h) * n1;
+  }
+  for (int x = threadIdx.x; x < p.G * (D / 4); x += kPxCombineThreads) {
+    const int g = x % p.G, c = x / p.G;
+    const float2* ml0 = p.prefix_ml + tile0 * 128 + row0 + g;
+    const float2* ml1 = p.own_ml + slot1 * p.G + g;
+    const float4* o0 = reinterpret_cast<const float4*>(p.prefix_o) +
+                       (tile0 * (D / 4) + c) * 128 + row0 + g;
+    const float4* o1 = reinterpret_cast<const float4*>(p.own_o) + (slot1 * (D / 4) + c) * p.G + g;
+    float top = -INFINITY;
+    for (int s = 0; s < n0; ++s) top = fmaxf(top, __ldcg(ml0 + s * step0 * 128).x);
+    for (int s = 0; s < n1; ++s) top = fmaxf(top, __ldcg(ml1 + static_cast<size_t>(s) * p.G).x);
+    float sum = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](const float2 ml, const float4 o) {
+      const float a = ex2(ml.x - top);
+      sum = fmaf(a, ml.y, sum);
+      acc.x = fmaf(a, o.x, acc.x);
+      acc.y = fmaf(a, o.y, acc.y);
+      acc.z = fmaf(a, o.z, acc.z);
+      acc.w = fmaf(a, o.w, acc.w);
+    };
+#pragma unroll 4
+    for (int s = 0; s < n0; ++s)
+      add(__ldcg(ml0 + s * step0 * 128), __ldcg(o0 + s * step0 * (D / 4) * 128));
+#pragma unroll 4
+    for (int s = 0; s < n1; ++s)
+      add(__ldcg(ml1 + static_cast<size_t>(s) * p.G),
+          __ldcg(o1 + static_cast<size_t>(s) * (D / 4) * p.G));
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const uint2 y = make_uint2(pack2<Tag>(acc.x * inv, acc.y * inv), pack2<Tag>(acc.z * inv, acc.w * inv));
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
+                              (static_cast<size_t>(b) * p.Hq + h * p.G + g) * D + 4 * c) = y;
   }
 }
 
