@@ -249,7 +249,7 @@ extern "C" int gqa_prefix_attn_decode(
   const size_t q_tiles = static_cast<size_t>((B + p.TB - 1) / p.TB + std::min(P, B)) * Hkv;
   const size_t prefix_slots = P ? q_tiles + 2 * static_cast<size_t>(sms) : 0;
   const size_t own_slots = max_blocks ? static_cast<size_t>(B) * Hkv + 4 * static_cast<size_t>(sms) : 0;
-  if (prefix_slots + own_slots > 0x3fffffffu)
+  if (prefix_slots + own_slots > 0x3ffffffu)
     return pfail(GQA_AV_ERR_UNSUPPORTED, "too many units of work");
   p.prefix_slots = static_cast<int>(prefix_slots);
   const size_t at_po = up256(sizeof(PxHeader));
@@ -273,7 +273,8 @@ extern "C" int gqa_prefix_attn_decode(
   e = launch_pdl(k, sms, kPxThreads, smem_bytes(D), stream, args);
   if (e != cudaSuccess) return pfail_cuda(e, "attention kernel launch");
   k = reinterpret_cast<const void*>(bf ? pick_combine<Bf16Tag>(D) : pick_combine<Fp16Tag>(D));
-  e = launch_pdl(k, B * Hkv, kPxCombineThreads, 0, stream, args);
+  const int parts = (p.G * (D / 4) + kPxCombineThreads - 1) / kPxCombineThreads;
+  e = launch_pdl(k, B * Hkv * parts, kPxCombineThreads, 0, stream, args);
   if (e != cudaSuccess) {
     cudaMemsetAsync(&p.head->next, 0, sizeof p.head->next, stream);   // the combine's job
     return pfail_cuda(e, "combine kernel launch");

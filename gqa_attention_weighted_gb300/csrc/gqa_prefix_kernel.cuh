@@ -34,7 +34,7 @@
 //
 // Warps: 0-3 and 4-7 softmax warpgroups (and the units' ends), 8 issues the
 // MMAs from one thread, 9 makes the plan, hands out units and issues the TMA
-// loads, one box a lane. Every wait is bounded (2 s): on expiry the role sets
+// loads, one box a lane; 10 and 11 only fill their warpgroup. Every wait is bounded (2 s): on expiry the role sets
 // the status word and leaves, the others run out in turn, copies and MMAs in
 // flight are waited for and tensor memory is freed.
 #pragma once
@@ -48,7 +48,11 @@
 
 namespace gqa_av {
 
-constexpr int kPxThreads = 320;
+constexpr int kPxThreads = 384;
+// Registers a thread: 168 at launch (65536 / 384, rounded down to 8); the last
+// warpgroup gives up enough of them for the softmax warpgroups' 128 scores a
+// thread: 2 * 128 * 200 + 128 * 104 = 384 * 168.
+constexpr int kPxSoftmaxRegs = 200, kPxAuxRegs = 104;
 constexpr int kPxMmaWarp = 8, kPxLoadWarp = 9;
 constexpr int kPxMaxGroups = 128;
 constexpr int kPxMaxB = 4096;
@@ -163,6 +167,21 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// Two fp32 multiply-adds and additions in one instruction each.
+__device__ __forceinline__ void fma2(float a, float b, float x, float y, float c, float d, float& r,
+                                     float& t) {
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\t"
+      "mov.b64 w, {%6, %7};\n\tfma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "=f"(r), "=f"(t)
+      : "f"(a), "f"(b), "f"(x), "f"(y), "f"(c), "f"(d));
+}
+__device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %3};\n\t"
+      "add.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(a), "+f"(b)
+      : "f"(x), "f"(y));
+}
+
 // A wait by a whole warp; the lanes agree on whether it ran out, so that they
 // leave together.
 __device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity, long long timeout_ns) {
@@ -191,11 +210,6 @@ struct PxUnit {
 __device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int v_pos(int i, int n) { return min(2 * i + 2, 2 * n - 1); }
 
-__device__ __forceinline__ int warp_sum(int x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
 __device__ __forceinline__ int warp_incl_sum(int x) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -206,8 +220,16 @@ __device__ __forceinline__ int warp_incl_sum(int x) {
   return x;
 }
 
+__device__ __forceinline__ int warp_max(int x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
 // The plan, made by a whole warp from the lengths: lane l holds groups 32 j + l
-// and the unit sums of the blocks 32 j + l of 32 sequences.
+// and the unit sums of the blocks 32 j + l of 32 sequences. It stands at the
+// head of every call's critical path, so all lengths are loaded at once and
+// 64-bit and double arithmetic is kept out of it.
 template <int D>
 struct PxPlan {
   using Shape = PxShape<D>;
@@ -224,39 +246,49 @@ struct PxPlan {
     return len / Shape::KEYS + (len % Shape::KEYS != 0);
   }
 
-  __device__ void make(const PrefixParams& p) {
+  __device__ __forceinline__ void make(const PrefixParams& p) {
     const int lane = threadIdx.x & 31;
     const int n = gridDim.x;
-    // Own tiles of the batch, and how many of them a unit takes: about four
-    // units a CTA, so that the last ones to end are short.
-    const int blocks = (p.B + 31) / 32;
-    long long own = 0;
-    int seqs = 0;
-    if (p.max_blocks > 0)
-      for (int k = 0; k < blocks; ++k) {
-        const int t = tiles_of(own_len(p, 32 * k + lane));
-        own += t;
-        seqs += t > 0;
-      }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) own += __shfl_xor_sync(0xffffffffu, own, o);
-    own *= p.Hkv;
-    own_tiles = static_cast<int>(max(1LL, (own + 4LL * n - 1) / (4LL * n)));
-    // Groups.
-    int carry = 0, carry_n = 0;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      begin[j] = end[j] = len[j] = tiles[j] = splits[j] = nq[j] = pair[j] = 0;
-      upto[j] = 0;
+      begin[j] = end[j] = len[j] = tiles[j] = splits[j] = pair[j] = upto[j] = own_upto[j] = 0;
+      nq[j] = 1;
+      const int g = 32 * j + lane;
+      if (32 * j < p.P && g < p.P) {
+        begin[j] = p.group_start ? min(max(p.group_start[g], 0), p.B) : 0;
+        end[j] = p.group_start ? min(max(p.group_start[g + 1], 0), p.B) : p.B;
+        len[j] = min(max(p.prefix_lens[g], 0), p.max_pblocks * p.bs);
+      }
+    }
+    // Own tiles of the batch, and how many of them a unit takes: about four
+    // units a CTA, so that the last ones to end are short. A lane's tiles may
+    // be 2^24 a sequence: summed over the warp as two halves.
+    const int blocks = p.max_blocks > 0 ? (p.B + 31) / 32 : 0;
+    unsigned low = 0, high = 0;
+#pragma unroll 8
+    for (int k = 0; k < blocks; ++k) {
+      const unsigned t = tiles_of(own_len(p, 32 * k + lane));
+      low += t & 4095u;
+      high += t >> 12;
+    }
+    low = __reduce_add_sync(0xffffffffu, low);
+    high = __reduce_add_sync(0xffffffffu, high);
+    const unsigned long long own =
+        ((static_cast<unsigned long long>(high) << 12) + low) * static_cast<unsigned>(p.Hkv);
+    const unsigned share = 4u * n;
+    own_tiles = own < 0x40000000u
+                    ? static_cast<int>((static_cast<unsigned>(own) + share - 1) / share)
+                    : static_cast<int>((own + share - 1) / share);
+    own_tiles = max(own_tiles, 1);
+    // Groups: starts not below their predecessors, tiles, query tiles.
+    int carry = 0, longest = 0;
+    float cost[2] = {0.0f, 0.0f};   // key tiles x query tiles, single and in pairs
+    int q[J];
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      q[j] = 0;
       if (32 * j < p.P) {
-        const int g = 32 * j + lane;
-        int a = 0, e = 0;
-        if (g < p.P) {
-          a = p.group_start ? min(max(p.group_start[g], 0), p.B) : 0;
-          e = p.group_start ? min(max(p.group_start[g + 1], 0), p.B) : p.B;
-          len[j] = min(max(p.prefix_lens[g], 0), p.max_pblocks * p.bs);
-        }
-        a = max(a, carry);
+        int a = max(begin[j], carry);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const int y = __shfl_up_sync(0xffffffffu, a, o);
@@ -264,105 +296,83 @@ struct PxPlan {
         }
         carry = __shfl_sync(0xffffffffu, a, 31);
         begin[j] = a;
-        end[j] = max(a, e);
-        tiles[j] = end[j] > begin[j] && len[j] > 0 ? tiles_of(len[j]) : 0;
+        end[j] = max(a, end[j]);
+        q[j] = (end[j] - begin[j] + p.TB - 1) / p.TB;
+        tiles[j] = q[j] > 0 ? tiles_of(len[j]) : 0;
+        cost[0] += static_cast<float>(tiles[j]) * static_cast<float>(q[j]);
+        cost[1] += static_cast<float>(tiles[j]) * static_cast<float>((q[j] + 1) / 2);
+        longest = max(longest, tiles[j]);
       }
     }
-    // How to cut the prefixes: each lane costs one choice of pairs or single
-    // tiles and of the tiles a split takes (1 to 8 units a CTA), from the
-    // time that the units take if all CTAs stay busy, own units included, and
-    // from the CTA with the most prefix units.
-    const bool pairs = Shape::NS == 2 && (lane & 1);
-    double cost[2] = {0.0, 0.0};     // prefix key tiles x query tiles, single and paired
-    long long items[2] = {0, 0};
-    int longest = 0;
-    for (int g = 0; g < p.P; ++g) {
-      int t = 0, m = 0;
+    longest = p.P > 0 ? warp_max(longest) : 0;
+    prefix_units = 0;
+    if (longest > 0) {
+      // How to cut the prefixes: each lane costs one choice of pairs or single
+      // tiles and of the tiles a split takes (1 to 8 units a CTA), from the
+      // time that the units take if all CTAs stay busy, own units included,
+      // and from the CTA with the most prefix units.
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        cost[0] += __shfl_xor_sync(0xffffffffu, cost[0], o);
+        cost[1] += __shfl_xor_sync(0xffffffffu, cost[1], o);
+      }
+      const bool pairs = Shape::NS == 2 && (lane & 1);
+      const float w = (pairs ? cost[1] : cost[0]) * static_cast<float>(p.Hkv);
+      int chunk = static_cast<int>(fminf(ceilf(w / static_cast<float>(((lane >> 2) + 1) * n)),
+                                         16777216.0f)) + ((lane >> 1) & 1);
+      if (lane >= 30) chunk = longest;   // no cut: always within the slots
+      chunk = max(1, min(chunk, longest));
+      int units = 0;                     // at most 2^13 tiles of 2^24 / chunk: see below
 #pragma unroll
       for (int j = 0; j < J; ++j)
-        if (g / 32 == j) {
-          t = __shfl_sync(0xffffffffu, tiles[j], g % 32);
-          m = __shfl_sync(0xffffffffu, end[j] - begin[j], g % 32);
+        for (int g = 32 * j; g < min(p.P, 32 * (j + 1)); ++g) {
+          const int t = __shfl_sync(0xffffffffu, tiles[j], g & 31);
+          const int m = __shfl_sync(0xffffffffu, q[j], g & 31);
+          const int more = (t + chunk - 1) / chunk;
+          const int wide = pairs ? (m + 1) / 2 : m;
+          // Past the slots the choice is dropped: no need to count on.
+          units = more > p.prefix_slots ? p.prefix_slots + 1
+                                        : min(units + more * wide, p.prefix_slots + 1);
         }
-      if (t == 0) continue;
-      const int q = (m + p.TB - 1) / p.TB;
-      cost[0] += static_cast<double>(t) * q;
-      cost[1] += static_cast<double>(t) * ((q + 1) / 2);
-      items[0] += q;
-      items[1] += (q + 1) / 2;
-      longest = max(longest, t);
-    }
-    prefix_units = 0;
-    int cut = 1;
-    bool use_pairs = false;
-    if (longest > 0) {
-      const int r = (lane >> 2) + 1;
-      const double w = cost[pairs] * p.Hkv;
-      long long chunk = static_cast<long long>(ceil(w / (static_cast<double>(r) * n))) + ((lane >> 1) & 1);
-      if (lane >= 30) chunk = longest;   // no cut: always within the slots
-      chunk = max(1LL, min(chunk, static_cast<long long>(longest)));
-      long long units = 0;
-      for (int g = 0; g < p.P; ++g) {
-        int t = 0, m = 0;
-#pragma unroll
-        for (int j = 0; j < J; ++j)
-          if (g / 32 == j) {
-            t = __shfl_sync(0xffffffffu, tiles[j], g % 32);
-            m = __shfl_sync(0xffffffffu, end[j] - begin[j], g % 32);
-          }
-        const int q = (m + p.TB - 1) / p.TB;
-        units += (t + chunk - 1) / chunk * (pairs ? (q + 1) / 2 : q);
-      }
+      const bool fits = static_cast<long long>(units) * p.Hkv <= p.prefix_slots;
       units *= p.Hkv;
       const float c = pairs ? p.c_pair : p.c_tile;
       const float one = static_cast<float>(chunk) * c + p.c_unit;
-      const float all = (static_cast<float>(w) * c + static_cast<float>(units) * p.c_unit +
+      const float all = (w * c + static_cast<float>(units) * p.c_unit +
                          static_cast<float>(own) * p.c_own) / static_cast<float>(n);
-      float est = fmaxf(all, static_cast<float>((units + n - 1) / n) * one);
-      if (units > p.prefix_slots) est = INFINITY;
-      float best = est;
+      const float est =
+          fits ? fmaxf(all, static_cast<float>((units + n - 1) / n) * one) : INFINITY;
+      // Costs are positive, so their bit patterns are ordered like them.
+      const unsigned best = __reduce_min_sync(0xffffffffu, __float_as_uint(est));
+      const int src = __ffs(__ballot_sync(0xffffffffu, __float_as_uint(est) == best)) - 1;
+      const int cut = __shfl_sync(0xffffffffu, chunk, src);
+      const bool use_pairs = Shape::NS == 2 && (src & 1);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) best = fminf(best, __shfl_xor_sync(0xffffffffu, best, o));
-      const int src = __ffs(__ballot_sync(0xffffffffu, est == best)) - 1;
-      cut = __shfl_sync(0xffffffffu, static_cast<int>(chunk), src);
-      use_pairs = __shfl_sync(0xffffffffu, static_cast<int>(pairs), src);
-    }
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      if (32 * j < p.P) {
-        if (tiles[j] > 0) {
-          const int q = (end[j] - begin[j] + p.TB - 1) / p.TB;
-          pair[j] = use_pairs && q > 1;
-          nq[j] = pair[j] ? (q + 1) / 2 : q;
+      for (int j = 0; j < J; ++j)
+        if (32 * j < p.P) {
           splits[j] = (tiles[j] + cut - 1) / cut;
+          pair[j] = use_pairs && q[j] > 1;
+          nq[j] = max(1, pair[j] ? (q[j] + 1) / 2 : q[j]);
+          upto[j] = prefix_units + warp_incl_sum(nq[j] * splits[j] * p.Hkv);
+          prefix_units = __shfl_sync(0xffffffffu, upto[j], 31);
         }
-        upto[j] = carry_n + warp_incl_sum(nq[j] * splits[j] * p.Hkv);
-        carry_n = __shfl_sync(0xffffffffu, upto[j], 31);
-      }
     }
-    prefix_units = carry_n;
     // Unit sums of the blocks of 32 sequences.
     own_units = 0;
 #pragma unroll
-    for (int j = 0; j < J; ++j) own_upto[j] = 0;
-    if (p.max_blocks > 0) {
-#pragma unroll
-      for (int j = 0; j < J; ++j)
+    for (int j = 0; j < J; ++j)
+      if (32 * j < blocks) {
+#pragma unroll 8
         for (int k = 32 * j; k < min(blocks, 32 * (j + 1)); ++k) {
           const int t = tiles_of(own_len(p, 32 * k + lane));
-          const int s = warp_sum((t + own_tiles - 1) / own_tiles) * p.Hkv;
-          if (k % 32 == lane) own_upto[j] = s;
+          const int sum = __reduce_add_sync(0xffffffffu, (t + own_tiles - 1) / own_tiles);
+          if ((k & 31) == lane) own_upto[j] = sum * p.Hkv;
         }
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (32 * j < blocks) {
-          own_upto[j] = own_units + warp_incl_sum(own_upto[j]);
-          own_units = __shfl_sync(0xffffffffu, own_upto[j], 31);
-        }
-    }
+        own_upto[j] = own_units + warp_incl_sum(own_upto[j]);
+        own_units = __shfl_sync(0xffffffffu, own_upto[j], 31);
+      }
   }
 
-  // The group and KV head ... of prefix unit u, or the sequence of an own one.
   struct Where {
     PxUnit unit;
     const int32_t* table;   // the table row of its keys
@@ -371,46 +381,51 @@ struct PxPlan {
     int kv;                 // KV head
     int q0;                 // first sequence
   };
-  __device__ Where find(const PrefixParams& p, int u) const {
+  // Part `i` of t tiles cut into s equal parts (the first t % s one longer).
+  static __device__ __forceinline__ void cut_out(Where& w, int i, int t, int s) {
+    const int each = t / s, more = t - each * s;
+    w.t0 = i * each + min(i, more);
+    w.unit.tiles = each + (i < more);
+    w.unit.last_valid = i == s - 1 ? w.len - (t - 1) * Shape::KEYS : Shape::KEYS;
+  }
+  // Unit u. A prefix unit counts (KV head, split, query tile), tiles fastest;
+  // an own one (sequence, KV head, split).
+  __device__ __forceinline__ Where find(const PrefixParams& p, int u) const {
     const int lane = threadIdx.x & 31;
     Where w;
     w.unit.own = u >= prefix_units;
+    w.unit.rows[0] = p.G;
+    w.unit.rows[1] = 0;
+    w.unit.pair = 0;
     if (!w.unit.own) {
-      int g = 0, a = 0, e = 0, len_g = 0, t = 0, s = 1, q = 1, pr = 0, last = 0;
       bool found = false;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         if (32 * j < p.P && !found) {
           const unsigned hit = __ballot_sync(0xffffffffu, u < upto[j]);
           if (hit) {
-            const int src = __ffs(hit) - 1;
             found = true;
-            g = 32 * j + src;
-            a = __shfl_sync(0xffffffffu, begin[j], src);
-            e = __shfl_sync(0xffffffffu, end[j], src);
-            len_g = __shfl_sync(0xffffffffu, len[j], src);
-            t = __shfl_sync(0xffffffffu, tiles[j], src);
-            s = __shfl_sync(0xffffffffu, splits[j], src);
-            q = __shfl_sync(0xffffffffu, nq[j], src);
-            pr = __shfl_sync(0xffffffffu, pair[j], src);
-            last = __shfl_sync(0xffffffffu, upto[j], src);
+            const int src = __ffs(hit) - 1;
+            const int a = __shfl_sync(0xffffffffu, begin[j], src);
+            const int e = __shfl_sync(0xffffffffu, end[j], src);
+            const int t = __shfl_sync(0xffffffffu, tiles[j], src);
+            const int s = __shfl_sync(0xffffffffu, splits[j], src);
+            const int q = __shfl_sync(0xffffffffu, nq[j], src);
+            const int pr = __shfl_sync(0xffffffffu, pair[j], src);
+            w.len = __shfl_sync(0xffffffffu, len[j], src);
+            const int local = u - (__shfl_sync(0xffffffffu, upto[j], src) - q * s * p.Hkv);
+            const int outer = local / q, i = local - outer * q;
+            w.kv = outer / s;
+            cut_out(w, outer - w.kv * s, t, s);
+            w.q0 = a + i * (pr ? 2 : 1) * p.TB;
+            w.unit.rows[0] = min(p.TB, e - w.q0) * p.G;
+            w.unit.rows[1] = pr ? max(0, min(p.TB, e - w.q0 - p.TB)) * p.G : 0;
+            w.unit.pair = w.unit.rows[1] > 0;
+            w.unit.slot = u;
+            w.table = p.prefix_table + static_cast<size_t>(32 * j + src) * p.max_pblocks;
           }
         }
       }
-      const int local = u - (last - q * s * p.Hkv);
-      const int i = local % q, split = local / q % s;
-      w.kv = local / q / s;
-      w.t0 = static_cast<int>(static_cast<long long>(split) * t / s);
-      const int t1 = static_cast<int>(static_cast<long long>(split + 1) * t / s);
-      w.q0 = a + i * (pr ? 2 : 1) * p.TB;
-      w.unit.rows[0] = min(p.TB, e - w.q0) * p.G;
-      w.unit.rows[1] = pr ? max(0, min(p.TB, e - w.q0 - p.TB)) * p.G : 0;
-      w.unit.pair = w.unit.rows[1] > 0;
-      w.unit.tiles = t1 - w.t0;
-      w.unit.last_valid = t1 == t ? len_g - (t - 1) * Shape::KEYS : Shape::KEYS;
-      w.unit.slot = u;
-      w.table = p.prefix_table + static_cast<size_t>(g) * p.max_pblocks;
-      w.len = len_g;
       return w;
     }
     const int v = u - prefix_units;
@@ -420,43 +435,29 @@ struct PxPlan {
     for (int j = 0; j < J; ++j) {
       if (!found) {
         const unsigned hit = __ballot_sync(0xffffffffu, v < own_upto[j]);
-        if (hit) {
-          const int src = __ffs(hit) - 1;
-          found = true;
-          block = 32 * j + src;
-          before = src > 0 ? __shfl_sync(0xffffffffu, own_upto[j], src > 0 ? src - 1 : 0)
-                           : before;
-        } else {
-          before = __shfl_sync(0xffffffffu, own_upto[j], 31);
-        }
+        const int at = hit ? __ffs(hit) - 2 : 31;
+        if (at >= 0) before = __shfl_sync(0xffffffffu, own_upto[j], at);
+        block = 32 * j + at + 1;
+        found = hit != 0;
       }
     }
     const int my_len = own_len(p, 32 * block + lane);
     const int my_splits = (tiles_of(my_len) + own_tiles - 1) / own_tiles;
     const int incl = warp_incl_sum(my_splits * p.Hkv);
-    const unsigned hit = __ballot_sync(0xffffffffu, v - before < incl);
-    const int src = hit ? __ffs(hit) - 1 : 31;
+    const int src = __ffs(__ballot_sync(0xffffffffu, v - before < incl) | 0x80000000u) - 1;
     const int s = max(1, __shfl_sync(0xffffffffu, my_splits, src));
-    const int len_b = __shfl_sync(0xffffffffu, my_len, src);
+    w.len = __shfl_sync(0xffffffffu, my_len, src);
     const int local = v - before - (__shfl_sync(0xffffffffu, incl, src) - s * p.Hkv);
-    const int t = tiles_of(len_b), split = local % s;
     w.kv = local / s;
-    w.t0 = static_cast<int>(static_cast<long long>(split) * t / s);
-    const int t1 = static_cast<int>(static_cast<long long>(split + 1) * t / s);
+    cut_out(w, local - w.kv * s, tiles_of(w.len), s);
     w.q0 = 32 * block + src;
-    w.unit.rows[0] = p.G;
-    w.unit.rows[1] = 0;
-    w.unit.pair = 0;
-    w.unit.tiles = t1 - w.t0;
-    w.unit.last_valid = t1 == t ? len_b - (t - 1) * Shape::KEYS : Shape::KEYS;
     w.unit.slot = v;
     w.table = p.block_table + static_cast<size_t>(w.q0) * p.max_blocks;
-    w.len = len_b;
     return w;
   }
 
   // For the combine kernel (one warp of one CTA).
-  __device__ void write(const PrefixParams& p) const {
+  __device__ __forceinline__ void write(const PrefixParams& p) const {
     const int lane = threadIdx.x & 31;
     if (lane == 0) p.head->own_tiles = own_tiles;
 #pragma unroll
@@ -545,13 +546,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   const bool aligned = (base_s & 1023u) == 0;   // the tiles need it; dynamic memory starts so
   if (!aligned && threadIdx.x == 0) atomicOr(&p.head->status, kErrPxLoad);
 
-  if (aligned && warp == kPxLoadWarp) {
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPxAuxRegs));
+    if (aligned && warp == kPxLoadWarp) {
     // ------------------------------------------------------- plan and loads
     PxPlan<D> plan;
     plan.make(p);
     const int total = plan.prefix_units + plan.own_units;
-    uint64_t keep, once = evict_first_policy();
-    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(keep));
+    const uint64_t policy = evict_first_policy();
     const int nch = KEYS / p.R;              // boxes of one 64-column part of a tile
     const int chunk = lane % nch, part = lane / nch;
     const bool boxed = part < PARTS;
@@ -577,6 +579,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       ++unit_no;
       if (w.unit.tiles == 0) break;
       const int n = w.unit.tiles;
+      // The row of tile i's box of this lane; rows past the length read zeros.
+      auto row_of = [&](int i) {
+        const int c = (w.t0 + i) * KEYS + chunk * p.R;
+        if (!boxed || i >= n || c >= w.len) return oob;
+        const int col = c / p.bs, block = w.table[col];
+        return block >= 0 && block < p.num_blocks ? block * p.bs + (c - col * p.bs) : oob;
+      };
+      int r0 = row_of(0), r1 = row_of(1), r2 = row_of(2);
       for (int i = 0; i <= w.unit.pair && ok; ++i) {
         const int buf = fills % Shape::QBUF;
         ok = warp_poll(qempty0 + 8 * buf, ((fills / Shape::QBUF) & 1) ^ 1, p.timeout_ns);
@@ -587,18 +597,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         if (lane < PARTS)
           tma_load_4d(qbuf_s + buf * Shape::QBYTES + lane * 128 * 128,
                       w.unit.own ? &p.q_one_map : &p.q_tile_map, 64 * lane, 0, w.kv,
-                      w.q0 + i * p.TB, qfull0 + 8 * buf, keep);
+                      w.q0 + i * p.TB, qfull0 + 8 * buf, policy);
         ++fills;
       }
       if (!ok) break;
-      // The row of tile i's box of this lane; rows past the length read zeros.
-      auto row_of = [&](int i) {
-        const int c = (w.t0 + i) * KEYS + chunk * p.R;
-        if (!boxed || i >= n || c >= w.len) return oob;
-        const int col = c / p.bs, block = w.table[col];
-        return block >= 0 && block < p.num_blocks ? block * p.bs + (c - col * p.bs) : oob;
-      };
-      const uint64_t policy = w.unit.own ? once : keep;
       auto load = [&](const CUtensorMap* map, int row) {
         const unsigned stage = pos % STAGES;
         if (!warp_poll(empty0 + 8 * stage, ((pos / STAGES) & 1) ^ 1, p.timeout_ns)) return false;
@@ -610,7 +612,6 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         ++pos;
         return true;
       };
-      int r0 = row_of(0), r1 = row_of(1), r2 = row_of(2);
       ok = load(&p.k_map, r0) && (n == 1 || load(&p.k_map, r1));
       for (int i = 0; i < n && ok; ++i) {
         const int r3 = row_of(i + 3);
@@ -622,6 +623,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       if (!ok) break;
       u = __shfl_sync(0xffffffffu, next, 0);
     }
+    if (blockIdx.x == gridDim.x - 1) plan.write(p);
     if (!ok) {
       if (lane == 0) atomicOr(&p.head->status, kErrPxLoad);
       for (unsigned i = pos > STAGES ? pos - STAGES : 0; i < pos; ++i)
@@ -629,11 +631,11 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       for (unsigned i = fills > Shape::QBUF ? fills - Shape::QBUF : 0; i < fills; ++i)
         mbar_wait(qfull0 + 8 * (i % Shape::QBUF), (i / Shape::QBUF) & 1, p.timeout_ns);
     }
-  } else if (aligned && warp == kPxMmaWarp) {
+    } else if (aligned && warp == kPxMmaWarp) {
     // ------------------------------------------------------------ MMA issue
     if (lane == 0) {
       constexpr uint32_t qk_idesc = px_idesc<Tag>(KEYS, false), pv_idesc = px_idesc<Tag>(D, true);
-      unsigned base = 0, fills = 0, done[2] = {0, 0};   // stages, fills, tiles of each stream
+      unsigned base = 0, fills = 0, done0 = 0, done1 = 0;   // stages, fills, tiles of each stream
       bool ok = true;
       for (unsigned unit_no = 0; ok; ++unit_no) {
         const int seg = unit_no % kPxSegs;
@@ -641,7 +643,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         const int n = units[seg].tiles, pair = units[seg].pair;
         mbar_arrive(uempty0 + 8 * seg);
         if (n == 0) break;
-        const int cnt[2] = {NS == 1 || pair ? n : (n + 1) / 2, NS == 1 ? 0 : pair ? n : n / 2};
+        const int n0 = NS == 1 || pair ? n : (n + 1) / 2, n1 = NS == 1 ? 0 : pair ? n : n / 2;
         auto tile_of = [&](int w, int j) { return NS == 1 || pair ? j : 2 * j + w; };
         auto s_of = [&](int w, unsigned tile_no) {
           return tmem + Shape::S_COL * (NS == 2 ? w : tile_no & 1);
@@ -654,7 +656,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           ok = ok && mbar_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns);
           if (!ok) return;
           tc_fence_after();
-          const unsigned no = done[w] + j;
+          const unsigned no = (w ? done1 : done0) + j;
           const uint64_t a = smem_desc(qbuf_s + buf * Shape::QBYTES, 16, 1024, 2);
           const uint64_t b = smem_desc(ring_s + stage * Shape::STAGE, 16, 1024, 2);
 #pragma unroll
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         auto pv = [&](int w, int j) {
           const int i = tile_of(w, j);
           const unsigned at = base + v_pos(i, n), stage = at % STAGES;
-          const unsigned no = done[w] + j;
+          const unsigned no = (w ? done1 : done0) + j;
           ok = ok && mbar_poll(pfull0 + 8 * (NS == 2 ? w : no & 1), (NS == 2 ? no : no >> 1) & 1,
                                p.timeout_ns);
           if (j == 0 && unit_no > 0) ok = ok && mbar_poll(ofree, (unit_no - 1) & 1, p.timeout_ns);
@@ -682,7 +684,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
                        b + (uint64_t)(kk * (2048 >> 4)), pv_idesc, j > 0 || kk > 0);
           if (!pair || w == 1) mma_commit(empty0 + 8 * stage);
           if (NS == 1) mma_commit(pvdone);
-          if (j == cnt[w] - 1) mma_commit(ofull0 + 8 * w);
+          if (j == (w ? n1 : n0) - 1) mma_commit(ofull0 + 8 * w);
         };
         if constexpr (NS == 1) {
           qk(0, 0);
@@ -692,19 +694,20 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           }
         } else {
           qk(0, 0);
-          if (cnt[1] > 0) qk(1, 0);
-          for (int j = 0; j < cnt[0] && ok; ++j)
-#pragma unroll
-            for (int w = 0; w < 2; ++w)
-              if (j < cnt[w]) {
-                pv(w, j);
-                if (j + 1 < cnt[w]) qk(w, j + 1);
-              }
+          if (n1 > 0) qk(1, 0);
+          for (int j = 0; j < n0 && ok; ++j) {
+            pv(0, j);
+            if (j + 1 < n0) qk(0, j + 1);
+            if (j < n1) {
+              pv(1, j);
+              if (j + 1 < n1) qk(1, j + 1);
+            }
+          }
         }
         base += 2 * n;
         fills += 1 + pair;
-        done[0] += cnt[0];
-        done[1] += cnt[1];
+        done0 += n0;
+        done1 += n1;
       }
       if (!ok) {
         atomicOr(&p.head->status, kErrPxMma);
@@ -713,30 +716,31 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       }
     }
     __syncwarp();
-  } else if (aligned) {
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPxSoftmaxRegs));
     // ------------------------------------------------- softmax, units' ends
     const int w = warp >> 2;                  // stream
     const int r = threadIdx.x & 127;          // row of the query tile, tensor-memory lane
     const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    if (blockIdx.x == 0 && warp == 4) {
-      PxPlan<D> plan;
-      plan.make(p);
-      plan.write(p);
-    }
-    unsigned base = 0, done = 0, ends[2] = {0, 0}, meets = 0;
-    bool ok = true;
+    unsigned base = 0, done = 0, ends0 = 0, ends1 = 0, meets = 0;
+    bool ok = aligned;
     for (unsigned unit_no = 0; ok; ++unit_no) {
       const int seg = unit_no % kPxSegs;
       if (!(ok = warp_poll(ufull0 + 8 * seg, (unit_no / kPxSegs) & 1, p.timeout_ns))) break;
-      const PxUnit un = units[seg];
+      PxUnit un;
+      un.tiles = units[seg].tiles;
+      un.pair = units[seg].pair;
+      un.last_valid = units[seg].last_valid;
+      un.slot = units[seg].slot;
+      un.own = units[seg].own;
+      const int rows = units[seg].rows[un.pair && w == 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(uempty0 + 8 * seg);
       const int n = un.tiles;
       if (n == 0) break;
-      const int cnt[2] = {NS == 1 || un.pair ? n : (n + 1) / 2,
-                          NS == 1 ? 0 : un.pair ? n : n / 2};
-      const int mine = cnt[w];
-      const int rows = un.pair && w == 1 ? un.rows[1] : un.rows[0];
+      const int n0 = NS == 1 || un.pair ? n : (n + 1) / 2, n1 = NS == 1 ? 0 : un.pair ? n : n / 2;
+      const int mine = w ? n1 : n0;
       const bool active = 32 * (warp & 3) < rows;   // warps without rows only keep step
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < mine; ++j) {
@@ -804,17 +808,18 @@ __global__ void __launch_bounds__(kPxThreads, 1)
               tmem_st32(o_addr + c, reinterpret_cast<const uint32_t*>(o));
             }
           }
-          const float shift = kOff - m;
+          const float shift = kOff - m, qscale = p.qscale;
           float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
           for (int c0 = 0; c0 < KEYS; c0 += 64) {
             uint32_t w16[32];
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
-              const float x = ex2(fmaf(s[c0 + c], p.qscale, shift));
-              const float y = ex2(fmaf(s[c0 + c + 1], p.qscale, shift));
-              sum[c & 2] += x;
-              sum[(c & 2) + 1] += y;
+              float x, y;
+              fma2(s[c0 + c], s[c0 + c + 1], qscale, qscale, shift, shift, x, y);
+              x = ex2(x);
+              y = ex2(y);
+              add2(sum[c & 2], sum[(c & 2) + 1], x, y);
               w16[c / 2] = pack2<Tag>(x, y);
             }
             tmem_st32(s_addr + c0 / 2, w16);
@@ -830,11 +835,11 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       done += mine;
       // The unit's end: O, m and l to its slot.
       const bool both = NS == 2 && !un.pair;        // one query tile, merged here
-      for (int x = 0; x < 2 && ok; ++x)
-        if (cnt[x] > 0 && (both || NS == 1 || x == w))
-          ok = warp_poll(ofull0 + 8 * x, ends[x] & 1, p.timeout_ns);
+      if (w == 0 || !un.pair) ok = warp_poll(ofull0, ends0 & 1, p.timeout_ns);
+      if (n1 > 0 && (w == 1 || both)) ok = ok && warp_poll(ofull0 + 8, ends1 & 1, p.timeout_ns);
       if (!ok) break;
-      for (int x = 0; x < 2; ++x) ends[x] += cnt[x] > 0;
+      ++ends0;
+      ends1 += n1 > 0;
       tc_fence_after();
       float a0 = 1.0f, a1 = 0.0f;
       if (both) {
@@ -843,7 +848,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         if (lane == 0) mbar_arrive(meet);
         if (!(ok = warp_poll(meet, meets & 1, p.timeout_ns))) break;
         ++meets;
-        if (cnt[1] > 0) {
+        if (n1 > 0) {
           const float2 x = ml[r], y = ml[128 + r];
           const float top = fmaxf(x.x, y.x);
           a0 = ex2(x.x - top);
@@ -873,7 +878,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         for (int c = c_begin; c < c_end; c += 32) {
           float o[32];
           tmem_ld32(o_addr + c, o);
-          if (both && cnt[1] > 0) {
+          if (both && n1 > 0) {
             float o1[32];
             tmem_ld32(o_addr + D + c, o1);
             tmem_wait_ld();
@@ -912,18 +917,25 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 }
 
 // out row = sum over its slots of 2^(m_s - M) O_s / sum of 2^(m_s - M) l_s, the
-// prefix's splits first, then the sequence's own. One CTA a (sequence, KV
-// head), a thread a row and 4 columns.
+// prefix's splits first, then the sequence's own, with a running maximum. A
+// CTA takes 128 of the (row, 4 columns) of one sequence and KV head, a thread
+// one; the slots come from L2 eight at a time, since a row may have dozens.
 constexpr int kPxCombineThreads = 128;
 
 template <typename Tag, int D>
 __global__ void __launch_bounds__(kPxCombineThreads)
     gqa_prefix_combine_kernel(const __grid_constant__ PrefixParams p) {
   using Shape = PxShape<D>;
-  const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, lane = threadIdx.x & 31;
+  const int parts = (p.G * (D / 4) + kPxCombineThreads - 1) / kPxCombineThreads;
+  const int bh = blockIdx.x / parts, b = bh / p.Hkv, h = bh - b * p.Hkv;
+  const int x = (blockIdx.x - bh * parts) * kPxCombineThreads + threadIdx.x;
+  const int lane = threadIdx.x & 31;
   grid_dependency_wait();
   grid_launch_dependents();
   if (blockIdx.x == 0 && threadIdx.x == 0) p.head->next = 0;   // for the next call
+  const int own_tiles = p.head->own_tiles;
+  const int own_base = p.max_blocks > 0 ? p.head->own_base[b] : 0;
+  const int own_len = PxPlan<D>::own_len(p, b);
   int group = -1;
   for (int j = 0; j < p.P; j += 32) {
     bool in = false;
@@ -934,57 +946,60 @@ __global__ void __launch_bounds__(kPxCombineThreads)
     const unsigned hit = __ballot_sync(0xffffffffu, in);
     if (hit) group = j + __ffs(hit) - 1;
   }
-  int n0 = 0, row0 = 0;
-  size_t tile0 = 0, step0 = 0;     // prefix: first tile of slots, tiles between splits
+  if (x >= p.G * (D / 4)) return;
+  const int g = x % p.G, c = x / p.G;
+  float top = -INFINITY, sum = 0.0f;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  // n slots, `step` tiles of `rows` rows apart.
+  auto add = [&](const float* o, const float2* ml, size_t tile, size_t step, int n, int rows, int row) {
+    const float4* o4 = reinterpret_cast<const float4*>(o) + (tile * (D / 4) + c) * rows + row;
+    const float2* m2 = ml + tile * rows + row;
+    constexpr int U = 8;
+    for (int s = 0; s < n; s += U) {
+      float2 m[U];
+      float4 v[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        m[i] = make_float2(-INFINITY, 0.0f);
+        v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (s + i < n) {
+          m[i] = __ldcg(m2 + (s + i) * step * rows);
+          v[i] = __ldcg(o4 + (s + i) * step * (D / 4) * rows);
+        }
+      }
+      float now = top;
+#pragma unroll
+      for (int i = 0; i < U; ++i) now = fmaxf(now, m[i].x);
+      const float old = ex2(top - now);
+      top = now;
+      sum *= old;
+      acc.x *= old; acc.y *= old; acc.z *= old; acc.w *= old;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const float a = ex2(m[i].x - now);
+        sum = fmaf(a, m[i].y, sum);
+        acc.x = fmaf(a, v[i].x, acc.x);
+        acc.y = fmaf(a, v[i].y, acc.y);
+        acc.z = fmaf(a, v[i].z, acc.z);
+        acc.w = fmaf(a, v[i].w, acc.w);
+      }
+    }
+  };
   if (group >= 0) {
-    const PxGroup g = p.head->group[group];
-    const int t = (b - g.begin) / p.TB;
-    const int i = g.pair ? t / 2 : t;
-    n0 = g.splits;
-    row0 = (b - g.begin - t * p.TB) * p.G;
-    tile0 = (static_cast<size_t>(g.base) + static_cast<size_t>(h) * g.splits * g.nq + i) * Shape::NS +
-            (g.pair ? t & 1 : 0);
-    step0 = static_cast<size_t>(g.nq) * Shape::NS;
+    const PxGroup gr = p.head->group[group];
+    const int t = (b - gr.begin) / p.TB;
+    const size_t unit = gr.base + static_cast<size_t>(h) * gr.splits * gr.nq + (gr.pair ? t / 2 : t);
+    add(p.prefix_o, p.prefix_ml, unit * Shape::NS + (gr.pair ? t & 1 : 0),
+        static_cast<size_t>(gr.nq) * Shape::NS, gr.splits, 128, (b - gr.begin - t * p.TB) * p.G + g);
   }
-  int n1 = 0;
-  size_t slot1 = 0;
-  if (p.max_blocks > 0) {
-    const int tiles = PxPlan<D>::tiles_of(PxPlan<D>::own_len(p, b));
-    n1 = (tiles + p.head->own_tiles - 1) / p.head->own_tiles;
-    slot1 = static_cast<size_t>(p.head->own_base[b]) + static_cast<size_t>(h) * n1;
+  if (own_len > 0) {
+    const int n = (PxPlan<D>::tiles_of(own_len) + own_tiles - 1) / own_tiles;
+    add(p.own_o, p.own_ml, own_base + static_cast<size_t>(h) * n, 1, n, p.G, g);
   }
-  for (int x = threadIdx.x; x < p.G * (D / 4); x += kPxCombineThreads) {
-    const int g = x % p.G, c = x / p.G;
-    const float2* ml0 = p.prefix_ml + tile0 * 128 + row0 + g;
-    const float2* ml1 = p.own_ml + slot1 * p.G + g;
-    const float4* o0 = reinterpret_cast<const float4*>(p.prefix_o) +
-                       (tile0 * (D / 4) + c) * 128 + row0 + g;
-    const float4* o1 = reinterpret_cast<const float4*>(p.own_o) + (slot1 * (D / 4) + c) * p.G + g;
-    float top = -INFINITY;
-    for (int s = 0; s < n0; ++s) top = fmaxf(top, __ldcg(ml0 + s * step0 * 128).x);
-    for (int s = 0; s < n1; ++s) top = fmaxf(top, __ldcg(ml1 + static_cast<size_t>(s) * p.G).x);
-    float sum = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    auto add = [&](const float2 ml, const float4 o) {
-      const float a = ex2(ml.x - top);
-      sum = fmaf(a, ml.y, sum);
-      acc.x = fmaf(a, o.x, acc.x);
-      acc.y = fmaf(a, o.y, acc.y);
-      acc.z = fmaf(a, o.z, acc.z);
-      acc.w = fmaf(a, o.w, acc.w);
-    };
-#pragma unroll 4
-    for (int s = 0; s < n0; ++s)
-      add(__ldcg(ml0 + s * step0 * 128), __ldcg(o0 + s * step0 * (D / 4) * 128));
-#pragma unroll 4
-    for (int s = 0; s < n1; ++s)
-      add(__ldcg(ml1 + static_cast<size_t>(s) * p.G),
-          __ldcg(o1 + static_cast<size_t>(s) * (D / 4) * p.G));
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const uint2 y = make_uint2(pack2<Tag>(acc.x * inv, acc.y * inv), pack2<Tag>(acc.z * inv, acc.w * inv));
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
-                              (static_cast<size_t>(b) * p.Hq + h * p.G + g) * D + 4 * c) = y;
-  }
+  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+  const uint2 y = make_uint2(pack2<Tag>(acc.x * inv, acc.y * inv), pack2<Tag>(acc.z * inv, acc.w * inv));
+  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
+                            (static_cast<size_t>(b) * p.Hq + h * p.G + g) * D + 4 * c) = y;
 }
 
 }  // namespace gqa_av
