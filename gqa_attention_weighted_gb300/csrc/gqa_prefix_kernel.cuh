@@ -33,8 +33,9 @@
 // S buffers and key tiles of 64.
 //
 // Warps: 0-3 and 4-7 softmax warpgroups (and the units' ends), 8 issues the
-// MMAs from one thread, 9 makes the plan, hands out units and issues the TMA
-// loads, one box a lane; 10 and 11 only fill their warpgroup. Every wait is bounded (2 s): on expiry the role sets
+// MMAs from one thread, 9 makes the plan, hands out units and loads queries and
+// K, 10 loads V (a box of a small block costs its issuing warp some time, so K
+// and V go out from two); 11 only fills the warpgroup. Every wait is bounded (2 s): on expiry the role sets
 // the status word and leaves, the others run out in turn, copies and MMAs in
 // flight are waited for and tensor memory is freed.
 #pragma once
@@ -53,7 +54,7 @@ constexpr int kPxThreads = 384;
 // warpgroup gives up enough of them for the softmax warpgroups' 128 scores a
 // thread: 2 * 128 * 200 + 128 * 104 = 384 * 168.
 constexpr int kPxSoftmaxRegs = 200, kPxAuxRegs = 104;
-constexpr int kPxMmaWarp = 8, kPxLoadWarp = 9;
+constexpr int kPxMmaWarp = 8, kPxKWarp = 9, kPxVWarp = 10;
 constexpr int kPxMaxGroups = 128;
 constexpr int kPxMaxB = 4096;
 constexpr int kPxSegs = 4;             // unit descriptors in flight
@@ -200,9 +201,14 @@ struct PxUnit {
   int tiles;          // key tiles; 0: no more units
   int pair;           // two query tiles, each with all key tiles
   int rows[2];        // rows of the query tiles
+  int q0;             // first sequence
   int last_valid;     // keys of the last tile
   int slot;           // its slot
   int own;            // a sequence's own unit
+  int kv;             // KV head
+  int t0;             // first key tile
+  int len;            // rows that its table row lists
+  const int32_t* table;
 };
 
 // Positions of a unit's K and V tiles in its run of 2 * tiles stages, in the
@@ -373,31 +379,23 @@ struct PxPlan {
       }
   }
 
-  struct Where {
-    PxUnit unit;
-    const int32_t* table;   // the table row of its keys
-    int len;                // rows that the table row lists
-    int t0;                 // first key tile
-    int kv;                 // KV head
-    int q0;                 // first sequence
-  };
   // Part `i` of t tiles cut into s equal parts (the first t % s one longer).
-  static __device__ __forceinline__ void cut_out(Where& w, int i, int t, int s) {
+  static __device__ __forceinline__ void cut_out(PxUnit& w, int i, int t, int s) {
     const int each = t / s, more = t - each * s;
     w.t0 = i * each + min(i, more);
-    w.unit.tiles = each + (i < more);
-    w.unit.last_valid = i == s - 1 ? w.len - (t - 1) * Shape::KEYS : Shape::KEYS;
+    w.tiles = each + (i < more);
+    w.last_valid = i == s - 1 ? w.len - (t - 1) * Shape::KEYS : Shape::KEYS;
   }
   // Unit u. A prefix unit counts (KV head, split, query tile), tiles fastest;
   // an own one (sequence, KV head, split).
-  __device__ __forceinline__ Where find(const PrefixParams& p, int u) const {
+  __device__ __forceinline__ PxUnit find(const PrefixParams& p, int u) const {
     const int lane = threadIdx.x & 31;
-    Where w;
-    w.unit.own = u >= prefix_units;
-    w.unit.rows[0] = p.G;
-    w.unit.rows[1] = 0;
-    w.unit.pair = 0;
-    if (!w.unit.own) {
+    PxUnit w;
+    w.own = u >= prefix_units;
+    w.rows[0] = p.G;
+    w.rows[1] = 0;
+    w.pair = 0;
+    if (!w.own) {
       bool found = false;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
@@ -418,10 +416,10 @@ struct PxPlan {
             w.kv = outer / s;
             cut_out(w, outer - w.kv * s, t, s);
             w.q0 = a + i * (pr ? 2 : 1) * p.TB;
-            w.unit.rows[0] = min(p.TB, e - w.q0) * p.G;
-            w.unit.rows[1] = pr ? max(0, min(p.TB, e - w.q0 - p.TB)) * p.G : 0;
-            w.unit.pair = w.unit.rows[1] > 0;
-            w.unit.slot = u;
+            w.rows[0] = min(p.TB, e - w.q0) * p.G;
+            w.rows[1] = pr ? max(0, min(p.TB, e - w.q0 - p.TB)) * p.G : 0;
+            w.pair = w.rows[1] > 0;
+            w.slot = u;
             w.table = p.prefix_table + static_cast<size_t>(32 * j + src) * p.max_pblocks;
           }
         }
@@ -451,7 +449,7 @@ struct PxPlan {
     w.kv = local / s;
     cut_out(w, local - w.kv * s, tiles_of(w.len), s);
     w.q0 = 32 * block + src;
-    w.unit.slot = v;
+    w.slot = v;
     w.table = p.block_table + static_cast<size_t>(w.q0) * p.max_blocks;
     return w;
   }
@@ -527,11 +525,11 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     mbar_init(drain, 1);
     for (int i = 0; i < kPxSegs; ++i) {
       mbar_init(ufull0 + 8 * i, 1);
-      mbar_init(uempty0 + 8 * i, 9);
+      mbar_init(uempty0 + 8 * i, 10);
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == kPxLoadWarp && lane < 4) {
+  if (warp == kPxKWarp && lane < 4) {
     const CUtensorMap* m = lane == 0 ? &p.k_map : lane == 1 ? &p.v_map : lane == 2 ? &p.q_tile_map
                                                                                    : &p.q_one_map;
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
@@ -548,89 +546,108 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPxAuxRegs));
-    if (aligned && warp == kPxLoadWarp) {
-    // ------------------------------------------------------- plan and loads
-    PxPlan<D> plan;
-    plan.make(p);
-    const int total = plan.prefix_units + plan.own_units;
-    const uint64_t policy = evict_first_policy();
-    const int nch = KEYS / p.R;              // boxes of one 64-column part of a tile
-    const int chunk = lane % nch, part = lane / nch;
-    const bool boxed = part < PARTS;
-    const int oob = p.num_blocks * p.bs;
-    unsigned pos = 0, fills = 0, unit_no = 0;
-    bool ok = true;
-    int u = blockIdx.x;
-    while (true) {
-      int next = 0;
-      typename PxPlan<D>::Where w;
-      w.unit.tiles = 0;
-      if (u < total) {
-        w = plan.find(p, u);
-        if (lane == 0) next = atomicAdd(&p.head->next, 1) + gridDim.x;
-      }
-      const int seg = unit_no % kPxSegs;
-      if (!(ok = warp_poll(uempty0 + 8 * seg, ((unit_no / kPxSegs) & 1) ^ 1, p.timeout_ns))) break;
-      if (lane == 0) {
-        units[seg] = w.unit;
-        mbar_arrive(ufull0 + 8 * seg);
-      }
-      __syncwarp();
-      ++unit_no;
-      if (w.unit.tiles == 0) break;
-      const int n = w.unit.tiles;
-      // The row of tile i's box of this lane; rows past the length read zeros.
-      auto row_of = [&](int i) {
-        const int c = (w.t0 + i) * KEYS + chunk * p.R;
-        if (!boxed || i >= n || c >= w.len) return oob;
-        const int col = c / p.bs, block = w.table[col];
+    if (aligned && (warp == kPxKWarp || warp == kPxVWarp)) {
+    // ------------------------------------- plan, units, queries and K, or V
+      const bool is_k = warp == kPxKWarp;
+      const uint64_t policy = evict_first_policy();
+      const int nch = KEYS / p.R;              // boxes of one 64-column part of a tile
+      const int oob = p.num_blocks * p.bs;
+      unsigned base = 0, fills = 0;
+      // Lane s: 1 + parity of this warp's last copy into stage s (0: none yet);
+      // lane 16 + s: into query buffer s.
+      unsigned held = 0;
+      bool ok = true;
+      // The pool row of this lane's box of tile i; rows past the length and
+      // entries outside the pool read zeros.
+      auto row_of = [&](const PxUnit& un, int i) {
+        const int c = (un.t0 + i) * KEYS + lane * p.R;
+        if (lane >= nch || i >= un.tiles || c >= un.len) return oob;
+        const int col = c / p.bs, block = un.table[col];
         return block >= 0 && block < p.num_blocks ? block * p.bs + (c - col * p.bs) : oob;
       };
-      int r0 = row_of(0), r1 = row_of(1), r2 = row_of(2);
-      for (int i = 0; i <= w.unit.pair && ok; ++i) {
-        const int buf = fills % Shape::QBUF;
-        ok = warp_poll(qempty0 + 8 * buf, ((fills / Shape::QBUF) & 1) ^ 1, p.timeout_ns);
-        if (!ok) break;
-        const int rows = w.unit.own ? p.G : p.TB * p.G;
-        if (lane == 0) mbar_arrive_expect_tx(qfull0 + 8 * buf, rows * 128 * PARTS);
-        __syncwarp();
-        if (lane < PARTS)
-          tma_load_4d(qbuf_s + buf * Shape::QBYTES + lane * 128 * 128,
-                      w.unit.own ? &p.q_one_map : &p.q_tile_map, 64 * lane, 0, w.kv,
-                      w.q0 + i * p.TB, qfull0 + 8 * buf, policy);
-        ++fills;
-      }
-      if (!ok) break;
-      auto load = [&](const CUtensorMap* map, int row) {
-        const unsigned stage = pos % STAGES;
-        if (!warp_poll(empty0 + 8 * stage, ((pos / STAGES) & 1) ^ 1, p.timeout_ns)) return false;
-        if (lane == 0) mbar_arrive_expect_tx(full0 + 8 * stage, Shape::STAGE);
-        __syncwarp();
-        if (boxed)
-          tma_load_3d(ring_s + stage * Shape::STAGE + part * KEYS * 128 + chunk * p.R * 128, map,
-                      64 * part, w.kv, row, full0 + 8 * stage, policy);
-        ++pos;
+      // One tile into the stage at position `at`: one thread issues the boxes.
+      auto load = [&](const CUtensorMap* map, const PxUnit& un, int row, unsigned at) {
+        const unsigned stage = at % STAGES;
+        if (!warp_poll(empty0 + 8 * stage, ((at / STAGES) & 1) ^ 1, p.timeout_ns)) return false;
+        const uint32_t bar = full0 + 8 * stage, dst = ring_s + stage * Shape::STAGE;
+        if (lane == 0) mbar_arrive_expect_tx(bar, Shape::STAGE);
+        if (lane == stage) held = 1 + ((at / STAGES) & 1);
+        for (int c = 0; c < nch; ++c) {
+          const int r = __shfl_sync(0xffffffffu, row, c);
+          if (lane == 0) {
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+              tma_load_3d(dst + part * KEYS * 128 + c * p.R * 128, map, 64 * part, un.kv, r, bar,
+                          policy);
+          }
+        }
         return true;
       };
-      ok = load(&p.k_map, r0) && (n == 1 || load(&p.k_map, r1));
-      for (int i = 0; i < n && ok; ++i) {
-        const int r3 = row_of(i + 3);
-        ok = load(&p.v_map, r0) && (i + 2 >= n || load(&p.k_map, r2));
-        r0 = r1;
-        r1 = r2;
-        r2 = r3;
+      PxPlan<D> plan;
+      int u = blockIdx.x, total = 0;
+      if (is_k) {
+        plan.make(p);
+        total = plan.prefix_units + plan.own_units;
       }
-      if (!ok) break;
-      u = __shfl_sync(0xffffffffu, next, 0);
-    }
-    if (blockIdx.x == gridDim.x - 1) plan.write(p);
-    if (!ok) {
-      if (lane == 0) atomicOr(&p.head->status, kErrPxLoad);
-      for (unsigned i = pos > STAGES ? pos - STAGES : 0; i < pos; ++i)
-        mbar_wait(full0 + 8 * (i % STAGES), (i / STAGES) & 1, p.timeout_ns);
-      for (unsigned i = fills > Shape::QBUF ? fills - Shape::QBUF : 0; i < fills; ++i)
-        mbar_wait(qfull0 + 8 * (i % Shape::QBUF), (i / Shape::QBUF) & 1, p.timeout_ns);
-    }
+      for (unsigned unit_no = 0; ok; ++unit_no) {
+        const int seg = unit_no % kPxSegs;
+        PxUnit un;
+        int next = 0;
+        if (is_k) {
+          un.tiles = 0;
+          if (u < total) {
+            un = plan.find(p, u);
+            if (lane == 0) next = atomicAdd(&p.head->next, 1) + gridDim.x;
+          }
+          if (!(ok = warp_poll(uempty0 + 8 * seg, ((unit_no / kPxSegs) & 1) ^ 1, p.timeout_ns))) break;
+          if (lane == 0) {
+            units[seg] = un;
+            mbar_arrive(ufull0 + 8 * seg);
+          }
+          __syncwarp();
+        } else {
+          if (!(ok = warp_poll(ufull0 + 8 * seg, (unit_no / kPxSegs) & 1, p.timeout_ns))) break;
+          un = units[seg];
+          __syncwarp();
+          if (lane == 0) mbar_arrive(uempty0 + 8 * seg);
+        }
+        const int n = un.tiles;
+        if (n == 0) break;
+        int row = row_of(un, 0);
+        if (is_k) {
+          for (int i = 0; i <= un.pair && ok; ++i, ++fills) {
+            const int buf = fills % Shape::QBUF;
+            ok = warp_poll(qempty0 + 8 * buf, ((fills / Shape::QBUF) & 1) ^ 1, p.timeout_ns);
+            if (!ok) break;
+            const uint32_t bar = qfull0 + 8 * buf;
+            if (lane == 16 + buf) held = 1 + ((fills / Shape::QBUF) & 1);
+            if (lane == 0) {
+              mbar_arrive_expect_tx(bar, (un.own ? p.G : p.TB * p.G) * 128 * PARTS);
+#pragma unroll
+              for (int part = 0; part < PARTS; ++part)
+                tma_load_4d(qbuf_s + buf * Shape::QBYTES + part * 128 * 128,
+                            un.own ? &p.q_one_map : &p.q_tile_map, 64 * part, 0, un.kv,
+                            un.q0 + i * p.TB, bar, policy);
+            }
+            __syncwarp();
+          }
+        }
+        for (int i = 0; i < n && ok; ++i) {
+          const int ahead = row_of(un, i + 1);
+          ok = load(is_k ? &p.k_map : &p.v_map, un, row, base + (is_k ? k_pos(i) : v_pos(i, n)));
+          row = ahead;
+        }
+        base += 2 * n;
+        u = __shfl_sync(0xffffffffu, next, 0);
+      }
+      if (is_k && blockIdx.x == gridDim.x - 1) plan.write(p);
+      if (!ok) {
+        // This warp's copies in flight land before the CTA leaves.
+        if (lane == 0) atomicOr(&p.head->status, kErrPxLoad);
+        if (held && lane < STAGES) mbar_wait(full0 + 8 * lane, held - 1, p.timeout_ns);
+        if (held && lane >= 16) mbar_wait(qfull0 + 8 * (lane - 16), held - 1, p.timeout_ns);
+        __syncwarp();
+      }
     } else if (aligned && warp == kPxMmaWarp) {
     // ------------------------------------------------------------ MMA issue
     if (lane == 0) {
