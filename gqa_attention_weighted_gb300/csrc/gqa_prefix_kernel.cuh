@@ -145,13 +145,72 @@ __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// D[tmem] (+)= A[tmem] * B[smem], 16-bit operands of one type.
-__device__ __forceinline__ void mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
-                                           uint32_t idesc, uint32_t accumulate) {
+// Issue by one lane of a converged warp. The operands of MMAs, commits and TMA
+// copies have to be in uniform registers; computed by the whole warp under
+// uniform control flow they stay there, while inside a one-lane branch each
+// operand is moved over for every instruction (measured: 107 cycles an MMA of
+// 64, and 110 a TMA box).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t leader;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(leader));
+  return leader;
+}
+// A value that is the same in all lanes, for uniform registers.
+__device__ __forceinline__ int uniform(int x) {
+  return static_cast<int>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(x)));
+}
+// D[tmem] (+)= A[smem] * B[smem], or A[tmem] * B[smem]: 16-bit operands of one type.
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t a, uint64_t b,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem,
+                                       uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void expect_one(uint32_t leader, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void tma_one_3d(uint32_t leader, uint32_t dst, const CUtensorMap* map,
+                                           int x0, int x1, int x2, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+      "@q cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x0), "r"(x1), "r"(x2), "r"(bar), "l"(policy),
+      "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void tma_one_4d(uint32_t leader, uint32_t dst, const CUtensorMap* map,
+                                           int x0, int x1, int x2, int x3, uint32_t bar,
+                                           uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %8, 0;\n\t"
+      "@q cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6], %7;\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x0), "r"(x1), "r"(x2), "r"(x3), "r"(bar),
+      "l"(policy), "r"(leader)
       : "memory");
 }
 
@@ -537,7 +596,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   const uint32_t qbuf_s = base_s, ring_s = base_s + Shape::QBUF * Shape::QBYTES;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -549,6 +608,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     if (aligned && (warp == kPxKWarp || warp == kPxVWarp)) {
     // ------------------------------------- plan, units, queries and K, or V
       const bool is_k = warp == kPxKWarp;
+      const uint32_t leader = elect_one();
       const uint64_t policy = evict_first_policy();
       const int nch = KEYS / p.R;              // boxes of one 64-column part of a tile
       const int oob = p.num_blocks * p.bs;
@@ -566,20 +626,18 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         return block >= 0 && block < p.num_blocks ? block * p.bs + (c - col * p.bs) : oob;
       };
       // One tile into the stage at position `at`: one thread issues the boxes.
-      auto load = [&](const CUtensorMap* map, const PxUnit& un, int row, unsigned at) {
+      auto load = [&](const CUtensorMap* map, int kv, int row, unsigned at) {
         const unsigned stage = at % STAGES;
         if (!warp_poll(empty0 + 8 * stage, ((at / STAGES) & 1) ^ 1, p.timeout_ns)) return false;
         const uint32_t bar = full0 + 8 * stage, dst = ring_s + stage * Shape::STAGE;
-        if (lane == 0) mbar_arrive_expect_tx(bar, Shape::STAGE);
+        expect_one(leader, bar, Shape::STAGE);
         if (lane == stage) held = 1 + ((at / STAGES) & 1);
         for (int c = 0; c < nch; ++c) {
           const int r = __shfl_sync(0xffffffffu, row, c);
-          if (lane == 0) {
 #pragma unroll
-            for (int part = 0; part < PARTS; ++part)
-              tma_load_3d(dst + part * KEYS * 128 + c * p.R * 128, map, 64 * part, un.kv, r, bar,
-                          policy);
-          }
+          for (int part = 0; part < PARTS; ++part)
+            tma_one_3d(leader, dst + part * KEYS * 128 + c * p.R * 128, map, 64 * part, kv, r, bar,
+                       policy);
         }
         return true;
       };
@@ -611,30 +669,28 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(uempty0 + 8 * seg);
         }
-        const int n = un.tiles;
+        const int n = uniform(un.tiles), kv = uniform(un.kv);
         if (n == 0) break;
         int row = row_of(un, 0);
         if (is_k) {
-          for (int i = 0; i <= un.pair && ok; ++i, ++fills) {
+          const int pair = uniform(un.pair), own = uniform(un.own), q0 = uniform(un.q0);
+          for (int i = 0; i <= pair && ok; ++i, ++fills) {
             const int buf = fills % Shape::QBUF;
             ok = warp_poll(qempty0 + 8 * buf, ((fills / Shape::QBUF) & 1) ^ 1, p.timeout_ns);
             if (!ok) break;
             const uint32_t bar = qfull0 + 8 * buf;
             if (lane == 16 + buf) held = 1 + ((fills / Shape::QBUF) & 1);
-            if (lane == 0) {
-              mbar_arrive_expect_tx(bar, (un.own ? p.G : p.TB * p.G) * 128 * PARTS);
+            expect_one(leader, bar, (own ? p.G : p.TB * p.G) * 128 * PARTS);
 #pragma unroll
-              for (int part = 0; part < PARTS; ++part)
-                tma_load_4d(qbuf_s + buf * Shape::QBYTES + part * 128 * 128,
-                            un.own ? &p.q_one_map : &p.q_tile_map, 64 * part, 0, un.kv,
-                            un.q0 + i * p.TB, bar, policy);
-            }
-            __syncwarp();
+            for (int part = 0; part < PARTS; ++part)
+              tma_one_4d(leader, qbuf_s + buf * Shape::QBYTES + part * 128 * 128,
+                         own ? &p.q_one_map : &p.q_tile_map, 64 * part, 0, kv, q0 + i * p.TB, bar,
+                         policy);
           }
         }
         for (int i = 0; i < n && ok; ++i) {
           const int ahead = row_of(un, i + 1);
-          ok = load(is_k ? &p.k_map : &p.v_map, un, row, base + (is_k ? k_pos(i) : v_pos(i, n)));
+          ok = load(is_k ? &p.k_map : &p.v_map, kv, row, base + (is_k ? k_pos(i) : v_pos(i, n)));
           row = ahead;
         }
         base += 2 * n;
@@ -650,15 +706,15 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       }
     } else if (aligned && warp == kPxMmaWarp) {
     // ------------------------------------------------------------ MMA issue
-    if (lane == 0) {
+      const uint32_t leader = elect_one();
       constexpr uint32_t qk_idesc = px_idesc<Tag>(KEYS, false), pv_idesc = px_idesc<Tag>(D, true);
       unsigned base = 0, fills = 0, done0 = 0, done1 = 0;   // stages, fills, tiles of each stream
       bool ok = true;
       for (unsigned unit_no = 0; ok; ++unit_no) {
         const int seg = unit_no % kPxSegs;
-        if (!(ok = mbar_poll(ufull0 + 8 * seg, (unit_no / kPxSegs) & 1, p.timeout_ns))) break;
-        const int n = units[seg].tiles, pair = units[seg].pair;
-        mbar_arrive(uempty0 + 8 * seg);
+        if (!(ok = warp_poll(ufull0 + 8 * seg, (unit_no / kPxSegs) & 1, p.timeout_ns))) break;
+        const int n = uniform(units[seg].tiles), pair = uniform(units[seg].pair);
+        if (lane == 0) mbar_arrive(uempty0 + 8 * seg);
         if (n == 0) break;
         const int n0 = NS == 1 || pair ? n : (n + 1) / 2, n1 = NS == 1 ? 0 : pair ? n : n / 2;
         auto tile_of = [&](int w, int j) { return NS == 1 || pair ? j : 2 * j + w; };
@@ -669,8 +725,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           const int i = tile_of(w, j);
           const unsigned at = base + k_pos(i), stage = at % STAGES;
           const unsigned fill = fills + (pair ? w : 0), buf = fill % Shape::QBUF;
-          if (j == 0) ok = ok && mbar_poll(qfull0 + 8 * buf, (fill / Shape::QBUF) & 1, p.timeout_ns);
-          ok = ok && mbar_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns);
+          if (j == 0) ok = ok && warp_poll(qfull0 + 8 * buf, (fill / Shape::QBUF) & 1, p.timeout_ns);
+          ok = ok && warp_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns);
           if (!ok) return;
           tc_fence_after();
           const unsigned no = (w ? done1 : done0) + j;
@@ -678,30 +734,30 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           const uint64_t b = smem_desc(ring_s + stage * Shape::STAGE, 16, 1024, 2);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_f16(s_of(w, no), a + (uint64_t)((kk / 4 * 128 * 128 + kk % 4 * 32) >> 4),
+            mma_ss(leader, s_of(w, no), a + (uint64_t)((kk / 4 * 128 * 128 + kk % 4 * 32) >> 4),
                     b + (uint64_t)((kk / 4 * KEYS * 128 + kk % 4 * 32) >> 4), qk_idesc, kk > 0);
-          if (!pair || w == 1) mma_commit(empty0 + 8 * stage);
-          if (pair ? j == n - 1 : i == n - 1) mma_commit(qempty0 + 8 * buf);
-          mma_commit(sfull0 + 8 * (NS == 2 ? w : no & 1));
+          if (!pair || w == 1) commit_one(leader, empty0 + 8 * stage);
+          if (pair ? j == n - 1 : i == n - 1) commit_one(leader, qempty0 + 8 * buf);
+          commit_one(leader, sfull0 + 8 * (NS == 2 ? w : no & 1));
         };
         auto pv = [&](int w, int j) {
           const int i = tile_of(w, j);
           const unsigned at = base + v_pos(i, n), stage = at % STAGES;
           const unsigned no = (w ? done1 : done0) + j;
-          ok = ok && mbar_poll(pfull0 + 8 * (NS == 2 ? w : no & 1), (NS == 2 ? no : no >> 1) & 1,
+          ok = ok && warp_poll(pfull0 + 8 * (NS == 2 ? w : no & 1), (NS == 2 ? no : no >> 1) & 1,
                                p.timeout_ns);
-          if (j == 0 && unit_no > 0) ok = ok && mbar_poll(ofree, (unit_no - 1) & 1, p.timeout_ns);
-          ok = ok && mbar_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns);
+          if (j == 0 && unit_no > 0) ok = ok && warp_poll(ofree, (unit_no - 1) & 1, p.timeout_ns);
+          ok = ok && warp_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns);
           if (!ok) return;
           tc_fence_after();
           const uint64_t b = smem_desc(ring_s + stage * Shape::STAGE, KEYS * 128, 1024, 2);
 #pragma unroll
           for (int kk = 0; kk < KEYS / 16; ++kk)
-            mma_f16_ta(tmem + Shape::O_COL0 + w * D, s_of(w, no) + 8 * kk,
+            mma_ts(leader, tmem + Shape::O_COL0 + w * D, s_of(w, no) + 8 * kk,
                        b + (uint64_t)(kk * (2048 >> 4)), pv_idesc, j > 0 || kk > 0);
-          if (!pair || w == 1) mma_commit(empty0 + 8 * stage);
-          if (NS == 1) mma_commit(pvdone);
-          if (j == (w ? n1 : n0) - 1) mma_commit(ofull0 + 8 * w);
+          if (!pair || w == 1) commit_one(leader, empty0 + 8 * stage);
+          if (NS == 1) commit_one(leader, pvdone);
+          if (j == (w ? n1 : n0) - 1) commit_one(leader, ofull0 + 8 * w);
         };
         if constexpr (NS == 1) {
           qk(0, 0);
@@ -727,12 +783,11 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         done1 += n1;
       }
       if (!ok) {
-        atomicOr(&p.head->status, kErrPxMma);
-        mma_commit(drain);
+        if (lane == 0) atomicOr(&p.head->status, kErrPxMma);
+        commit_one(leader, drain);
         mbar_wait(drain, 0, p.timeout_ns);
       }
-    }
-    __syncwarp();
+      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPxSoftmaxRegs));
