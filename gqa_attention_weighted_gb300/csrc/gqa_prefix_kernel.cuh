@@ -52,13 +52,12 @@ namespace gqa_av {
 constexpr int kPxThreads = 384;
 // Registers a thread: 168 at launch (65536 / 384, rounded down to 8); the last
 // warpgroup gives up enough of them for the softmax warpgroups' 128 scores a
-// thread: 2 * 128 * 200 + 128 * 104 = 384 * 168.
-constexpr int kPxSoftmaxRegs = 200, kPxAuxRegs = 104;
+// thread: 2 * 128 * 184 + 128 * 136 = 384 * 168.
+constexpr int kPxSoftmaxRegs = 184, kPxAuxRegs = 136;
 constexpr int kPxMmaWarp = 8, kPxKWarp = 9, kPxVWarp = 10;
 constexpr int kPxMaxGroups = 128;
 constexpr int kPxMaxB = 4096;
-constexpr int kPxSegs = 4;             // unit descriptors in flight
-constexpr int kPxMaxStages = 12;
+constexpr int kPxSegs = 2;             // unit descriptors in flight
 constexpr float kPxGrow = 8.0f;        // log2 of the growth of a maximum that is tolerated
 constexpr unsigned kErrPxLoad = 16u, kErrPxMma = 32u, kErrPxSoftmax = 64u;
 
@@ -72,7 +71,8 @@ struct PxShape {
   static constexpr int QBUF = NS;                      // query buffers
   static constexpr int STAGES = D == 64 ? 11 : 5;
   static constexpr int TILES_BYTES = QBUF * QBYTES + STAGES * STAGE;
-  static constexpr int SMEM = TILES_BYTES + 3072;
+  static constexpr int MISC = D == 64 ? 2048 : 1024;   // barriers, units, plan
+  static constexpr int SMEM = TILES_BYTES + MISC + 2048;
   static constexpr uint32_t S_COL = KEYS;              // tensor-memory columns of an S buffer
   static constexpr uint32_t O_COL0 = 256;
 };
@@ -242,6 +242,8 @@ __device__ __forceinline__ void add2(float& a, float& b, float x, float y) {
       : "f"(x), "f"(y));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
 // A wait by a whole warp; the lanes agree on whether it ran out, so that they
 // leave together.
 __device__ __forceinline__ bool warp_poll(uint32_t bar, uint32_t parity, long long timeout_ns) {
@@ -255,22 +257,35 @@ __device__ __forceinline__ void hold(float* v) {
   for (int i = 0; i < N; ++i) asm volatile("" : "+f"(v[i]));
 }
 
-// What the consumers of a unit need to know.
-struct PxUnit {
-  int tiles;          // key tiles; 0: no more units
-  int pair;           // two query tiles, each with all key tiles
-  int rows[2];        // rows of the query tiles
-  int q0;             // first sequence
-  int last_valid;     // keys of the last tile
-  int slot;           // its slot
-  int own;            // a sequence's own unit
-  int kv;             // KV head
-  int t0;             // first key tile
-  int len;            // rows that its table row lists
+// One run of key tiles: keys of one table row for one KV head.
+struct PxPart {
   const int32_t* table;
+  int len;            // rows that the table row lists
+  int t0, tiles;      // key tiles
+  int last_valid;     // keys of the last one
+  int kv;             // KV head
+  int q0;             // first sequence
+  int slot;
+};
+// What a CTA works on at a time.
+//   kSplit: one query tile; two streams take the even and the odd key tiles.
+//   kPair: two query tiles, a stream each, over the same key tiles.
+//   kOwn: own units of two (sequence, KV head, split)s, a stream each.
+enum { kSplit, kPair, kOwn };
+struct PxUnit {
+  PxPart part[2];     // kOwn: one for each stream; else the first
+  int rows[2];        // rows of the query tiles
+  int mode;
+  int own;            // a sequence's own keys
 };
 
-// Positions of a unit's K and V tiles in its run of 2 * tiles stages, in the
+// The tiles of a unit in the order of their use, i = 0 .. n - 1: tile j of
+// stream w when the streams take turns until the shorter one ends.
+__device__ __forceinline__ int turn(int w, int j, int n0, int n1) {
+  const int m = min(n0, n1);
+  return j < m ? 2 * j + w : m + j;
+}
+// Positions of tile i's K and V in the unit's run of 2 n stages, about the
 // order of their first use: K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
 __device__ __forceinline__ int k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ int v_pos(int i, int n) { return min(2 * i + 2, 2 * n - 1); }
@@ -285,23 +300,33 @@ __device__ __forceinline__ int warp_incl_sum(int x) {
   return x;
 }
 
-__device__ __forceinline__ int warp_max(int x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
+// x / y, y > 0. Below 2^21 in fp32: the quotient of x + 1/2 is at least 1/(2y)
+// from the next integer, further than its error.
+__device__ __forceinline__ int quick_div(int x, int y) {
+  if (static_cast<unsigned>(x) < (1u << 21))
+    return __float2int_rz(__fdividef(static_cast<float>(x) + 0.5f, static_cast<float>(y)));
+  return x / y;
 }
 
-// The plan, made by a whole warp from the lengths: lane l holds groups 32 j + l
-// and the unit sums of the blocks 32 j + l of 32 sequences. It stands at the
-// head of every call's critical path, so all lengths are loaded at once and
-// 64-bit and double arithmetic is kept out of it.
+// The sequences' own part of the plan, in shared memory.
+struct PxOwn {
+  int upto[kPxMaxB / 32];   // units of the blocks of 32 sequences up to each
+  int tiles;                // key tiles of a unit
+  int units;
+  float work;               // key tiles of the batch, times KV heads
+  int paired;               // units are taken two at a time
+};
+
+// The plan, made from the lengths by two warps at the head of every call, so
+// its loads go out together and slow arithmetic is kept out of it. The V warp
+// makes the own part; the K warp makes the groups' part, lane l holding groups
+// 32 j + l, and finds units by it.
 template <int D>
 struct PxPlan {
   using Shape = PxShape<D>;
   static constexpr int J = kPxMaxGroups / 32;
   int begin[J], end[J], len[J], tiles[J], splits[J], nq[J], pair[J], upto[J];
-  int prefix_units, own_tiles, own_units;
-  int own_upto[J];
+  int prefix_units;
 
   static __device__ __forceinline__ int own_len(const PrefixParams& p, int b) {
     const int cap = p.max_blocks * p.bs;
@@ -311,12 +336,69 @@ struct PxPlan {
     return len / Shape::KEYS + (len % Shape::KEYS != 0);
   }
 
-  __device__ __forceinline__ void make(const PrefixParams& p) {
+  // By the V warp. A unit takes so many tiles that a CTA gets about four, so
+  // that the last ones to end are short. The sums of a lane's tiles may pass
+  // 2^32 over the warp: added as two halves.
+  static __device__ __forceinline__ void make_own(const PrefixParams& p, PxOwn* own) {
     const int lane = threadIdx.x & 31;
-    const int n = gridDim.x;
+    const int blocks = p.max_blocks > 0 ? (p.B + 31) / 32 : 0;
+    constexpr int kKept = 8;          // blocks whose tiles stay in registers
+    int kept[kKept];
+    unsigned low = 0, high = 0;
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) kept[k] = k < blocks ? own_len(p, 32 * k + lane) : 0;
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+      kept[k] = tiles_of(kept[k]);
+      low += kept[k] & 4095;
+      high += kept[k] >> 12;
+    }
+#pragma unroll 4
+    for (int k = kKept; k < blocks; ++k) {
+      const int t = tiles_of(own_len(p, 32 * k + lane));
+      low += t & 4095;
+      high += t >> 12;
+    }
+    low = __reduce_add_sync(0xffffffffu, low);
+    high = __reduce_add_sync(0xffffffffu, high);
+    const unsigned long long all =
+        ((static_cast<unsigned long long>(high) << 12) + low) * static_cast<unsigned>(p.Hkv);
+    const int share = 4 * gridDim.x;
+    const int each = max(1, all < (1u << 30) ? quick_div(static_cast<int>(all) + share - 1, share)
+                                             : static_cast<int>((all + share - 1) / share));
+    int units = 0;
+    for (int k0 = 0; k0 < blocks; k0 += 32) {
+      int mine = 0;
+#pragma unroll
+      for (int k = 0; k < kKept; ++k)
+        if (k0 == 0 && k < blocks) {
+          const int sum = __reduce_add_sync(0xffffffffu, quick_div(kept[k] + each - 1, each));
+          if (k == lane) mine = sum * p.Hkv;
+        }
+      for (int k = max(k0, kKept); k < min(blocks, k0 + 32); ++k) {
+        const int t = tiles_of(own_len(p, 32 * k + lane));
+        const int sum = __reduce_add_sync(0xffffffffu, quick_div(t + each - 1, each));
+        if (k - k0 == lane) mine = sum * p.Hkv;
+      }
+      mine = units + warp_incl_sum(mine);
+      if (k0 + lane < kPxMaxB / 32) own->upto[k0 + lane] = mine;
+      units = __shfl_sync(0xffffffffu, mine, 31);
+    }
+    if (lane == 0) {
+      own->tiles = each;
+      own->units = units;
+      own->work = static_cast<float>(all);
+      own->paired = Shape::NS == 2 && units > static_cast<int>(gridDim.x);
+    }
+    __syncwarp();
+  }
+
+  // By the K warp: the groups' lengths, while the V warp reads the others.
+  __device__ __forceinline__ void load_groups(const PrefixParams& p) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      begin[j] = end[j] = len[j] = tiles[j] = splits[j] = pair[j] = upto[j] = own_upto[j] = 0;
+      begin[j] = end[j] = len[j] = tiles[j] = splits[j] = pair[j] = upto[j] = 0;
       nq[j] = 1;
       const int g = 32 * j + lane;
       if (32 * j < p.P && g < p.P) {
@@ -325,198 +407,167 @@ struct PxPlan {
         len[j] = min(max(p.prefix_lens[g], 0), p.max_pblocks * p.bs);
       }
     }
-    // Own tiles of the batch, and how many of them a unit takes: about four
-    // units a CTA, so that the last ones to end are short. A lane's tiles may
-    // be 2^24 a sequence: summed over the warp as two halves.
-    const int blocks = p.max_blocks > 0 ? (p.B + 31) / 32 : 0;
-    unsigned low = 0, high = 0;
-#pragma unroll 8
-    for (int k = 0; k < blocks; ++k) {
-      const unsigned t = tiles_of(own_len(p, 32 * k + lane));
-      low += t & 4095u;
-      high += t >> 12;
-    }
-    low = __reduce_add_sync(0xffffffffu, low);
-    high = __reduce_add_sync(0xffffffffu, high);
-    const unsigned long long own =
-        ((static_cast<unsigned long long>(high) << 12) + low) * static_cast<unsigned>(p.Hkv);
-    const unsigned share = 4u * n;
-    own_tiles = own < 0x40000000u
-                    ? static_cast<int>((static_cast<unsigned>(own) + share - 1) / share)
-                    : static_cast<int>((own + share - 1) / share);
-    own_tiles = max(own_tiles, 1);
-    // Groups: starts not below their predecessors, tiles, query tiles.
+  }
+  __device__ __forceinline__ int query_tiles(const PrefixParams& p, int j) const {
+    return quick_div(end[j] - begin[j] + p.TB - 1, p.TB);
+  }
+  __device__ __forceinline__ void make_groups(const PrefixParams& p, const PxOwn* own) {
+    const int lane = threadIdx.x & 31;
+    const int n = gridDim.x;
+    // Starts not below their predecessors; tiles; query tiles.
     int carry = 0, longest = 0;
-    float cost[2] = {0.0f, 0.0f};   // key tiles x query tiles, single and in pairs
-    int q[J];
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      q[j] = 0;
-      if (32 * j < p.P) {
-        int a = max(begin[j], carry);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, a, o);
-          if (lane >= o) a = max(a, y);
-        }
-        carry = __shfl_sync(0xffffffffu, a, 31);
-        begin[j] = a;
-        end[j] = max(a, end[j]);
-        q[j] = (end[j] - begin[j] + p.TB - 1) / p.TB;
-        tiles[j] = q[j] > 0 ? tiles_of(len[j]) : 0;
-        cost[0] += static_cast<float>(tiles[j]) * static_cast<float>(q[j]);
-        cost[1] += static_cast<float>(tiles[j]) * static_cast<float>((q[j] + 1) / 2);
-        longest = max(longest, tiles[j]);
-      }
-    }
-    longest = p.P > 0 ? warp_max(longest) : 0;
-    prefix_units = 0;
-    if (longest > 0) {
-      // How to cut the prefixes: each lane costs one choice of pairs or single
-      // tiles and of the tiles a split takes (1 to 8 units a CTA), from the
-      // time that the units take if all CTAs stay busy, own units included,
-      // and from the CTA with the most prefix units.
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        cost[0] += __shfl_xor_sync(0xffffffffu, cost[0], o);
-        cost[1] += __shfl_xor_sync(0xffffffffu, cost[1], o);
-      }
-      const bool pairs = Shape::NS == 2 && (lane & 1);
-      const float w = (pairs ? cost[1] : cost[0]) * static_cast<float>(p.Hkv);
-      int chunk = static_cast<int>(fminf(ceilf(w / static_cast<float>(((lane >> 2) + 1) * n)),
-                                         16777216.0f)) + ((lane >> 1) & 1);
-      if (lane >= 30) chunk = longest;   // no cut: always within the slots
-      chunk = max(1, min(chunk, longest));
-      int units = 0;                     // at most 2^13 tiles of 2^24 / chunk: see below
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-        for (int g = 32 * j; g < min(p.P, 32 * (j + 1)); ++g) {
-          const int t = __shfl_sync(0xffffffffu, tiles[j], g & 31);
-          const int m = __shfl_sync(0xffffffffu, q[j], g & 31);
-          const int more = (t + chunk - 1) / chunk;
-          const int wide = pairs ? (m + 1) / 2 : m;
-          // Past the slots the choice is dropped: no need to count on.
-          units = more > p.prefix_slots ? p.prefix_slots + 1
-                                        : min(units + more * wide, p.prefix_slots + 1);
-        }
-      const bool fits = static_cast<long long>(units) * p.Hkv <= p.prefix_slots;
-      units *= p.Hkv;
-      const float c = pairs ? p.c_pair : p.c_tile;
-      const float one = static_cast<float>(chunk) * c + p.c_unit;
-      const float all = (w * c + static_cast<float>(units) * p.c_unit +
-                         static_cast<float>(own) * p.c_own) / static_cast<float>(n);
-      const float est =
-          fits ? fmaxf(all, static_cast<float>((units + n - 1) / n) * one) : INFINITY;
-      // Costs are positive, so their bit patterns are ordered like them.
-      const unsigned best = __reduce_min_sync(0xffffffffu, __float_as_uint(est));
-      const int src = __ffs(__ballot_sync(0xffffffffu, __float_as_uint(est) == best)) - 1;
-      const int cut = __shfl_sync(0xffffffffu, chunk, src);
-      const bool use_pairs = Shape::NS == 2 && (src & 1);
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-        if (32 * j < p.P) {
-          splits[j] = (tiles[j] + cut - 1) / cut;
-          pair[j] = use_pairs && q[j] > 1;
-          nq[j] = max(1, pair[j] ? (q[j] + 1) / 2 : q[j]);
-          upto[j] = prefix_units + warp_incl_sum(nq[j] * splits[j] * p.Hkv);
-          prefix_units = __shfl_sync(0xffffffffu, upto[j], 31);
-        }
-    }
-    // Unit sums of the blocks of 32 sequences.
-    own_units = 0;
+    float cost0 = 0.0f, cost1 = 0.0f;   // key tiles x query tiles, single and in pairs
 #pragma unroll
     for (int j = 0; j < J; ++j)
-      if (32 * j < blocks) {
-#pragma unroll 8
-        for (int k = 32 * j; k < min(blocks, 32 * (j + 1)); ++k) {
-          const int t = tiles_of(own_len(p, 32 * k + lane));
-          const int sum = __reduce_add_sync(0xffffffffu, (t + own_tiles - 1) / own_tiles);
-          if ((k & 31) == lane) own_upto[j] = sum * p.Hkv;
+      if (32 * j < p.P) {
+        int a = max(begin[j], carry);
+        if (p.P > 1) {
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, a, o);
+            if (lane >= o) a = max(a, y);
+          }
+          carry = __shfl_sync(0xffffffffu, a, 31);
         }
-        own_upto[j] = own_units + warp_incl_sum(own_upto[j]);
-        own_units = __shfl_sync(0xffffffffu, own_upto[j], 31);
+        begin[j] = a;
+        end[j] = max(a, end[j]);
+        const int q = query_tiles(p, j);
+        tiles[j] = q > 0 ? tiles_of(len[j]) : 0;
+        cost0 += static_cast<float>(tiles[j]) * static_cast<float>(q);
+        cost1 += static_cast<float>(tiles[j]) * static_cast<float>((q + 1) / 2);
+        longest = max(longest, tiles[j]);
+      }
+    prefix_units = 0;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (longest == 0) return;
+    // How to cut the prefixes: each lane costs one choice of pairs or single
+    // query tiles and of the key tiles a split takes (1 to 8 units a CTA), from
+    // the time that the units take if all CTAs stay busy, own units included,
+    // and from the CTA with the most prefix units.
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      cost0 += __shfl_xor_sync(0xffffffffu, cost0, o);
+      cost1 += __shfl_xor_sync(0xffffffffu, cost1, o);
+    }
+    const bool pairs = Shape::NS == 2 && (lane & 1);
+    const float w = (pairs ? cost1 : cost0) * static_cast<float>(p.Hkv);
+    const float per = __fdividef(w, static_cast<float>(((lane >> 2) + 1) * n));
+    int chunk = static_cast<int>(fminf(ceilf(per), 16777216.0f)) + ((lane >> 1) & 1);
+    if (lane >= 30) chunk = longest;   // no cut: always within the slots
+    chunk = max(1, min(chunk, longest));
+    int units = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (32 * j < p.P) {
+        const int q_mine = query_tiles(p, j);
+        for (int g = 0; g < min(p.P - 32 * j, 32); ++g) {
+          const int t = __shfl_sync(0xffffffffu, tiles[j], g);
+          const int q = __shfl_sync(0xffffffffu, q_mine, g);
+          const int more = quick_div(t + chunk - 1, chunk);
+          // A choice past the slots is dropped: no need to count on.
+          units = more > p.prefix_slots
+                      ? p.prefix_slots + 1
+                      : min(units + more * (pairs ? (q + 1) / 2 : q), p.prefix_slots + 1);
+        }
+      }
+    const bool fits = static_cast<long long>(units) * p.Hkv <= p.prefix_slots;
+    units *= p.Hkv;
+    const float c = pairs ? p.c_pair : p.c_tile;
+    const float one = static_cast<float>(chunk) * c + p.c_unit;
+    const float all = __fdividef(w * c + static_cast<float>(units) * p.c_unit + own->work * p.c_own,
+                                 static_cast<float>(n));
+    const float est =
+        fits ? fmaxf(all, static_cast<float>(quick_div(units + n - 1, n)) * one) : INFINITY;
+    // Costs are positive, so their bit patterns are ordered like them.
+    const unsigned best = __reduce_min_sync(0xffffffffu, __float_as_uint(est));
+    const int src = __ffs(__ballot_sync(0xffffffffu, __float_as_uint(est) == best)) - 1;
+    const int cut = __shfl_sync(0xffffffffu, chunk, src);
+    const bool use_pairs = Shape::NS == 2 && (src & 1);
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+      if (32 * j < p.P) {
+        const int q = query_tiles(p, j);
+        splits[j] = quick_div(tiles[j] + cut - 1, cut);
+        pair[j] = use_pairs && q > 1;
+        nq[j] = max(1, pair[j] ? (q + 1) / 2 : q);
+        upto[j] = prefix_units + warp_incl_sum(nq[j] * splits[j] * p.Hkv);
+        prefix_units = __shfl_sync(0xffffffffu, upto[j], 31);
       }
   }
 
-  // Part `i` of t tiles cut into s equal parts (the first t % s one longer).
-  static __device__ __forceinline__ void cut_out(PxUnit& w, int i, int t, int s) {
-    const int each = t / s, more = t - each * s;
+  // Part i of t tiles cut into s equal parts (the first t % s one longer).
+  static __device__ __forceinline__ void cut_out(PxPart& w, int i, int t, int s) {
+    const int each = quick_div(t, s), more = t - each * s;
     w.t0 = i * each + min(i, more);
     w.tiles = each + (i < more);
     w.last_valid = i == s - 1 ? w.len - (t - 1) * Shape::KEYS : Shape::KEYS;
   }
-  // Unit u. A prefix unit counts (KV head, split, query tile), tiles fastest;
-  // an own one (sequence, KV head, split).
-  __device__ __forceinline__ PxUnit find(const PrefixParams& p, int u) const {
-    const int lane = threadIdx.x & 31;
-    PxUnit w;
-    w.own = u >= prefix_units;
-    w.rows[0] = p.G;
-    w.rows[1] = 0;
-    w.pair = 0;
-    if (!w.own) {
-      bool found = false;
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        if (32 * j < p.P && !found) {
-          const unsigned hit = __ballot_sync(0xffffffffu, u < upto[j]);
-          if (hit) {
-            found = true;
-            const int src = __ffs(hit) - 1;
-            const int a = __shfl_sync(0xffffffffu, begin[j], src);
-            const int e = __shfl_sync(0xffffffffu, end[j], src);
-            const int t = __shfl_sync(0xffffffffu, tiles[j], src);
-            const int s = __shfl_sync(0xffffffffu, splits[j], src);
-            const int q = __shfl_sync(0xffffffffu, nq[j], src);
-            const int pr = __shfl_sync(0xffffffffu, pair[j], src);
-            w.len = __shfl_sync(0xffffffffu, len[j], src);
-            const int local = u - (__shfl_sync(0xffffffffu, upto[j], src) - q * s * p.Hkv);
-            const int outer = local / q, i = local - outer * q;
-            w.kv = outer / s;
-            cut_out(w, outer - w.kv * s, t, s);
-            w.q0 = a + i * (pr ? 2 : 1) * p.TB;
-            w.rows[0] = min(p.TB, e - w.q0) * p.G;
-            w.rows[1] = pr ? max(0, min(p.TB, e - w.q0 - p.TB)) * p.G : 0;
-            w.pair = w.rows[1] > 0;
-            w.slot = u;
-            w.table = p.prefix_table + static_cast<size_t>(32 * j + src) * p.max_pblocks;
-          }
-        }
-      }
-      return w;
-    }
-    const int v = u - prefix_units;
-    int block = 0, before = 0;
+  // Prefix unit u: counted (group, KV head, split, query tile), tiles fastest.
+  __device__ __forceinline__ void find_prefix(const PrefixParams& p, int u, PxUnit& un) const {
+    PxPart& w = un.part[0];
+    un.own = 0;
+    un.part[1].tiles = 0;
     bool found = false;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      if (!found) {
-        const unsigned hit = __ballot_sync(0xffffffffu, v < own_upto[j]);
-        const int at = hit ? __ffs(hit) - 2 : 31;
-        if (at >= 0) before = __shfl_sync(0xffffffffu, own_upto[j], at);
-        block = 32 * j + at + 1;
-        found = hit != 0;
+      if (32 * j < p.P && !found) {
+        const unsigned hit = __ballot_sync(0xffffffffu, u < upto[j]);
+        if (hit) {
+          found = true;
+          const int src = __ffs(hit) - 1;
+          const int a = __shfl_sync(0xffffffffu, begin[j], src);
+          const int e = __shfl_sync(0xffffffffu, end[j], src);
+          const int t = __shfl_sync(0xffffffffu, tiles[j], src);
+          const int s = __shfl_sync(0xffffffffu, splits[j], src);
+          const int q = __shfl_sync(0xffffffffu, nq[j], src);
+          const int pr = __shfl_sync(0xffffffffu, pair[j], src);
+          w.len = __shfl_sync(0xffffffffu, len[j], src);
+          const int local = u - (__shfl_sync(0xffffffffu, upto[j], src) - q * s * p.Hkv);
+          const int outer = quick_div(local, q), i = local - outer * q;
+          w.kv = quick_div(outer, s);
+          cut_out(w, outer - w.kv * s, t, s);
+          w.q0 = a + i * (pr ? 2 : 1) * p.TB;
+          un.rows[0] = min(p.TB, e - w.q0) * p.G;
+          un.rows[1] = pr ? max(0, min(p.TB, e - w.q0 - p.TB)) * p.G : 0;
+          un.mode = un.rows[1] > 0 ? kPair : kSplit;
+          w.slot = u;
+          w.table = p.prefix_table + static_cast<size_t>(32 * j + src) * p.max_pblocks;
+        }
       }
     }
+  }
+  // Own unit v: counted (sequence, KV head, split).
+  static __device__ __forceinline__ void find_own(const PrefixParams& p, const PxOwn* own, int v,
+                                                  PxPart& w) {
+    const int lane = threadIdx.x & 31;
+    int block = 0, before = 0;
+    for (int k0 = 0;; k0 += 32) {
+      const int upto = own->upto[k0 + lane];
+      const unsigned hit = __ballot_sync(0xffffffffu, v < upto);
+      const int at = hit ? __ffs(hit) - 2 : 31;
+      if (at >= 0) before = __shfl_sync(0xffffffffu, upto, at);
+      block = k0 + at + 1;
+      if (hit || k0 + 32 >= kPxMaxB / 32) break;
+    }
     const int my_len = own_len(p, 32 * block + lane);
-    const int my_splits = (tiles_of(my_len) + own_tiles - 1) / own_tiles;
+    const int my_splits = quick_div(tiles_of(my_len) + own->tiles - 1, own->tiles);
     const int incl = warp_incl_sum(my_splits * p.Hkv);
     const int src = __ffs(__ballot_sync(0xffffffffu, v - before < incl) | 0x80000000u) - 1;
     const int s = max(1, __shfl_sync(0xffffffffu, my_splits, src));
     w.len = __shfl_sync(0xffffffffu, my_len, src);
     const int local = v - before - (__shfl_sync(0xffffffffu, incl, src) - s * p.Hkv);
-    w.kv = local / s;
+    w.kv = quick_div(local, s);
     cut_out(w, local - w.kv * s, tiles_of(w.len), s);
     w.q0 = 32 * block + src;
     w.slot = v;
     w.table = p.block_table + static_cast<size_t>(w.q0) * p.max_blocks;
-    return w;
   }
 
-  // For the combine kernel (one warp of one CTA).
-  __device__ __forceinline__ void write(const PrefixParams& p) const {
+  // For the combine kernel (the K warp of one CTA).
+  __device__ __forceinline__ void write(const PrefixParams& p, const PxOwn* own) const {
     const int lane = threadIdx.x & 31;
-    if (lane == 0) p.head->own_tiles = own_tiles;
+    const int each = own->tiles;
+    if (lane == 0) p.head->own_tiles = each;
 #pragma unroll
     for (int j = 0; j < J; ++j)
       if (32 * j + lane < p.P)
@@ -525,7 +576,7 @@ struct PxPlan {
     int base = 0;
     if (p.max_blocks > 0)
       for (int k = 0; 32 * k < p.B; ++k) {
-        const int n = (tiles_of(own_len(p, 32 * k + lane)) + own_tiles - 1) / own_tiles * p.Hkv;
+        const int n = quick_div(tiles_of(own_len(p, 32 * k + lane)) + each - 1, each) * p.Hkv;
         const int incl = warp_incl_sum(n);
         if (32 * k + lane < p.B) p.head->own_base[32 * k + lane] = base + incl - n;
         base += __shfl_sync(0xffffffffu, incl, 31);
@@ -547,17 +598,19 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Shape::TILES_BYTES);
-  const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * kPxMaxStages;
-  const uint32_t qfull0 = empty0 + 8 * kPxMaxStages, qempty0 = qfull0 + 16;
+  const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * STAGES;
+  const uint32_t qfull0 = empty0 + 8 * STAGES, qempty0 = qfull0 + 16;
   const uint32_t sfull0 = qempty0 + 16, pfull0 = sfull0 + 16;   // a stream's, or an S buffer's
-  const uint32_t ofull0 = pfull0 + 16, ofree = ofull0 + 16, pvdone = ofree + 8;
+  const uint32_t ofull0 = pfull0 + 16, ofree0 = ofull0 + 16, pvdone = ofree0 + 16;
   const uint32_t meet = pvdone + 8, drain = meet + 8;
   const uint32_t ufull0 = drain + 8, uempty0 = ufull0 + 8 * kPxSegs;
-  constexpr int kBars = 2 * kPxMaxStages + 15 + 2 * kPxSegs;
+  constexpr int kBars = 2 * STAGES + 15 + 2 * kPxSegs;
   PxUnit* units = reinterpret_cast<PxUnit*>(bars + kBars);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(units + kPxSegs);
-  float2* ml = reinterpret_cast<float2*>(smem + Shape::TILES_BYTES + 1024);   // [2][128]
-  static_assert(8 * kBars + sizeof(PxUnit) * kPxSegs + 4 <= 1024, "misc shared memory");
+  PxOwn* own_plan = reinterpret_cast<PxOwn*>(units + kPxSegs);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(own_plan + 1);
+  float2* ml = reinterpret_cast<float2*>(smem + Shape::TILES_BYTES + Shape::MISC);   // [2][128]
+  static_assert(8 * kBars + sizeof(PxUnit) * kPxSegs + sizeof(PxOwn) + 4 <= Shape::MISC,
+                "shared memory besides the tiles");
 
   if (warp == kPxMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -577,8 +630,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       mbar_init(sfull0 + 8 * i, 1);
       mbar_init(pfull0 + 8 * i, 4);
       mbar_init(ofull0 + 8 * i, 1);
+      mbar_init(ofree0 + 8 * i, 8);
     }
-    mbar_init(ofree, 8);
     mbar_init(pvdone, 1);
     mbar_init(meet, 8);
     mbar_init(drain, 1);
@@ -602,11 +655,14 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   grid_launch_dependents();
   const bool aligned = (base_s & 1023u) == 0;   // the tiles need it; dynamic memory starts so
   if (!aligned && threadIdx.x == 0) atomicOr(&p.head->status, kErrPxLoad);
+  // kOwn: the second stream's rows lie in lanes of other warps than the first's
+  // where they fit, so that the two softmax warps sit on different schedulers.
+  const int own_shift = p.G <= 32 ? 32 : p.G <= 64 ? 64 : 0;
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPxAuxRegs));
     if (aligned && (warp == kPxKWarp || warp == kPxVWarp)) {
-    // ------------------------------------- plan, units, queries and K, or V
+      // ----------------------------------- plan, units, queries and K, or V
       const bool is_k = warp == kPxKWarp;
       const uint32_t leader = elect_one();
       const uint64_t policy = evict_first_policy();
@@ -617,86 +673,114 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       // lane 16 + s: into query buffer s.
       unsigned held = 0;
       bool ok = true;
-      // The pool row of this lane's box of tile i; rows past the length and
-      // entries outside the pool read zeros.
-      auto row_of = [&](const PxUnit& un, int i) {
-        const int c = (un.t0 + i) * KEYS + lane * p.R;
-        if (lane >= nch || i >= un.tiles || c >= un.len) return oob;
-        const int col = c / p.bs, block = un.table[col];
-        return block >= 0 && block < p.num_blocks ? block * p.bs + (c - col * p.bs) : oob;
-      };
-      // One tile into the stage at position `at`: one thread issues the boxes.
-      auto load = [&](const CUtensorMap* map, int kv, int row, unsigned at) {
-        const unsigned stage = at % STAGES;
-        if (!warp_poll(empty0 + 8 * stage, ((at / STAGES) & 1) ^ 1, p.timeout_ns)) return false;
-        const uint32_t bar = full0 + 8 * stage, dst = ring_s + stage * Shape::STAGE;
-        expect_one(leader, bar, Shape::STAGE);
-        if (lane == stage) held = 1 + ((at / STAGES) & 1);
-        for (int c = 0; c < nch; ++c) {
-          const int r = __shfl_sync(0xffffffffu, row, c);
-#pragma unroll
-          for (int part = 0; part < PARTS; ++part)
-            tma_one_3d(leader, dst + part * KEYS * 128 + c * p.R * 128, map, 64 * part, kv, r, bar,
-                       policy);
-        }
-        return true;
-      };
       PxPlan<D> plan;
-      int u = blockIdx.x, total = 0;
+      int u = blockIdx.x, prefix_units = 0, total = 0;
       if (is_k) {
-        plan.make(p);
-        total = plan.prefix_units + plan.own_units;
+        plan.load_groups(p);
+        named_sync(1, 64);
+        plan.make_groups(p, own_plan);
+        prefix_units = uniform(plan.prefix_units);
+        total = prefix_units + (own_plan->paired ? (own_plan->units + 1) / 2 : own_plan->units);
+      } else {
+        PxPlan<D>::make_own(p, own_plan);
+        named_sync(1, 64);
       }
       for (unsigned unit_no = 0; ok; ++unit_no) {
         const int seg = unit_no % kPxSegs;
-        PxUnit un;
+        PxUnit& un = units[seg];
         int next = 0;
         if (is_k) {
-          un.tiles = 0;
-          if (u < total) {
-            un = plan.find(p, u);
-            if (lane == 0) next = atomicAdd(&p.head->next, 1) + gridDim.x;
-          }
           if (!(ok = warp_poll(uempty0 + 8 * seg, ((unit_no / kPxSegs) & 1) ^ 1, p.timeout_ns))) break;
+          PxUnit made;
+          made.part[0].tiles = made.part[1].tiles = 0;
+          if (u < total) {
+            if (lane == 0) next = atomicAdd(&p.head->next, 1) + gridDim.x;
+            if (u < prefix_units) {
+              plan.find_prefix(p, u, made);
+            } else {
+              const int twice = own_plan->paired;
+              const int v = (u - prefix_units) << twice;
+              made.own = 1;
+              made.mode = twice ? kOwn : kSplit;
+              made.rows[0] = made.rows[1] = p.G;
+              for (int i = 0; i <= twice; ++i)
+                if (v + i < own_plan->units) {
+                  PxPart w;
+                  PxPlan<D>::find_own(p, own_plan, v + i, w);
+                  if (i == 0) made.part[0] = w;
+                  else made.part[1] = w;
+                }
+            }
+          }
           if (lane == 0) {
-            units[seg] = un;
+            un = made;
             mbar_arrive(ufull0 + 8 * seg);
           }
           __syncwarp();
         } else {
           if (!(ok = warp_poll(ufull0 + 8 * seg, (unit_no / kPxSegs) & 1, p.timeout_ns))) break;
-          un = units[seg];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(uempty0 + 8 * seg);
         }
-        const int n = uniform(un.tiles), kv = uniform(un.kv);
-        if (n == 0) break;
-        int row = row_of(un, 0);
+        const PxPart part0 = un.part[0], part1 = un.part[1];
+        const int mode = uniform(un.mode), own = uniform(un.own);
+        __syncwarp();
+        if (!is_k && lane == 0) mbar_arrive(uempty0 + 8 * seg);
+        const int n0 = uniform(part0.tiles), n1 = mode == kOwn ? uniform(part1.tiles) : 0;
+        const int n = n0 + n1;
+        if (n0 == 0) break;
+        const int kv0 = uniform(part0.kv), kv1 = uniform(part1.kv);
+        const int both = 2 * min(n0, n1);      // tiles during which the streams take turns
+        // Which part tile i of the unit's order is of, and the pool row of this
+        // lane's box of it; rows past the length and entries outside the pool
+        // read zeros.
+        auto of_second = [&](int i) { return i < both ? i & 1 : n1 > n0; };
+        auto row_of = [&](int i) {
+          const bool second = of_second(i);
+          const int tile = i < both ? i >> 1 : i - both / 2;
+          const int c = ((second ? part1.t0 : part0.t0) + tile) * KEYS + lane * p.R;
+          if (lane >= nch || i >= n || c >= (second ? part1.len : part0.len)) return oob;
+          const int col = quick_div(c, p.bs), block = (second ? part1.table : part0.table)[col];
+          return block >= 0 && block < p.num_blocks ? block * p.bs + (c - col * p.bs) : oob;
+        };
+        int row = row_of(0);
         if (is_k) {
-          const int pair = uniform(un.pair), own = uniform(un.own), q0 = uniform(un.q0);
-          for (int i = 0; i <= pair && ok; ++i, ++fills) {
+          const int q0 = uniform(part0.q0), q1 = mode == kPair ? q0 + p.TB : uniform(part1.q0);
+          const int more = mode == kPair || n1 > 0;
+          for (int i = 0; i <= more && ok; ++i, ++fills) {
             const int buf = fills % Shape::QBUF;
             ok = warp_poll(qempty0 + 8 * buf, ((fills / Shape::QBUF) & 1) ^ 1, p.timeout_ns);
             if (!ok) break;
             const uint32_t bar = qfull0 + 8 * buf;
             if (lane == 16 + buf) held = 1 + ((fills / Shape::QBUF) & 1);
             expect_one(leader, bar, (own ? p.G : p.TB * p.G) * 128 * PARTS);
+            const uint32_t dst = qbuf_s + buf * Shape::QBYTES + (mode == kOwn && i ? own_shift * 128 : 0);
 #pragma unroll
             for (int part = 0; part < PARTS; ++part)
-              tma_one_4d(leader, qbuf_s + buf * Shape::QBYTES + part * 128 * 128,
-                         own ? &p.q_one_map : &p.q_tile_map, 64 * part, 0, kv, q0 + i * p.TB, bar,
-                         policy);
+              tma_one_4d(leader, dst + part * 128 * 128, own ? &p.q_one_map : &p.q_tile_map,
+                         64 * part, 0, mode == kOwn && i ? kv1 : kv0, i ? q1 : q0, bar, policy);
           }
         }
+        const CUtensorMap* map = is_k ? &p.k_map : &p.v_map;
         for (int i = 0; i < n && ok; ++i) {
-          const int ahead = row_of(un, i + 1);
-          ok = load(is_k ? &p.k_map : &p.v_map, kv, row, base + (is_k ? k_pos(i) : v_pos(i, n)));
+          const int ahead = row_of(i + 1);
+          const unsigned at = base + (is_k ? k_pos(i) : v_pos(i, n)), stage = at % STAGES;
+          if (!(ok = warp_poll(empty0 + 8 * stage, ((at / STAGES) & 1) ^ 1, p.timeout_ns))) break;
+          const uint32_t bar = full0 + 8 * stage, dst = ring_s + stage * Shape::STAGE;
+          const int kv = of_second(i) ? kv1 : kv0;
+          expect_one(leader, bar, Shape::STAGE);
+          if (lane == stage) held = 1 + ((at / STAGES) & 1);
+          for (int c = 0; c < nch; ++c) {
+            const int r = __shfl_sync(0xffffffffu, row, c);
+#pragma unroll
+            for (int part = 0; part < PARTS; ++part)
+              tma_one_3d(leader, dst + part * KEYS * 128 + c * p.R * 128, map, 64 * part, kv, r, bar,
+                         policy);
+          }
           row = ahead;
         }
         base += 2 * n;
         u = __shfl_sync(0xffffffffu, next, 0);
       }
-      if (is_k && blockIdx.x == gridDim.x - 1) plan.write(p);
+      if (is_k && blockIdx.x == gridDim.x - 1) plan.write(p, own_plan);
       if (!ok) {
         // This warp's copies in flight land before the CTA leaves.
         if (lane == 0) atomicOr(&p.head->status, kErrPxLoad);
@@ -705,26 +789,31 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         __syncwarp();
       }
     } else if (aligned && warp == kPxMmaWarp) {
-    // ------------------------------------------------------------ MMA issue
+      // ---------------------------------------------------------- MMA issue
       const uint32_t leader = elect_one();
       constexpr uint32_t qk_idesc = px_idesc<Tag>(KEYS, false), pv_idesc = px_idesc<Tag>(D, true);
       unsigned base = 0, fills = 0, done0 = 0, done1 = 0;   // stages, fills, tiles of each stream
-      bool ok = true;
+      // The softmax warps have run through their code once (below).
+      bool ok = warp_poll(ofree0, 0, p.timeout_ns) && warp_poll(ofree0 + 8, 0, p.timeout_ns);
       for (unsigned unit_no = 0; ok; ++unit_no) {
         const int seg = unit_no % kPxSegs;
         if (!(ok = warp_poll(ufull0 + 8 * seg, (unit_no / kPxSegs) & 1, p.timeout_ns))) break;
-        const int n = uniform(units[seg].tiles), pair = uniform(units[seg].pair);
+        const int mode = uniform(units[seg].mode);
+        const int t0 = uniform(units[seg].part[0].tiles), t1 = uniform(units[seg].part[1].tiles);
+        __syncwarp();
         if (lane == 0) mbar_arrive(uempty0 + 8 * seg);
-        if (n == 0) break;
-        const int n0 = NS == 1 || pair ? n : (n + 1) / 2, n1 = NS == 1 ? 0 : pair ? n : n / 2;
-        auto tile_of = [&](int w, int j) { return NS == 1 || pair ? j : 2 * j + w; };
+        if (t0 == 0) break;
+        const int n0 = NS == 1 || mode != kSplit ? t0 : (t0 + 1) / 2;
+        const int n1 = NS == 1 ? 0 : mode == kSplit ? t0 / 2 : mode == kPair ? t0 : t1;
+        const int n = mode == kPair ? t0 : n0 + n1;
+        auto tile_of = [&](int w, int j) { return NS == 1 || mode == kPair ? j : turn(w, j, n0, n1); };
         auto s_of = [&](int w, unsigned tile_no) {
           return tmem + Shape::S_COL * (NS == 2 ? w : tile_no & 1);
         };
         auto qk = [&](int w, int j) {
           const int i = tile_of(w, j);
           const unsigned at = base + k_pos(i), stage = at % STAGES;
-          const unsigned fill = fills + (pair ? w : 0), buf = fill % Shape::QBUF;
+          const unsigned fill = fills + (mode != kSplit ? w : 0), buf = fill % Shape::QBUF;
           if (j == 0) ok = ok && warp_poll(qfull0 + 8 * buf, (fill / Shape::QBUF) & 1, p.timeout_ns);
           ok = ok && warp_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns);
           if (!ok) return;
@@ -735,9 +824,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
             mma_ss(leader, s_of(w, no), a + (uint64_t)((kk / 4 * 128 * 128 + kk % 4 * 32) >> 4),
-                    b + (uint64_t)((kk / 4 * KEYS * 128 + kk % 4 * 32) >> 4), qk_idesc, kk > 0);
-          if (!pair || w == 1) commit_one(leader, empty0 + 8 * stage);
-          if (pair ? j == n - 1 : i == n - 1) commit_one(leader, qempty0 + 8 * buf);
+                   b + (uint64_t)((kk / 4 * KEYS * 128 + kk % 4 * 32) >> 4), qk_idesc, kk > 0);
+          if (mode != kPair || w == 1) commit_one(leader, empty0 + 8 * stage);
+          if (mode == kSplit ? i == n - 1 : j == (w ? n1 : n0) - 1)
+            commit_one(leader, qempty0 + 8 * buf);
           commit_one(leader, sfull0 + 8 * (NS == 2 ? w : no & 1));
         };
         auto pv = [&](int w, int j) {
@@ -746,7 +836,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           const unsigned no = (w ? done1 : done0) + j;
           ok = ok && warp_poll(pfull0 + 8 * (NS == 2 ? w : no & 1), (NS == 2 ? no : no >> 1) & 1,
                                p.timeout_ns);
-          if (j == 0 && unit_no > 0) ok = ok && warp_poll(ofree, (unit_no - 1) & 1, p.timeout_ns);
+          if (j == 0) ok = ok && warp_poll(ofree0 + 8 * w, unit_no & 1, p.timeout_ns);
           ok = ok && warp_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns);
           if (!ok) return;
           tc_fence_after();
@@ -754,8 +844,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < KEYS / 16; ++kk)
             mma_ts(leader, tmem + Shape::O_COL0 + w * D, s_of(w, no) + 8 * kk,
-                       b + (uint64_t)(kk * (2048 >> 4)), pv_idesc, j > 0 || kk > 0);
-          if (!pair || w == 1) commit_one(leader, empty0 + 8 * stage);
+                   b + (uint64_t)(kk * (2048 >> 4)), pv_idesc, j > 0 || kk > 0);
+          if (mode != kPair || w == 1) commit_one(leader, empty0 + 8 * stage);
           if (NS == 1) commit_one(leader, pvdone);
           if (j == (w ? n1 : n0) - 1) commit_one(leader, ofull0 + 8 * w);
         };
@@ -766,11 +856,15 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             pv(0, j);
           }
         } else {
+          // Every unit's phase of both ofree barriers is waited for, here or by pv.
+          if (n1 == 0) ok = warp_poll(ofree0 + 8, unit_no & 1, p.timeout_ns);
           qk(0, 0);
           if (n1 > 0) qk(1, 0);
-          for (int j = 0; j < n0 && ok; ++j) {
-            pv(0, j);
-            if (j + 1 < n0) qk(0, j + 1);
+          for (int j = 0; j < max(n0, n1) && ok; ++j) {
+            if (j < n0) {
+              pv(0, j);
+              if (j + 1 < n0) qk(0, j + 1);
+            }
             if (j < n1) {
               pv(1, j);
               if (j + 1 < n1) qk(1, j + 1);
@@ -778,7 +872,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           }
         }
         base += 2 * n;
-        fills += 1 + pair;
+        fills += mode == kSplit ? 1 : 1 + (n1 > 0);
         done0 += n0;
         done1 += n1;
       }
@@ -793,43 +887,59 @@ __global__ void __launch_bounds__(kPxThreads, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPxSoftmaxRegs));
     // ------------------------------------------------- softmax, units' ends
     const int w = warp >> 2;                  // stream
-    const int r = threadIdx.x & 127;          // row of the query tile, tensor-memory lane
+    const int r = threadIdx.x & 127;          // tensor-memory lane
     const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     unsigned base = 0, done = 0, ends0 = 0, ends1 = 0, meets = 0;
     bool ok = aligned;
-    for (unsigned unit_no = 0; ok; ++unit_no) {
+    // The first round takes no unit: one key tile of whatever lies in S, run
+    // through while the plan is made, so that the instructions are in the
+    // caches when the first scores arrive (2 us less for them, measured). Its
+    // weights go to S, which no product has written yet: the MMA warp waits
+    // for all warps' ofree of this round before its first one.
+    for (unsigned round = 0; ok; ++round) {
+      const bool dry = round == 0;
+      const unsigned unit_no = round - 1;
       const int seg = unit_no % kPxSegs;
-      if (!(ok = warp_poll(ufull0 + 8 * seg, (unit_no / kPxSegs) & 1, p.timeout_ns))) break;
-      PxUnit un;
-      un.tiles = units[seg].tiles;
-      un.pair = units[seg].pair;
-      un.last_valid = units[seg].last_valid;
-      un.slot = units[seg].slot;
-      un.own = units[seg].own;
-      const int rows = units[seg].rows[un.pair && w == 1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(uempty0 + 8 * seg);
-      const int n = un.tiles;
-      if (n == 0) break;
-      const int n0 = NS == 1 || un.pair ? n : (n + 1) / 2, n1 = NS == 1 ? 0 : un.pair ? n : n / 2;
+      if (!dry && !(ok = warp_poll(ufull0 + 8 * seg, (unit_no / kPxSegs) & 1, p.timeout_ns))) break;
+      const PxUnit& un = units[seg];
+      int mode = kOwn, t0 = 1, t1 = 1, rows = 128, slot = 0, own = 1, last_valid = KEYS;
+      if (!dry) {
+        mode = un.mode;
+        t0 = un.part[0].tiles;
+        t1 = un.part[1].tiles;
+        const int mine = mode == kOwn ? w : 0;
+        rows = un.rows[mode == kPair ? w : 0];
+        slot = un.part[mine].slot;
+        last_valid = un.part[mine].last_valid;
+        own = un.own;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(uempty0 + 8 * seg);
+        if (t0 == 0) break;
+      }
+      const int n0 = NS == 1 || mode != kSplit ? t0 : (t0 + 1) / 2;
+      const int n1 = NS == 1 ? 0 : mode == kSplit ? t0 / 2 : mode == kPair ? t0 : t1;
+      const int n = mode == kPair ? t0 : n0 + n1;
       const int mine = w ? n1 : n0;
-      const bool active = 32 * (warp & 3) < rows;   // warps without rows only keep step
+      const int row = r - (mode == kOwn && w && !dry ? own_shift : 0);   // of the query tile
+      // Warps without rows only keep step.
+      const bool active = __any_sync(0xffffffffu, row >= 0 && row < rows);
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < mine; ++j) {
         const unsigned no = done + j;
         const int sb = NS == 2 ? w : no & 1;
-        if (!(ok = warp_poll(sfull0 + 8 * sb, (NS == 2 ? no : no >> 1) & 1, p.timeout_ns))) break;
+        if (!dry && !(ok = warp_poll(sfull0 + 8 * sb, (NS == 2 ? no : no >> 1) & 1, p.timeout_ns)))
+          break;
         tc_fence_after();
-        const int i = NS == 1 || un.pair ? j : 2 * j + w;
-        const int valid = i == n - 1 ? un.last_valid : KEYS;
-        if (valid < KEYS && (w == 0 || !un.pair)) {
+        const int i = NS == 1 || mode == kPair ? j : turn(w, j, n0, n1);
+        const int valid = (mode == kSplit ? i == n - 1 : j == mine - 1) ? last_valid : KEYS;
+        if (valid < KEYS && (mode != kPair || w == 0)) {
           // V rows past the length may hold NaN: zeroed before the product.
           const unsigned at = base + v_pos(i, n), stage = at % STAGES;
           if (!(ok = warp_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns))) break;
           uint8_t* v = smem + Shape::QBUF * Shape::QBYTES + stage * Shape::STAGE;
           const int line = (KEYS - valid) * 8;   // 16-byte pieces of one part
           for (int t = r; t < line * PARTS; t += 128) {
-            const int part = t / line, c = t - part * line;
+            const int part = quick_div(t, line), c = t - part * line;
             *reinterpret_cast<uint4*>(v + part * KEYS * 128 + valid * 128 + c * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
           }
@@ -854,7 +964,11 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 #pragma unroll
           for (int c = 0; c < 4; ++c) mx[c] = s[c];
 #pragma unroll
-          for (int c = 4; c < KEYS; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
+          for (int c = 4; c < KEYS; c += 8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mx[e] = c + 4 < KEYS ? max3(mx[e], s[c + e], s[(c + 4 + e) % KEYS]) : fmaxf(mx[e], s[c + e]);
+          }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
           if (j == 0) {
             m = top == -INFINITY ? -1e30f : top;   // nothing finite yet: weights of 0
@@ -901,20 +1015,25 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(pfull0 + 8 * sb);
+        if (!dry && lane == 0) mbar_arrive(pfull0 + 8 * sb);
       }
       if (!ok) break;
-      done += mine;
-      // The unit's end: O, m and l to its slot.
-      const bool both = NS == 2 && !un.pair;        // one query tile, merged here
-      if (w == 0 || !un.pair) ok = warp_poll(ofull0, ends0 & 1, p.timeout_ns);
-      if (n1 > 0 && (w == 1 || both)) ok = ok && warp_poll(ofull0 + 8, ends1 & 1, p.timeout_ns);
-      if (!ok) break;
-      ++ends0;
-      ends1 += n1 > 0;
+      // The unit's end: O, m and l to its slot. A single query tile's two
+      // streams (kSplit) are merged here and each warpgroup writes half of the
+      // columns; else a stream writes its own rows.
+      const bool merge = NS == 2 && mode == kSplit;
+      if (!dry) {
+        done += mine;
+        if (n0 > 0 && (w == 0 || mode == kSplit)) ok = warp_poll(ofull0, ends0 & 1, p.timeout_ns);
+        if (n1 > 0 && (w == 1 || merge)) ok = ok && warp_poll(ofull0 + 8, ends1 & 1, p.timeout_ns);
+        if (!ok) break;
+        ends0 += n0 > 0;
+        ends1 += n1 > 0;
+        base += 2 * n;
+      }
       tc_fence_after();
       float a0 = 1.0f, a1 = 0.0f;
-      if (both) {
+      if (merge) {
         if (mine > 0) ml[128 * w + r] = make_float2(m, l);
         __syncwarp();
         if (lane == 0) mbar_arrive(meet);
@@ -929,28 +1048,20 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           l = x.y * a0 + y.y * a1;
         }
       }
-      if (active) {
-        const int stride = un.own ? p.G : 128;
-        const int sub = un.pair ? w : 0;
-        float4* dst;
-        float2* dst_ml;
-        if (un.own) {
-          dst = reinterpret_cast<float4*>(p.own_o) + static_cast<size_t>(un.slot) * (D / 4) * p.G;
-          dst_ml = p.own_ml + static_cast<size_t>(un.slot) * p.G;
-        } else {
-          const size_t tile = static_cast<size_t>(un.slot) * NS + sub;
-          dst = reinterpret_cast<float4*>(p.prefix_o) + tile * (D / 4) * 128;
-          dst_ml = p.prefix_ml + tile * 128;
-        }
-        // A pair's streams write their own tiles; else the warpgroups share
-        // the columns of the one tile.
-        const int c_begin = un.pair ? 0 : w * (D / 2), c_end = un.pair ? D : c_begin + D / 2;
-        const uint32_t o_addr = tmem + lane_addr + Shape::O_COL0 + (un.pair ? w * D : 0);
+      if (active && !dry && (mode == kSplit || mine > 0)) {
+        const bool live = row >= 0 && row < rows;
+        const int stride = own ? p.G : 128;
+        const size_t tile = own ? slot : static_cast<size_t>(slot) * NS + (mode == kPair ? w : 0);
+        float4* dst = reinterpret_cast<float4*>(own ? p.own_o : p.prefix_o) + tile * (D / 4) * stride;
+        float2* dst_ml = (own ? p.own_ml : p.prefix_ml) + tile * stride;
+        const int c_begin = mode == kSplit ? w * (D / 2) : 0;
+        const int c_end = mode == kSplit ? c_begin + D / 2 : D;
+        const uint32_t o_addr = tmem + lane_addr + Shape::O_COL0 + (mode == kSplit ? 0 : w * D);
 #pragma unroll 1
         for (int c = c_begin; c < c_end; c += 32) {
           float o[32];
           tmem_ld32(o_addr + c, o);
-          if (both && n1 > 0) {
+          if (merge && n1 > 0) {
             float o1[32];
             tmem_ld32(o_addr + D + c, o1);
             tmem_wait_ld();
@@ -962,19 +1073,26 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             tmem_wait_ld();
             hold<32>(o);
           }
-          if (r < rows) {
+          if (live) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              __stcg(dst + static_cast<size_t>((c + e) / 4) * stride + r,
+              __stcg(dst + static_cast<size_t>((c + e) / 4) * stride + row,
                      make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
           }
         }
-        if (r < rows && (un.pair || w == 0)) __stcg(dst_ml + r, make_float2(m, l));
+        if (live && (mode != kSplit || w == 0)) __stcg(dst_ml + row, make_float2(m, l));
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(ofree);
-      base += 2 * n;
+      if (lane == 0) {   // 8 arrivals a barrier: all warps once, or a stream's own twice
+        if (mode == kSplit) {
+          mbar_arrive(ofree0);
+          mbar_arrive(ofree0 + 8);
+        } else {
+          mbar_arrive(ofree0 + 8 * w);
+          mbar_arrive(ofree0 + 8 * w);
+        }
+      }
     }
     if (!ok && lane == 0) atomicOr(&p.head->status, kErrPxSoftmax);
   }
