@@ -71,11 +71,16 @@ int check_args(const void* q, const void* k_pool, const void* v_pool, const int3
     return pfail(GQA_AV_ERR_UNSUPPORTED, "Hq / Hkv = %d is above 128", Hq / Hkv);
   if (block_size % 8)
     return pfail(GQA_AV_ERR_UNSUPPORTED, "block_size=%d must be a multiple of 8", block_size);
-  if (B > 4096 || P > 128)
-    return pfail(GQA_AV_ERR_UNSUPPORTED, "B=%d is above 4096 or P=%d above 128", B, P);
-  const long long most = 0x7fffffffLL / block_size;
-  if (num_blocks > most || max_blocks > most || max_prefix_blocks > most)
-    return pfail(GQA_AV_ERR_UNSUPPORTED, "a pool or a table row of 2^31 or more cache rows");
+  if (B > kPxMaxB || P > kPxMaxGroups)
+    return pfail(GQA_AV_ERR_UNSUPPORTED, "B=%d is above %d or P=%d above %d", B, kPxMaxB, P,
+                 kPxMaxGroups);
+  if (Hkv > (1 << 14) || static_cast<long long>(B) * Hkv > (1 << 20))
+    return pfail(GQA_AV_ERR_UNSUPPORTED, "Hkv=%d is above 2^14 or B * Hkv = %lld above 2^20", Hkv,
+                 static_cast<long long>(B) * Hkv);
+  const long long most = 0x7fffffffLL / block_size, longest = (1LL << 26) / block_size;
+  if (num_blocks > most || max_blocks > longest || max_prefix_blocks > longest)
+    return pfail(GQA_AV_ERR_UNSUPPORTED,
+                 "a pool of 2^31 or more cache rows, or a table row of more than 2^26");
   if ((addr(q) | addr(k_pool) | addr(v_pool) | addr(out)) & 15u)
     return pfail(GQA_AV_ERR_UNSUPPORTED, "q, the pools and out must be 16-byte aligned");
   return GQA_AV_OK;
@@ -228,6 +233,11 @@ extern "C" int gqa_prefix_attn_decode(
   p.B = B; p.P = P; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.TB = 128 / p.G;
   p.bs = block_size; p.num_blocks = num_blocks;
   p.max_pblocks = max_prefix_blocks; p.max_blocks = max_blocks;
+  // Division by the block size as a product: with shift = 28 + ceil(log2(bs)) the
+  // rounded-up factor is below 2^30 and off by less than 2^-28 bs, relatively to
+  // 2^shift, which a dividend below 2^26 does not notice.
+  for (p.bs_shift = 28; (1LL << (p.bs_shift - 28)) < block_size;) ++p.bs_shift;
+  p.bs_mul = static_cast<unsigned>(((1ULL << p.bs_shift) + block_size - 1) / block_size);
   const int keys = D == 256 ? PxShape<256>::KEYS : PxShape<128>::KEYS;
   for (p.R = 8; p.R < keys && block_size % (2 * p.R) == 0;) p.R *= 2;
   // log2(e) in the scale; a scale of 0 becomes the smallest normal number, which
@@ -249,8 +259,6 @@ extern "C" int gqa_prefix_attn_decode(
   const size_t q_tiles = static_cast<size_t>((B + p.TB - 1) / p.TB + std::min(P, B)) * Hkv;
   const size_t prefix_slots = P ? q_tiles + 2 * static_cast<size_t>(sms) : 0;
   const size_t own_slots = max_blocks ? static_cast<size_t>(B) * Hkv + 4 * static_cast<size_t>(sms) : 0;
-  if (prefix_slots + own_slots > 0x3ffffffu)
-    return pfail(GQA_AV_ERR_UNSUPPORTED, "too many units of work");
   p.prefix_slots = static_cast<int>(prefix_slots);
   const size_t at_po = up256(sizeof(PxHeader));
   const size_t at_pm = at_po + prefix_slots * ns * 128 * D * 4;

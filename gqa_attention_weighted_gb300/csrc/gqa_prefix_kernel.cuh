@@ -55,7 +55,7 @@ constexpr int kPxThreads = 384;
 // thread: 2 * 128 * 184 + 128 * 136 = 384 * 168.
 constexpr int kPxSoftmaxRegs = 184, kPxAuxRegs = 136;
 constexpr int kPxMmaWarp = 8, kPxKWarp = 9, kPxVWarp = 10;
-constexpr int kPxMaxGroups = 128;
+constexpr int kPxMaxGroups = 32;       // a lane of the plan each
 constexpr int kPxMaxB = 4096;
 constexpr int kPxSegs = 2;             // unit descriptors in flight
 constexpr float kPxGrow = 8.0f;        // log2 of the growth of a maximum that is tolerated
@@ -107,6 +107,8 @@ struct alignas(64) PrefixParams {
   float2* own_ml;                 // [units][G]
   int B, P, Hq, Hkv, G, TB;
   int bs, num_blocks, max_pblocks, max_blocks;
+  unsigned bs_mul;                // c / bs = c * bs_mul >> bs_shift for c < 2^26
+  int bs_shift;
   int R;                          // rows of a K or V box: gcd(bs, KEYS)
   float qscale;                   // |scale| * log2(e)
   int negate;                     // scale < 0
@@ -300,12 +302,11 @@ __device__ __forceinline__ int warp_incl_sum(int x) {
   return x;
 }
 
-// x / y, y > 0. Below 2^21 in fp32: the quotient of x + 1/2 is at least 1/(2y)
-// from the next integer, further than its error.
+// x / y for 0 <= x < 2^21 and y > 0, in fp32: the quotient of x + 1/2 is at
+// least 1 / (2 y) away from an integer, further than its error. The host keeps
+// tiles, units and sequences below that.
 __device__ __forceinline__ int quick_div(int x, int y) {
-  if (static_cast<unsigned>(x) < (1u << 21))
-    return __float2int_rz(__fdividef(static_cast<float>(x) + 0.5f, static_cast<float>(y)));
-  return x / y;
+  return __float2int_rz(__fdividef(static_cast<float>(x) + 0.5f, static_cast<float>(y)));
 }
 
 // The sequences' own part of the plan, in shared memory.
@@ -317,15 +318,16 @@ struct PxOwn {
   int paired;               // units are taken two at a time
 };
 
-// The plan, made from the lengths by two warps at the head of every call, so
-// its loads go out together and slow arithmetic is kept out of it. The V warp
-// makes the own part; the K warp makes the groups' part, lane l holding groups
-// 32 j + l, and finds units by it.
+// The plan, made from the lengths by two warps at the head of every call. Its
+// code runs once a call and is fetched cold each time, at about 7 ns an
+// instruction (measured: 3.2 us for one part, 1 us when run again), so it is
+// kept short: 32 groups at most, no integer division, no unrolling but that of
+// loads. The V warp makes the own part; the K warp the groups', a lane each,
+// and finds units by it.
 template <int D>
 struct PxPlan {
   using Shape = PxShape<D>;
-  static constexpr int J = kPxMaxGroups / 32;
-  int begin[J], end[J], len[J], tiles[J], splits[J], nq[J], pair[J], upto[J];
+  int begin, end, len, tiles, splits, nq, pair, upto;   // this lane's group
   int prefix_units;
 
   static __device__ __forceinline__ int own_len(const PrefixParams& p, int b) {
@@ -333,61 +335,52 @@ struct PxPlan {
     return b < p.B ? (p.seq_lens ? min(max(p.seq_lens[b], 0), cap) : cap) : 0;
   }
   static __device__ __forceinline__ int tiles_of(int len) {
-    return len / Shape::KEYS + (len % Shape::KEYS != 0);
+    return (len + Shape::KEYS - 1) / Shape::KEYS;
   }
 
   // By the V warp. A unit takes so many tiles that a CTA gets about four, so
-  // that the last ones to end are short. The sums of a lane's tiles may pass
-  // 2^32 over the warp: added as two halves.
+  // that the last ones to end are short. The sum of the tiles is made of two
+  // halves: it may pass 2^31.
   static __device__ __forceinline__ void make_own(const PrefixParams& p, PxOwn* own) {
     const int lane = threadIdx.x & 31;
-    const int blocks = p.max_blocks > 0 ? (p.B + 31) / 32 : 0;
-    constexpr int kKept = 8;          // blocks whose tiles stay in registers
-    int kept[kKept];
+    const int seqs = p.max_blocks > 0 ? p.B : 0;
     unsigned low = 0, high = 0;
+    for (int b0 = 0; b0 < seqs; b0 += 256) {
+      int len[8];
 #pragma unroll
-    for (int k = 0; k < kKept; ++k) kept[k] = k < blocks ? own_len(p, 32 * k + lane) : 0;
+      for (int k = 0; k < 8; ++k) len[k] = own_len(p, b0 + 32 * k + lane);
 #pragma unroll
-    for (int k = 0; k < kKept; ++k) {
-      kept[k] = tiles_of(kept[k]);
-      low += kept[k] & 4095;
-      high += kept[k] >> 12;
-    }
-#pragma unroll 4
-    for (int k = kKept; k < blocks; ++k) {
-      const int t = tiles_of(own_len(p, 32 * k + lane));
-      low += t & 4095;
-      high += t >> 12;
+      for (int k = 0; k < 8; ++k) {
+        low += tiles_of(len[k]) & 4095;
+        high += tiles_of(len[k]) >> 12;
+      }
     }
     low = __reduce_add_sync(0xffffffffu, low);
     high = __reduce_add_sync(0xffffffffu, high);
-    const unsigned long long all =
-        ((static_cast<unsigned long long>(high) << 12) + low) * static_cast<unsigned>(p.Hkv);
-    const int share = 4 * gridDim.x;
-    const int each = max(1, all < (1u << 30) ? quick_div(static_cast<int>(all) + share - 1, share)
-                                             : static_cast<int>((all + share - 1) / share));
+    const float work = (static_cast<float>(high) * 4096.0f + static_cast<float>(low)) *
+                       static_cast<float>(p.Hkv);
+    // Rounded up with a margin for the rounding of the sum: never more than
+    // four units a CTA beyond one a sequence and KV head.
+    const int each = __float2int_ru(
+        fminf(fmaxf(1.0f, __fdividef(work * 1.00001f, static_cast<float>(4 * gridDim.x))), 1048576.0f));
     int units = 0;
-    for (int k0 = 0; k0 < blocks; k0 += 32) {
+#pragma unroll 1
+    for (int k0 = 0; 32 * k0 < seqs; k0 += 32) {
       int mine = 0;
-#pragma unroll
-      for (int k = 0; k < kKept; ++k)
-        if (k0 == 0 && k < blocks) {
-          const int sum = __reduce_add_sync(0xffffffffu, quick_div(kept[k] + each - 1, each));
-          if (k == lane) mine = sum * p.Hkv;
-        }
-      for (int k = max(k0, kKept); k < min(blocks, k0 + 32); ++k) {
-        const int t = tiles_of(own_len(p, 32 * k + lane));
+#pragma unroll 2
+      for (int k = 0; k < 32 && 32 * (k0 + k) < seqs; ++k) {
+        const int t = tiles_of(own_len(p, 32 * (k0 + k) + lane));
         const int sum = __reduce_add_sync(0xffffffffu, quick_div(t + each - 1, each));
-        if (k - k0 == lane) mine = sum * p.Hkv;
+        mine = k == lane ? sum * p.Hkv : mine;
       }
       mine = units + warp_incl_sum(mine);
-      if (k0 + lane < kPxMaxB / 32) own->upto[k0 + lane] = mine;
+      own->upto[k0 + lane] = mine;
       units = __shfl_sync(0xffffffffu, mine, 31);
     }
     if (lane == 0) {
       own->tiles = each;
       own->units = units;
-      own->work = static_cast<float>(all);
+      own->work = work;
       own->paired = Shape::NS == 2 && units > static_cast<int>(gridDim.x);
     }
     __syncwarp();
@@ -396,103 +389,73 @@ struct PxPlan {
   // By the K warp: the groups' lengths, while the V warp reads the others.
   __device__ __forceinline__ void load_groups(const PrefixParams& p) {
     const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      begin[j] = end[j] = len[j] = tiles[j] = splits[j] = pair[j] = upto[j] = 0;
-      nq[j] = 1;
-      const int g = 32 * j + lane;
-      if (32 * j < p.P && g < p.P) {
-        begin[j] = p.group_start ? min(max(p.group_start[g], 0), p.B) : 0;
-        end[j] = p.group_start ? min(max(p.group_start[g + 1], 0), p.B) : p.B;
-        len[j] = min(max(p.prefix_lens[g], 0), p.max_pblocks * p.bs);
+    begin = 0;
+    end = lane < p.P ? p.B : 0;
+    len = 0;
+    if (lane < p.P) {
+      len = p.prefix_lens[lane];
+      if (p.group_start) {
+        begin = p.group_start[lane];
+        end = p.group_start[lane + 1];
       }
     }
-  }
-  __device__ __forceinline__ int query_tiles(const PrefixParams& p, int j) const {
-    return quick_div(end[j] - begin[j] + p.TB - 1, p.TB);
   }
   __device__ __forceinline__ void make_groups(const PrefixParams& p, const PxOwn* own) {
     const int lane = threadIdx.x & 31;
     const int n = gridDim.x;
-    // Starts not below their predecessors; tiles; query tiles.
-    int carry = 0, longest = 0;
-    float cost0 = 0.0f, cost1 = 0.0f;   // key tiles x query tiles, single and in pairs
+    // Starts within the batch and not below their predecessors.
+    begin = min(max(begin, 0), p.B);
+    if (p.P > 1) {
 #pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (32 * j < p.P) {
-        int a = max(begin[j], carry);
-        if (p.P > 1) {
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, a, o);
-            if (lane >= o) a = max(a, y);
-          }
-          carry = __shfl_sync(0xffffffffu, a, 31);
-        }
-        begin[j] = a;
-        end[j] = max(a, end[j]);
-        const int q = query_tiles(p, j);
-        tiles[j] = q > 0 ? tiles_of(len[j]) : 0;
-        cost0 += static_cast<float>(tiles[j]) * static_cast<float>(q);
-        cost1 += static_cast<float>(tiles[j]) * static_cast<float>((q + 1) / 2);
-        longest = max(longest, tiles[j]);
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, begin, o);
+        if (lane >= o) begin = max(begin, y);
       }
-    prefix_units = 0;
-    longest = __reduce_max_sync(0xffffffffu, longest);
+    }
+    end = max(begin, min(end, p.B));
+    len = min(max(len, 0), p.max_pblocks * p.bs);
+    const int q = quick_div(end - begin + p.TB - 1, p.TB);    // query tiles
+    tiles = lane < p.P && q > 0 ? tiles_of(len) : 0;
+    splits = upto = prefix_units = 0;
+    nq = 1;
+    pair = 0;
+    const int longest = __reduce_max_sync(0xffffffffu, tiles);
     if (longest == 0) return;
     // How to cut the prefixes: each lane costs one choice of pairs or single
     // query tiles and of the key tiles a split takes (1 to 8 units a CTA), from
     // the time that the units take if all CTAs stay busy, own units included,
     // and from the CTA with the most prefix units.
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      cost0 += __shfl_xor_sync(0xffffffffu, cost0, o);
-      cost1 += __shfl_xor_sync(0xffffffffu, cost1, o);
-    }
     const bool pairs = Shape::NS == 2 && (lane & 1);
-    const float w = (pairs ? cost1 : cost0) * static_cast<float>(p.Hkv);
-    const float per = __fdividef(w, static_cast<float>(((lane >> 2) + 1) * n));
-    int chunk = static_cast<int>(fminf(ceilf(per), 16777216.0f)) + ((lane >> 1) & 1);
-    if (lane >= 30) chunk = longest;   // no cut: always within the slots
-    chunk = max(1, min(chunk, longest));
-    int units = 0;
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (32 * j < p.P) {
-        const int q_mine = query_tiles(p, j);
-        for (int g = 0; g < min(p.P - 32 * j, 32); ++g) {
-          const int t = __shfl_sync(0xffffffffu, tiles[j], g);
-          const int q = __shfl_sync(0xffffffffu, q_mine, g);
-          const int more = quick_div(t + chunk - 1, chunk);
-          // A choice past the slots is dropped: no need to count on.
-          units = more > p.prefix_slots
-                      ? p.prefix_slots + 1
-                      : min(units + more * (pairs ? (q + 1) / 2 : q), p.prefix_slots + 1);
-        }
-      }
-    const bool fits = static_cast<long long>(units) * p.Hkv <= p.prefix_slots;
-    units *= p.Hkv;
+    float w = 0.0f;                     // key tiles x query tiles (or pairs)
+    for (int g = 0; g < p.P; ++g) {
+      const int t = __shfl_sync(0xffffffffu, tiles, g), m = __shfl_sync(0xffffffffu, q, g);
+      w += static_cast<float>(t) * static_cast<float>(pairs ? (m + 1) / 2 : m);
+    }
+    w *= static_cast<float>(p.Hkv);
+    int chunk = __float2int_ru(__fdividef(w, static_cast<float>(((lane >> 2) + 1) * n))) +
+                ((lane >> 1) & 1);
+    chunk = lane >= 30 ? longest : max(1, min(chunk, longest));   // 30, 31: no cut, always fits
+    float units = 0.0f;
+    for (int g = 0; g < p.P; ++g) {
+      const int t = __shfl_sync(0xffffffffu, tiles, g), m = __shfl_sync(0xffffffffu, q, g);
+      units += static_cast<float>(quick_div(t + chunk - 1, chunk)) *
+               static_cast<float>(pairs ? (m + 1) / 2 : m);
+    }
+    units *= static_cast<float>(p.Hkv);
     const float c = pairs ? p.c_pair : p.c_tile;
     const float one = static_cast<float>(chunk) * c + p.c_unit;
-    const float all = __fdividef(w * c + static_cast<float>(units) * p.c_unit + own->work * p.c_own,
-                                 static_cast<float>(n));
-    const float est =
-        fits ? fmaxf(all, static_cast<float>(quick_div(units + n - 1, n)) * one) : INFINITY;
+    const float all = __fdividef(w * c + units * p.c_unit + own->work * p.c_own, static_cast<float>(n));
+    const float rounds = ceilf(__fdividef(units - 0.5f, static_cast<float>(n)));
+    const float est = units <= static_cast<float>(p.prefix_slots) ? fmaxf(all, rounds * one) : INFINITY;
     // Costs are positive, so their bit patterns are ordered like them.
     const unsigned best = __reduce_min_sync(0xffffffffu, __float_as_uint(est));
     const int src = __ffs(__ballot_sync(0xffffffffu, __float_as_uint(est) == best)) - 1;
     const int cut = __shfl_sync(0xffffffffu, chunk, src);
-    const bool use_pairs = Shape::NS == 2 && (src & 1);
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (32 * j < p.P) {
-        const int q = query_tiles(p, j);
-        splits[j] = quick_div(tiles[j] + cut - 1, cut);
-        pair[j] = use_pairs && q > 1;
-        nq[j] = max(1, pair[j] ? (q + 1) / 2 : q);
-        upto[j] = prefix_units + warp_incl_sum(nq[j] * splits[j] * p.Hkv);
-        prefix_units = __shfl_sync(0xffffffffu, upto[j], 31);
-      }
+    splits = quick_div(tiles + cut - 1, cut);
+    pair = Shape::NS == 2 && (src & 1) && q > 1;
+    nq = max(1, pair ? (q + 1) / 2 : q);
+    upto = warp_incl_sum(nq * splits * p.Hkv);
+    prefix_units = __shfl_sync(0xffffffffu, upto, 31);
   }
 
   // Part i of t tiles cut into s equal parts (the first t % s one longer).
@@ -505,52 +468,40 @@ struct PxPlan {
   // Prefix unit u: counted (group, KV head, split, query tile), tiles fastest.
   __device__ __forceinline__ void find_prefix(const PrefixParams& p, int u, PxUnit& un) const {
     PxPart& w = un.part[0];
+    const int g = __ffs(__ballot_sync(0xffffffffu, u < upto)) - 1;
+    const int a = __shfl_sync(0xffffffffu, begin, g), e = __shfl_sync(0xffffffffu, end, g);
+    const int t = __shfl_sync(0xffffffffu, tiles, g), s = __shfl_sync(0xffffffffu, splits, g);
+    const int q = __shfl_sync(0xffffffffu, nq, g), pr = __shfl_sync(0xffffffffu, pair, g);
+    w.len = __shfl_sync(0xffffffffu, len, g);
+    const int local = u - (__shfl_sync(0xffffffffu, upto, g) - q * s * p.Hkv);
+    const int outer = quick_div(local, q), i = local - outer * q;
+    w.kv = quick_div(outer, s);
+    cut_out(w, outer - w.kv * s, t, s);
+    w.q0 = a + (i << pr) * p.TB;
+    un.rows[0] = min(p.TB, e - w.q0) * p.G;
+    un.rows[1] = pr ? max(0, min(p.TB, e - w.q0 - p.TB)) * p.G : 0;
+    un.mode = un.rows[1] > 0 ? kPair : kSplit;
     un.own = 0;
-    un.part[1].tiles = 0;
-    bool found = false;
-#pragma unroll
-    for (int j = 0; j < J; ++j) {
-      if (32 * j < p.P && !found) {
-        const unsigned hit = __ballot_sync(0xffffffffu, u < upto[j]);
-        if (hit) {
-          found = true;
-          const int src = __ffs(hit) - 1;
-          const int a = __shfl_sync(0xffffffffu, begin[j], src);
-          const int e = __shfl_sync(0xffffffffu, end[j], src);
-          const int t = __shfl_sync(0xffffffffu, tiles[j], src);
-          const int s = __shfl_sync(0xffffffffu, splits[j], src);
-          const int q = __shfl_sync(0xffffffffu, nq[j], src);
-          const int pr = __shfl_sync(0xffffffffu, pair[j], src);
-          w.len = __shfl_sync(0xffffffffu, len[j], src);
-          const int local = u - (__shfl_sync(0xffffffffu, upto[j], src) - q * s * p.Hkv);
-          const int outer = quick_div(local, q), i = local - outer * q;
-          w.kv = quick_div(outer, s);
-          cut_out(w, outer - w.kv * s, t, s);
-          w.q0 = a + i * (pr ? 2 : 1) * p.TB;
-          un.rows[0] = min(p.TB, e - w.q0) * p.G;
-          un.rows[1] = pr ? max(0, min(p.TB, e - w.q0 - p.TB)) * p.G : 0;
-          un.mode = un.rows[1] > 0 ? kPair : kSplit;
-          w.slot = u;
-          w.table = p.prefix_table + static_cast<size_t>(32 * j + src) * p.max_pblocks;
-        }
-      }
-    }
+    w.slot = u;
+    w.table = p.prefix_table + static_cast<size_t>(g) * p.max_pblocks;
   }
   // Own unit v: counted (sequence, KV head, split).
   static __device__ __forceinline__ void find_own(const PrefixParams& p, const PxOwn* own, int v,
                                                   PxPart& w) {
     const int lane = threadIdx.x & 31;
     int block = 0, before = 0;
-    for (int k0 = 0;; k0 += 32) {
+#pragma unroll 1
+    for (int k0 = 0; k0 < kPxMaxB / 32; k0 += 32) {
       const int upto = own->upto[k0 + lane];
       const unsigned hit = __ballot_sync(0xffffffffu, v < upto);
       const int at = hit ? __ffs(hit) - 2 : 31;
       if (at >= 0) before = __shfl_sync(0xffffffffu, upto, at);
       block = k0 + at + 1;
-      if (hit || k0 + 32 >= kPxMaxB / 32) break;
+      if (hit) break;
     }
+    const int each = own->tiles;
     const int my_len = own_len(p, 32 * block + lane);
-    const int my_splits = quick_div(tiles_of(my_len) + own->tiles - 1, own->tiles);
+    const int my_splits = quick_div(tiles_of(my_len) + each - 1, each);
     const int incl = warp_incl_sum(my_splits * p.Hkv);
     const int src = __ffs(__ballot_sync(0xffffffffu, v - before < incl) | 0x80000000u) - 1;
     const int s = max(1, __shfl_sync(0xffffffffu, my_splits, src));
@@ -568,13 +519,10 @@ struct PxPlan {
     const int lane = threadIdx.x & 31;
     const int each = own->tiles;
     if (lane == 0) p.head->own_tiles = each;
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-      if (32 * j + lane < p.P)
-        p.head->group[32 * j + lane] = {begin[j], end[j], splits[j], nq[j], pair[j],
-                                        upto[j] - nq[j] * splits[j] * p.Hkv};
+    if (lane < p.P) p.head->group[lane] = {begin, end, splits, nq, pair, upto - nq * splits * p.Hkv};
     int base = 0;
     if (p.max_blocks > 0)
+#pragma unroll 1
       for (int k = 0; 32 * k < p.B; ++k) {
         const int n = quick_div(tiles_of(own_len(p, 32 * k + lane)) + each - 1, each) * p.Hkv;
         const int incl = warp_incl_sum(n);
@@ -738,7 +686,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           const int tile = i < both ? i >> 1 : i - both / 2;
           const int c = ((second ? part1.t0 : part0.t0) + tile) * KEYS + lane * p.R;
           if (lane >= nch || i >= n || c >= (second ? part1.len : part0.len)) return oob;
-          const int col = quick_div(c, p.bs), block = (second ? part1.table : part0.table)[col];
+          const int col = static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(c)) * p.bs_mul) >> p.bs_shift);
+          const int block = (second ? part1.table : part0.table)[col];
           return block >= 0 && block < p.num_blocks ? block * p.bs + (c - col * p.bs) : oob;
         };
         int row = row_of(0);
@@ -1126,16 +1075,12 @@ __global__ void __launch_bounds__(kPxCombineThreads)
   const int own_tiles = p.head->own_tiles;
   const int own_base = p.max_blocks > 0 ? p.head->own_base[b] : 0;
   const int own_len = PxPlan<D>::own_len(p, b);
-  int group = -1;
-  for (int j = 0; j < p.P; j += 32) {
-    bool in = false;
-    if (j + lane < p.P) {
-      const PxGroup& g = p.head->group[j + lane];
-      in = b >= g.begin && b < g.end && g.splits > 0;
-    }
-    const unsigned hit = __ballot_sync(0xffffffffu, in);
-    if (hit) group = j + __ffs(hit) - 1;
+  bool in = false;
+  if (lane < p.P) {
+    const PxGroup& g = p.head->group[lane];
+    in = b >= g.begin && b < g.end && g.splits > 0;
   }
+  const int group = __ffs(__ballot_sync(0xffffffffu, in)) - 1;
   if (x >= p.G * (D / 4)) return;
   const int g = x % p.G, c = x / p.G;
   float top = -INFINITY, sum = 0.0f;
@@ -1183,7 +1128,7 @@ __global__ void __launch_bounds__(kPxCombineThreads)
         static_cast<size_t>(gr.nq) * Shape::NS, gr.splits, 128, (b - gr.begin - t * p.TB) * p.G + g);
   }
   if (own_len > 0) {
-    const int n = (PxPlan<D>::tiles_of(own_len) + own_tiles - 1) / own_tiles;
+    const int n = quick_div(PxPlan<D>::tiles_of(own_len) + own_tiles - 1, own_tiles);
     add(p.own_o, p.own_ml, own_base + static_cast<size_t>(h) * n, 1, n, p.G, g);
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;

@@ -38,8 +38,8 @@
  * shapes and lengths give bitwise-identical out.
  *
  * Limits: D 64, 128 or 256; G <= 128; block_size a multiple of 8; q, out and
- * the pools 16-byte aligned; B <= 4096, P <= 128; num_blocks * block_size and
- * what one table row can hold below 2^31 rows.
+ * the pools 16-byte aligned; B <= 4096, Hkv <= 2^14, B * Hkv <= 2^20, P <= 32;
+ * num_blocks * block_size below 2^31 and at most 2^26 rows in one table row.
  *
  * Execution: asynchronous on `stream`, no host synchronisation; the lengths
  * and groups are read on the device, so a captured graph follows them. The

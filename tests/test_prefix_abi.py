@@ -41,8 +41,10 @@ CALL = dict(q=FAKE, k=FAKE, v=FAKE, ptab=FAKE, plen=FAKE, gs=FAKE, tab=FAKE, len
     (dict(q=None), 1), (dict(k=None), 1), (dict(out=None), 1), (dict(ptab=None), 1),
     (dict(plen=None), 1), (dict(tab=None), 1), (dict(P=2, gs=None), 1), (dict(tab=FAKE + 2), 1),
     (dict(lens=FAKE + 1), 1), (dict(D=96), 2), (dict(D=512), 2), (dict(Hq=258), 2),
-    (dict(bs=12), 2), (dict(bs=4), 2), (dict(B=4097), 2), (dict(P=129), 2),
-    (dict(nb=1 << 27), 2), (dict(mb=1 << 27), 2), (dict(q=FAKE + 8), 2), (dict(v=FAKE + 2), 2),
+    (dict(bs=12), 2), (dict(bs=4), 2), (dict(B=4097), 2), (dict(P=129), 2), (dict(P=33), 2),
+    (dict(B=4096, Hq=512, Hkv=512), 2),
+    (dict(nb=1 << 27), 2), (dict(mb=1 << 27), 2),
+    (dict(mb=(1 << 22) + 1), 2), (dict(mpb=(1 << 22) + 1), 2), (dict(q=FAKE + 8), 2), (dict(v=FAKE + 2), 2),
 ])
 def test_host_checks(native, change, status):
     a = dict(CALL, **change)
