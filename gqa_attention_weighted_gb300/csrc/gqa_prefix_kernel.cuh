@@ -1085,51 +1085,59 @@ __global__ void __launch_bounds__(kPxCombineThreads)
   const int g = x % p.G, c = x / p.G;
   float top = -INFINITY, sum = 0.0f;
   float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  // n slots, `step` tiles of `rows` rows apart.
-  auto add = [&](const float* o, const float2* ml, size_t tile, size_t step, int n, int rows, int row) {
-    const float4* o4 = reinterpret_cast<const float4*>(o) + (tile * (D / 4) + c) * rows + row;
-    const float2* m2 = ml + tile * rows + row;
-    constexpr int U = 8;
-    for (int s = 0; s < n; s += U) {
-      float2 m[U];
-      float4 v[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        m[i] = make_float2(-INFINITY, 0.0f);
-        v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (s + i < n) {
-          m[i] = __ldcg(m2 + (s + i) * step * rows);
-          v[i] = __ldcg(o4 + (s + i) * step * (D / 4) * rows);
-        }
-      }
-      float now = top;
-#pragma unroll
-      for (int i = 0; i < U; ++i) now = fmaxf(now, m[i].x);
-      const float old = ex2(top - now);
-      top = now;
-      sum *= old;
-      acc.x *= old; acc.y *= old; acc.z *= old; acc.w *= old;
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const float a = ex2(m[i].x - now);
-        sum = fmaf(a, m[i].y, sum);
-        acc.x = fmaf(a, v[i].x, acc.x);
-        acc.y = fmaf(a, v[i].y, acc.y);
-        acc.z = fmaf(a, v[i].z, acc.z);
-        acc.w = fmaf(a, v[i].w, acc.w);
-      }
-    }
-  };
+  // The slots, prefix's first: n0 of 128 rows, `step` tiles apart, then n1 of G rows.
+  const float4 *o0 = nullptr, *o1 = nullptr;
+  const float2 *m0 = nullptr, *m1 = nullptr;
+  int n0 = 0, n1 = 0;
+  size_t step = 0;
   if (group >= 0) {
     const PxGroup gr = p.head->group[group];
-    const int t = (b - gr.begin) / p.TB;
+    const int t = quick_div(b - gr.begin, p.TB);
     const size_t unit = gr.base + static_cast<size_t>(h) * gr.splits * gr.nq + (gr.pair ? t / 2 : t);
-    add(p.prefix_o, p.prefix_ml, unit * Shape::NS + (gr.pair ? t & 1 : 0),
-        static_cast<size_t>(gr.nq) * Shape::NS, gr.splits, 128, (b - gr.begin - t * p.TB) * p.G + g);
+    const size_t tile = unit * Shape::NS + (gr.pair ? t & 1 : 0);
+    const int row = (b - gr.begin - t * p.TB) * p.G + g;
+    n0 = gr.splits;
+    step = static_cast<size_t>(gr.nq) * Shape::NS * 128;
+    o0 = reinterpret_cast<const float4*>(p.prefix_o) + (tile * (D / 4) + c) * 128 + row;
+    m0 = p.prefix_ml + tile * 128 + row;
   }
   if (own_len > 0) {
-    const int n = quick_div(PxPlan<D>::tiles_of(own_len) + own_tiles - 1, own_tiles);
-    add(p.own_o, p.own_ml, own_base + static_cast<size_t>(h) * n, 1, n, p.G, g);
+    n1 = quick_div(PxPlan<D>::tiles_of(own_len) + own_tiles - 1, own_tiles);
+    const size_t tile = own_base + static_cast<size_t>(h) * n1;
+    o1 = reinterpret_cast<const float4*>(p.own_o) + (tile * (D / 4) + c) * p.G + g;
+    m1 = p.own_ml + tile * p.G + g;
+  }
+  constexpr int U = 8;
+  for (int s = 0; s < n0 + n1; s += U) {
+    float2 m[U];
+    float4 v[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      m[i] = make_float2(-INFINITY, 0.0f);
+      v[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (s + i < n0 + n1) {
+        const bool own = s + i >= n0;
+        const size_t at = own ? static_cast<size_t>(s + i - n0) * p.G : (s + i) * step;
+        m[i] = __ldcg((own ? m1 : m0) + at);
+        v[i] = __ldcg((own ? o1 : o0) + at * (D / 4));
+      }
+    }
+    float now = top;
+#pragma unroll
+    for (int i = 0; i < U; ++i) now = fmaxf(now, m[i].x);
+    const float old = ex2(top - now);
+    top = now;
+    sum *= old;
+    acc.x *= old; acc.y *= old; acc.z *= old; acc.w *= old;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const float a = ex2(m[i].x - now);
+      sum = fmaf(a, m[i].y, sum);
+      acc.x = fmaf(a, v[i].x, acc.x);
+      acc.y = fmaf(a, v[i].y, acc.y);
+      acc.z = fmaf(a, v[i].z, acc.z);
+      acc.w = fmaf(a, v[i].w, acc.w);
+    }
   }
   const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
   const uint2 y = make_uint2(pack2<Tag>(acc.x * inv, acc.y * inv), pack2<Tag>(acc.z * inv, acc.w * inv));
