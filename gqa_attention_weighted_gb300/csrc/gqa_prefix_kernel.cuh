@@ -140,6 +140,24 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
       "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tmem_ld16_nowait(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+      "%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tmem_wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -896,27 +914,36 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         }
         if (active) {
           const uint32_t s_addr = tmem + lane_addr + Shape::S_COL * sb;
-          float s[KEYS];
+          // Loops over 64 keys, S read twice: unrolled over 128 the code of a
+          // tile is past what a scheduler's instruction cache feeds, and the
+          // fetches cost more than the second read of tensor memory.
+          if (valid < KEYS || p.negate) {
+            // Keys past the length, and a negative scale, in S itself.
+#pragma unroll 1
+            for (int c0 = 0; c0 < KEYS; c0 += 16) {
+              float s[16];
+              tmem_ld16_nowait(s_addr + c0, s);
+              tmem_wait_ld();
+              hold<16>(s);
 #pragma unroll
-          for (int c = 0; c < KEYS; c += 32) tmem_ld32(s_addr + c, s + c);
-          tmem_wait_ld();
-          hold<KEYS>(s);
-          if (p.negate) {
-#pragma unroll
-            for (int c = 0; c < KEYS; ++c) s[c] = -s[c];
+              for (int c = 0; c < 16; ++c)
+                s[c] = c0 + c < valid ? (p.negate ? -s[c] : s[c]) : -INFINITY;
+              tmem_st16(s_addr + c0, reinterpret_cast<const uint32_t*>(s));
+            }
+            tmem_wait_st();
           }
-          if (valid < KEYS) {
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+          for (int c0 = 0; c0 < KEYS; c0 += 64) {
+            float s[64];
+            tmem_ld32(s_addr + c0, s);
+            tmem_ld32(s_addr + c0 + 32, s + 32);
+            tmem_wait_ld();
+            hold<64>(s);
 #pragma unroll
-            for (int c = 0; c < KEYS; ++c) s[c] = c < valid ? s[c] : -INFINITY;
-          }
-          float mx[4];
+            for (int c = 0; c < 64; c += 8)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) mx[c] = s[c];
-#pragma unroll
-          for (int c = 4; c < KEYS; c += 8) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mx[e] = c + 4 < KEYS ? max3(mx[e], s[c + e], s[(c + 4 + e) % KEYS]) : fmaxf(mx[e], s[c + e]);
+              for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
           }
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
           if (j == 0) {
@@ -945,19 +972,24 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           }
           const float shift = kOff - m, qscale = p.qscale;
           float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
+#pragma unroll 1
           for (int c0 = 0; c0 < KEYS; c0 += 64) {
+            float s[64];
             uint32_t w16[32];
+            tmem_ld32(s_addr + c0, s);
+            tmem_ld32(s_addr + c0 + 32, s + 32);
+            tmem_wait_ld();
+            hold<64>(s);
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
               float x, y;
-              fma2(s[c0 + c], s[c0 + c + 1], qscale, qscale, shift, shift, x, y);
+              fma2(s[c], s[c + 1], qscale, qscale, shift, shift, x, y);
               x = ex2(x);
               y = ex2(y);
               add2(sum[c & 2], sum[(c & 2) + 1], x, y);
               w16[c / 2] = pack2<Tag>(x, y);
             }
-            tmem_st32(s_addr + c0 / 2, w16);
+            tmem_st32(s_addr + c0 / 2, w16);   // over scores that have been read
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
