@@ -825,17 +825,13 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         } else {
           // Every unit's phase of both ofree barriers is waited for, here or by pv.
           if (n1 == 0) ok = warp_poll(ofree0 + 8, unit_no & 1, p.timeout_ns);
-          qk(0, 0);
-          if (n1 > 0) qk(1, 0);
-          for (int j = 0; j < max(n0, n1) && ok; ++j) {
-            if (j < n0) {
-              pv(0, j);
-              if (j + 1 < n0) qk(0, j + 1);
-            }
-            if (j < n1) {
-              pv(1, j);
-              if (j + 1 < n1) qk(1, j + 1);
-            }
+          // The streams in turn: the PV of a tile, then the QK of the next. One
+          // site for each product keeps the code small.
+#pragma unroll 1
+          for (int t = -2; t < 2 * max(n0, n1) && ok; ++t) {
+            const int w = t & 1, j = t >> 1, cnt = w ? n1 : n0;
+            if (j >= 0 && j < cnt) pv(w, j);
+            if (j + 1 < cnt) qk(w, j + 1);
           }
         }
         base += 2 * n;
