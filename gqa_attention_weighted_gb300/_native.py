@@ -124,8 +124,14 @@ def _check(status: int) -> None:
         raise GqaAvError(status, f"{name}: {msg}")
 
 
+# The current stream's handle without a Stream object around it (a few us a call).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream) -> Optional[int]:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -374,25 +380,24 @@ def _check_kv(status: int) -> None:
         raise GqaAvError(status, f"{name}: {lib.gqa_kv_last_error().decode()}")
 
 
-def _int32(name: str, t, *shape) -> None:
-    """A contiguous CUDA int32 tensor of this shape (None: any size)."""
-    if (not t.is_cuda or t.dtype != torch.int32 or not t.is_contiguous() or t.dim() != len(shape)
-            or any(n is not None and n != m for n, m in zip(shape, t.shape))):
-        want = "[" + ", ".join("*" if n is None else str(n) for n in shape) + "]"
-        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of shape {want}, not "
-                         f"{t.dtype} {tuple(t.shape)}")
+def _int32(name: str, t, shape) -> None:
+    """A contiguous CUDA int32 tensor of this shape."""
+    if t.dtype is not torch.int32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of shape {tuple(shape)}, "
+                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
 def _pools(k_pool: torch.Tensor, v_pool: torch.Tensor):
-    if k_pool.dim() != 4 or tuple(v_pool.shape) != tuple(k_pool.shape):
+    shape, dtype = k_pool.shape, k_pool.dtype
+    if len(shape) != 4 or v_pool.shape != shape:
         raise ValueError("k_pool and v_pool must both be [num_blocks, block_size, Hkv, D], not "
-                         f"{tuple(k_pool.shape)} and {tuple(v_pool.shape)}")
-    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if k_pool.dtype not in _V_DTYPE or v_pool.dtype != k_pool.dtype:
+                         f"{tuple(shape)} and {tuple(v_pool.shape)}")
+    if dtype not in _V_DTYPE or v_pool.dtype is not dtype:
         raise ValueError("k_pool and v_pool must both be bfloat16 or both float16")
-    return tuple(k_pool.shape)
+    if not (k_pool.is_cuda and v_pool.is_cuda and k_pool.is_contiguous()
+            and v_pool.is_contiguous()):
+        raise ValueError("k_pool and v_pool must be contiguous CUDA tensors")
+    return shape
 
 
 def gqa_kv_tables(cached_lens, new_lens, free_list, free_count, block_table, seq_lens, token_start,
@@ -402,23 +407,28 @@ def gqa_kv_tables(cached_lens, new_lens, free_list, free_count, block_table, seq
     of ``free_list[:free_count]`` in request order and ``block_table`` is updated in place;
     ``seq_lens``, ``token_start``, ``slots``, ``positions`` and ``free_left`` are written.
     Requests that find no blocks keep their length and get slots of -1."""
-    _int32("block_table", block_table, None, None)
+    if block_table.dim() != 2 or free_list.dim() != 1 or slots.dim() != 1:
+        raise ValueError("block_table must be [B, max_blocks], free_list and slots of one "
+                         "dimension")
     B, max_blocks = block_table.shape
-    for name, t in (("cached_lens", cached_lens), ("new_lens", new_lens), ("seq_lens", seq_lens)):
-        _int32(name, t, B)
+    T, n_free = slots.shape[0], free_list.shape[0]
+    _int32("block_table", block_table, (B, max_blocks))
+    _int32("cached_lens", cached_lens, (B,))
+    _int32("new_lens", new_lens, (B,))
+    _int32("seq_lens", seq_lens, (B,))
     if pos_base is not None:
-        _int32("pos_base", pos_base, B)
-    _int32("free_list", free_list, None)
-    _int32("free_count", free_count, 1)
-    _int32("free_left", free_left, 1)
-    _int32("token_start", token_start, B + 1)
-    _int32("slots", slots, None)
-    _int32("positions", positions, slots.shape[0])
+        _int32("pos_base", pos_base, (B,))
+    _int32("free_list", free_list, (n_free,))
+    _int32("free_count", free_count, (1,))
+    _int32("free_left", free_left, (1,))
+    _int32("token_start", token_start, (B + 1,))
+    _int32("slots", slots, (T,))
+    _int32("positions", positions, (T,))
     _check_kv(lib.gqa_kv_tables(_ptr(cached_lens), _ptr(new_lens), _ptr(pos_base), _ptr(free_list),
                                 _ptr(free_count), _ptr(block_table), _ptr(seq_lens),
                                 _ptr(token_start), _ptr(slots), _ptr(positions), _ptr(free_left),
-                                B, slots.shape[0], max_blocks, free_list.shape[0], int(block_size),
-                                int(num_blocks), _stream_handle(stream)))
+                                B, T, max_blocks, n_free, int(block_size), int(num_blocks),
+                                _stream_handle(stream)))
 
 
 def gqa_kv_norm_rope_append(q, k, v, positions, slots, inv_freq, q_out, k_pool, v_pool,
@@ -430,45 +440,45 @@ def gqa_kv_norm_rope_append(q, k, v, positions, slots, inv_freq, q_out, k_pool, 
     ``q_out`` (float32 or the input type), keys and values to rows ``slots`` of the pools. q, k and
     v may be views of one packed projection. Returns ``q_out``."""
     num_blocks, block_size, Hkv, D = _pools(k_pool, v_pool)
-    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+    dtype = k_pool.dtype
+    if q.dim() != 3:
         raise ValueError("q must be [T,Hq,D], k and v [T,Hkv,D]")
     T, Hq = q.shape[:2]
-    if (q.shape[2] != D or tuple(k.shape) != (T, Hkv, D) or tuple(v.shape) != (T, Hkv, D)
-            or tuple(q_out.shape) != (T, Hq, D)):
+    if (q.shape[2] != D or k.shape != (T, Hkv, D) or v.shape != (T, Hkv, D)
+            or q_out.shape != (T, Hq, D)):
         raise ValueError(f"inconsistent shapes: q {tuple(q.shape)}, k {tuple(k.shape)}, v "
                          f"{tuple(v.shape)}, q_out {tuple(q_out.shape)}, pools "
                          f"{tuple(k_pool.shape)}")
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        if not t.is_cuda or t.dtype != k_pool.dtype:
+    strides = []
+    for name, t, heads in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
+        if t.dtype is not dtype or not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor of the pools' type")
-        if T and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D)):
+        st = t.stride()
+        if T and (st[2] != 1 or (heads > 1 and st[1] != D)):
             raise ValueError(f"a token's heads must be contiguous in {name}")
-    if not q_out.is_cuda or not q_out.is_contiguous() or q_out.dtype not in (torch.float32,
-                                                                             k_pool.dtype):
+        strides.append(st[0])
+    q32 = q_out.dtype is torch.float32
+    if not (q32 or q_out.dtype is dtype) or not q_out.is_cuda or not q_out.is_contiguous():
         raise ValueError("q_out must be a contiguous CUDA tensor, float32 or of the pools' type")
-    _int32("slots", slots, T)
-    if positions.dim() == 1:
-        _int32("positions", positions, T)
-    else:
-        _int32("positions", positions, None, T)
+    _int32("slots", slots, (T,))
     axes = 1 if positions.dim() == 1 else positions.shape[0]
-    if (not inv_freq.is_cuda or inv_freq.dtype != torch.float32 or inv_freq.dim() != 1
+    _int32("positions", positions, (T,) if positions.dim() == 1 else (axes, T))
+    if (inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_cuda
             or not inv_freq.is_contiguous()):
         raise ValueError("inv_freq must be a contiguous CUDA float32 tensor of one dimension")
     if sections is not None and len(sections) != axes:
         raise ValueError(f"{len(sections)} sections for {axes} position axes")
     for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None and (not t.is_cuda or t.dtype != k_pool.dtype or tuple(t.shape) != (D,)
+        if t is not None and (t.dtype is not dtype or t.shape != (D,) or not t.is_cuda
                               or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous CUDA tensor [D] of the pools' type")
     sec = None if sections is None else (ctypes.c_int * axes)(*[int(n) for n in sections])
-    od = GQA_KV_F32 if q_out.dtype == torch.float32 else _V_DTYPE[k_pool.dtype]
+    code = _V_DTYPE[dtype]
     _check_kv(lib.gqa_kv_norm_rope_append(
-        _ptr(q), _ptr(k), _ptr(v), q.stride(0), k.stride(0), v.stride(0), _ptr(positions), sec,
-        axes, _ptr(inv_freq), _ptr(q_weight), _ptr(k_weight), float(eps), float(weight_offset),
-        1 if interleaved else 0, _ptr(slots), _ptr(q_out), od, _ptr(k_pool), _ptr(v_pool), T, Hq,
-        Hkv, D, 2 * inv_freq.shape[0], _V_DTYPE[k_pool.dtype], block_size, num_blocks,
-        _stream_handle(stream)))
+        _ptr(q), _ptr(k), _ptr(v), *strides, _ptr(positions), sec, axes, _ptr(inv_freq),
+        _ptr(q_weight), _ptr(k_weight), float(eps), float(weight_offset), 1 if interleaved else 0,
+        _ptr(slots), _ptr(q_out), GQA_KV_F32 if q32 else code, _ptr(k_pool), _ptr(v_pool), T, Hq,
+        Hkv, D, 2 * inv_freq.shape[0], code, block_size, num_blocks, _stream_handle(stream)))
     return q_out
 
 
@@ -487,30 +497,35 @@ def gqa_prefix_attn_decode(q, k_pool, v_pool, prefix_table, prefix_lens, group_s
     no shared prefixes; ``block_table`` None: no own rows. q and out are [B,Hq,D] of the pools' type
     (scale defaults to 1/sqrt(D)); writes and returns ``out``."""
     num_blocks, block_size, Hkv, D = _pools(k_pool, v_pool)
+    dtype = k_pool.dtype
     if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape:
         raise ValueError(f"q and out must be [B,Hq,{D}], not {tuple(q.shape)} and "
                          f"{tuple(out.shape)}")
     B, Hq = q.shape[:2]
-    for name, t in (("q", q), ("out", out)):
-        if not t.is_cuda or not t.is_contiguous() or t.dtype != k_pool.dtype:
-            raise ValueError(f"{name} must be a contiguous CUDA tensor of the pools' type")
+    if (q.dtype is not dtype or out.dtype is not dtype
+            or not (q.is_cuda and out.is_cuda and q.is_contiguous() and out.is_contiguous())):
+        raise ValueError("q and out must be contiguous CUDA tensors of the pools' type")
     P = max_pblocks = max_blocks = 0
     if prefix_table is not None:
-        _int32("prefix_table", prefix_table, None, None)
+        if prefix_table.dim() != 2:
+            raise ValueError("prefix_table must be [P, max_prefix_blocks]")
         P, max_pblocks = prefix_table.shape
-        _int32("prefix_lens", prefix_lens, P)
+        _int32("prefix_table", prefix_table, (P, max_pblocks))
+        _int32("prefix_lens", prefix_lens, (P,))
         if group_start is not None:
-            _int32("group_start", group_start, P + 1)
+            _int32("group_start", group_start, (P + 1,))
     if block_table is not None:
-        _int32("block_table", block_table, B, None)
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [B, max_blocks]")
         max_blocks = block_table.shape[1]
+        _int32("block_table", block_table, (B, max_blocks))
     if seq_lens is not None:
-        _int32("seq_lens", seq_lens, B)
+        _int32("seq_lens", seq_lens, (B,))
     sc = float(D) ** -0.5 if scale is None else float(scale)
     _check_prefix(lib.gqa_prefix_attn_decode(
         _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(prefix_table) if P else None,
         _ptr(prefix_lens) if P else None, _ptr(group_start) if P else None, _ptr(block_table),
-        _ptr(seq_lens), _ptr(out), B, P, Hq, Hkv, D, _V_DTYPE[k_pool.dtype], block_size, num_blocks,
+        _ptr(seq_lens), _ptr(out), B, P, Hq, Hkv, D, _V_DTYPE[dtype], block_size, num_blocks,
         max_pblocks, max_blocks, sc, _stream_handle(stream)))
     return out
 

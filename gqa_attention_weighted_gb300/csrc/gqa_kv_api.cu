@@ -114,8 +114,11 @@ extern "C" int gqa_kv_tables(const int32_t* cached_lens, const int32_t* new_lens
   p.num_blocks = num_blocks;
   const size_t smem = static_cast<size_t>(B) * 12;
   const void* fn = reinterpret_cast<const void*>(gqa_kv_tables_kernel);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTabMaxB * 12);
-  if (e != cudaSuccess) return kfail_cuda(e, "cudaFuncSetAttribute");
+  cudaError_t e = cudaSuccess;
+  if (smem > 40960) {   // within the default limit otherwise
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTabMaxB * 12);
+    if (e != cudaSuccess) return kfail_cuda(e, "cudaFuncSetAttribute");
+  }
   const int grid = std::max(1, T / kTabTokensPerCta + (T % kTabTokensPerCta != 0));
   void* args[] = {&p};
   e = launch(fn, grid, kTabThreads, smem, static_cast<cudaStream_t>(stream), args);

@@ -188,114 +188,148 @@ __device__ __forceinline__ void pair_rotation(unsigned long long turn64, int pos
   sincospif(half_turns, s, c);
 }
 
-// A warp takes part of a token's heads, 32 / L heads a step: a lane owns 8
-// adjacent elements (16 bytes) of a head, the same ones in every step, so cos
-// and sin are made once a token and part. The squares are summed and the
-// other half of a pair is fetched by shuffles inside the head's L lanes.
+// A warp takes part of a token's heads, 32 / L heads a step. A lane owns both
+// elements of four pairs of a head, the same ones in every step: four and four
+// elements half a rotation apart, or eight adjacent ones (interleaved), so a
+// rotation needs no other lane, and cos and sin are made once a token and part.
+// Elements past the rotation are dealt out the same way and left alone. The
+// squares are summed by shuffles inside the head's L lanes. Bound by HBM for
+// long inputs, by latency for short ones: the loads of the next kAhead steps
+// are under way while a step is worked on. Measured at 16384 tokens of
+// 32 + 8 + 8 heads of 128, bf16: 142 us with eight adjacent elements a lane,
+// whose mates came by shuffles, and one step's loads at a time; 107 us with two.
 template <typename Tag, int L, bool kInterleaved, bool kQ32>
 __global__ void __launch_bounds__(32 * kRopeWarps) gqa_kv_rope_kernel(const RopeParams p) {
   __shared__ unsigned long long turn[kRopeMaxPairs];
+  constexpr int kHeads = 32 / L;                // heads a step
+  constexpr int kAhead = 2;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int li = lane % L, sub = lane / L;
-  constexpr int kHeads = 32 / L;   // heads a step
   grid_dependency_wait();
   grid_launch_dependents();
   for (int i = threadIdx.x; i < p.pairs; i += blockDim.x) {
     const double f = static_cast<double>(p.inv_freq[i]) * 0.15915494309189534561;  // 1 / (2 pi)
     turn[i] = static_cast<unsigned long long>((f - floor(f)) * 18446744073709551616.0);
   }
-  __syncthreads();
-
-  const int d0 = 8 * li;
-  const bool live = d0 < p.D;
+  // Elements e0 .. e0 + 3 and e1 .. e1 + 3; of pairs 4 li .. 4 li + 3 where rotated.
+  const bool live = 8 * li < p.D;
+  const bool rot = 4 * li < p.pairs;
+  int e0 = 8 * li, e1 = e0 + 4;
+  if (!kInterleaved) {
+    e0 = rot ? 4 * li : p.pairs + 4 * li;
+    e1 = rot ? p.pairs + 4 * li : e0 + p.D / 2 - p.pairs;
+  }
   const int all = p.Hq + 2 * p.Hkv;
-  const int half = p.pairs;                     // split pairs: (i, i + half)
-  const bool rot = d0 < 2 * p.pairs;
-  const bool upper = !kInterleaved && d0 >= half;
-  const int pair0 = kInterleaved ? d0 / 2 : (upper ? d0 - half : d0);
-  constexpr int kPairs = kInterleaved ? 4 : 8;  // pairs that this lane's elements are in
-  const int mate = kInterleaved ? lane : (upper ? lane - half / 8 : lane + half / 8);
+  const float inv_d = 1.0f / static_cast<float>(p.D);
+  auto load8 = [&](const void* base, size_t at) {   // at: the head's first element
+    const char* src = static_cast<const char*>(base) + 2 * at;
+    if constexpr (kInterleaved) return __ldcs(reinterpret_cast<const uint4*>(src + 2 * e0));
+    const uint2 a = __ldcs(reinterpret_cast<const uint2*>(src + 2 * e0));
+    const uint2 b = __ldcs(reinterpret_cast<const uint2*>(src + 2 * e1));
+    return make_uint4(a.x, a.y, b.x, b.y);
+  };
+  uint4 qw = make_uint4(0u, 0u, 0u, 0u), kw = qw;
+  if (live && p.qw) qw = load8(p.qw, 0);
+  if (live && p.kw) kw = load8(p.kw, 0);
+  __syncthreads();
 
   const long long jobs = static_cast<long long>(p.T) * p.chunks;
   for (long long job = static_cast<long long>(blockIdx.x) * kRopeWarps + warp; job < jobs;
        job += static_cast<long long>(gridDim.x) * kRopeWarps) {
     const int t = static_cast<int>(job / p.chunks);
     const int first = static_cast<int>(job - static_cast<long long>(t) * p.chunks) * p.iters;
+    const int last = min(first + p.iters, (all + kHeads - 1) / kHeads);
+    auto fetch = [&](int it) {
+      const int h = it * kHeads + sub;
+      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
+      if (live && h < all && it < last) {
+        const bool is_q = h < p.Hq, is_k = h < p.Hq + p.Hkv;
+        const int head = is_q ? h : h - p.Hq - (is_k ? 0 : p.Hkv);
+        raw = load8(is_q ? p.q : is_k ? p.k : p.v,
+                    (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride) * t +
+                        static_cast<long long>(head) * p.D);
+      }
+      return raw;
+    };
+    uint4 next[kAhead];
+#pragma unroll
+    for (int a = 0; a < kAhead; ++a) next[a] = fetch(first + a);
     const int slot = p.slots[t];
     const bool keep = slot >= 0 && slot < p.rows;
-    float c[kPairs], s[kPairs];
+    float c[4], s[4];
 #pragma unroll
-    for (int e = 0; e < kPairs; ++e) {
+    for (int e = 0; e < 4; ++e) {
       c[e] = 1.0f;
       s[e] = 0.0f;
-    }
-    if (rot) {
-#pragma unroll
-      for (int e = 0; e < kPairs; ++e) {
-        const int i = pair0 + e;
+      if (rot) {
+        const int i = 4 * li + e;
         const int axis = (i >= p.sec_end[0]) + (i >= p.sec_end[1]) + (i >= p.sec_end[2]);
         pair_rotation(turn[i], p.positions[static_cast<size_t>(axis) * p.T + t], &c[e], &s[e]);
       }
     }
-    for (int it = first; it < first + p.iters; ++it) {
-      const int h = it * kHeads + sub;
-      const bool is_q = h < p.Hq;
-      const bool is_k = !is_q && h < p.Hq + p.Hkv;
-      const int kv = h - p.Hq - (is_k ? 0 : p.Hkv);   // its KV head when not a query
-      const bool in = live && h < all && (is_q || keep);
-      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-      if (in) {
-        const char* src = static_cast<const char*>(is_q ? p.q : is_k ? p.k : p.v);
-        const long long at = (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride) * t +
-                             static_cast<long long>(is_q ? h : kv) * p.D + d0;
-        raw = __ldcs(reinterpret_cast<const uint4*>(src + 2 * at));
+    for (int it0 = first; it0 < last; it0 += kAhead) {
+      uint4 now[kAhead];
+#pragma unroll
+      for (int a = 0; a < kAhead; ++a) {
+        now[a] = next[a];
+        next[a] = fetch(it0 + kAhead + a);
       }
-      float x[8];
-      widen8(Tag{}, raw, x);
-      float ss = 0.0f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+      for (int a = 0; a < kAhead; ++a) {
+        const int it = it0 + a;
+        if (it >= last) break;
+        const int h = it * kHeads + sub;
+        const bool is_q = h < p.Hq;
+        const bool is_k = !is_q && h < p.Hq + p.Hkv;
+        uint4 raw = now[a];
+        // Steps of values only (the last ones) are copied as they are.
+        if (it * kHeads < p.Hq + p.Hkv) {
+          float x[8];
+          widen8(Tag{}, raw, x);
+          if (p.qw || p.kw) {
+            float ss = 0.0f;
 #pragma unroll
-      for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      const void* w = is_q ? p.qw : is_k ? p.kw : nullptr;
-      if (w && live) {
-        const float r = rsqrtf(ss / static_cast<float>(p.D) + p.eps);
-        float g[8];
-        widen8(Tag{}, __ldg(reinterpret_cast<const uint4*>(static_cast<const char*>(w) + 2 * d0)), g);
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * r * (g[e] + p.w_offset);
-      }
-      float y[8];
-      if constexpr (kInterleaved) {
+            for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (is_q ? p.qw != nullptr : p.kw != nullptr) {
+              const float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+              float g[8];
+              widen8(Tag{}, is_q ? qw : kw, g);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[2 * e] = x[2 * e] * c[e] - x[2 * e + 1] * s[e];
-          y[2 * e + 1] = x[2 * e + 1] * c[e] + x[2 * e] * s[e];
+              for (int e = 0; e < 8; ++e) x[e] = x[e] * r * (g[e] + p.w_offset);
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float& u = x[kInterleaved ? 2 * e : e];
+            float& v = x[kInterleaved ? 2 * e + 1 : e + 4];
+            const float y = u * c[e] - v * s[e];
+            v = v * c[e] + u * s[e];
+            u = y;
+          }
+          if (kQ32 && is_q && live) {
+            float* dst = static_cast<float*>(p.q_out) + (static_cast<size_t>(t) * p.Hq + h) * p.D;
+            *reinterpret_cast<float4*>(dst + e0) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4*>(dst + e1) = make_float4(x[4], x[5], x[6], x[7]);
+          }
+          if (is_q || is_k)
+            raw = make_uint4(pack2<Tag>(x[0], x[1]), pack2<Tag>(x[2], x[3]), pack2<Tag>(x[4], x[5]),
+                             pack2<Tag>(x[6], x[7]));
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float o = __shfl_sync(0xffffffffu, x[e], mate & 31);
-          y[e] = upper ? x[e] * c[e] + o * s[e] : x[e] * c[e] - o * s[e];
+        if (live && h < all && (is_q ? !kQ32 : keep)) {
+          char* base = static_cast<char*>(is_q ? p.q_out : is_k ? p.k_pool : p.v_pool);
+          const size_t row = is_q ? static_cast<size_t>(t) * p.Hq + h
+                                  : static_cast<size_t>(slot) * p.Hkv + (h - p.Hq - (is_k ? 0 : p.Hkv));
+          char* dst = base + 2 * row * p.D;
+          if constexpr (kInterleaved) {
+            *reinterpret_cast<uint4*>(dst + 2 * e0) = raw;
+          } else {
+            *reinterpret_cast<uint2*>(dst + 2 * e0) = make_uint2(raw.x, raw.y);
+            *reinterpret_cast<uint2*>(dst + 2 * e1) = make_uint2(raw.z, raw.w);
+          }
         }
       }
-      if (!in) continue;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = rot ? y[e] : x[e];
-      if (kQ32 && is_q) {
-        const size_t at = (static_cast<size_t>(t) * p.Hq + h) * p.D + d0;
-        float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.q_out) + at);
-        dst[0] = make_float4(y[0], y[1], y[2], y[3]);
-        dst[1] = make_float4(y[4], y[5], y[6], y[7]);
-        continue;
-      }
-      if (is_q || is_k)
-        raw = make_uint4(pack2<Tag>(y[0], y[1]), pack2<Tag>(y[2], y[3]), pack2<Tag>(y[4], y[5]),
-                         pack2<Tag>(y[6], y[7]));
-      char* base = static_cast<char*>(is_q ? p.q_out : is_k ? p.k_pool : p.v_pool);
-      const size_t row = is_q ? static_cast<size_t>(t) * p.Hq + h
-                              : static_cast<size_t>(slot) * p.Hkv + kv;
-      *reinterpret_cast<uint4*>(base + 2 * (row * p.D + d0)) = raw;
     }
   }
 }
