@@ -944,14 +944,16 @@ __global__ void __launch_bounds__(kPxThreads, 1)
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
           if (j == 0) {
             m = top == -INFINITY ? -1e30f : top;   // nothing finite yet: weights of 0
-          } else if (__any_sync(0xffffffffu, top > m + kPxGrow)) {
+          } else if (__any_sync(0xffffffffu, row >= 0 && row < rows && top > m + kPxGrow)) {
+            // Each row by itself: lanes without a row hold anything, and must
+            // not move the others' maxima.
             // The previous tiles' products are done: S of this tile was
             // multiplied after them, or (one stream) the wait below.
             if (NS == 1) {
               if (!(ok = warp_poll(pvdone, (no - 1) & 1, p.timeout_ns))) break;
               tc_fence_after();
             }
-            const float now = fmaxf(m, top), a = ex2(m - now);
+            const float now = top > m + kPxGrow ? top : m, a = ex2(m - now);
             m = now;
             l *= a;
             const uint32_t o_addr = tmem + lane_addr + Shape::O_COL0 + w * D;

@@ -228,3 +228,16 @@ def test_other_streams_graphs_and_reuse_of_the_workspace(gq):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("D,G", [(64, 5), (128, 3), (256, 7)])
+def test_results_do_not_depend_on_earlier_calls(gq, D, G):
+    # Query tiles that are not full, own units of a few rows: what an earlier call left in
+    # shared and tensor memory lies in the other rows.
+    rng = np.random.default_rng(12)
+    x = make(rng, 21, 2 * G, 2, D, 16, "bf16", [1500], [0, 20], list(range(0, 840, 40)))
+    y = make(rng, 40, 8, 2, D, 16, "bf16", [2500], None, [300] * 40, spread=60.0)
+    first = call(gq, x)
+    for _ in range(3):
+        call(gq, y)
+        assert torch.equal(call(gq, x), first)
