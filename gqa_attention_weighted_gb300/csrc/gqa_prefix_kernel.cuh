@@ -356,7 +356,9 @@ struct PxPlan {
     return (len + Shape::KEYS - 1) / Shape::KEYS;
   }
 
-  // By the V warp. A unit takes so many tiles that a CTA gets about four, so
+  // By the V warp. A unit takes so many tiles that a CTA gets about four (two
+  // with one stream, whose units do not overlap: 52 us where it was 55 at 64
+  // sequences behind 32768 rows, 16 + 1 heads of 256), so
   // that the last ones to end are short. The sum of the tiles is made of two
   // halves: it may pass 2^31.
   static __device__ __forceinline__ void make_own(const PrefixParams& p, PxOwn* own) {
@@ -380,7 +382,7 @@ struct PxPlan {
     // Rounded up with a margin for the rounding of the sum: never more than
     // four units a CTA beyond one a sequence and KV head.
     const int each = __float2int_ru(
-        fminf(fmaxf(1.0f, __fdividef(work * 1.00001f, static_cast<float>(4 * gridDim.x))), 1048576.0f));
+        fminf(fmaxf(1.0f, __fdividef(work * 1.00001f, static_cast<float>((Shape::NS == 1 ? 2 : 4) * gridDim.x))), 1048576.0f));
     int units = 0;
 #pragma unroll 1
     for (int k0 = 0; 32 * k0 < seqs; k0 += 32) {
