@@ -193,11 +193,15 @@ __device__ __forceinline__ void pair_rotation(unsigned long long turn64, int pos
 // elements half a rotation apart, or eight adjacent ones (interleaved), so a
 // rotation needs no other lane, and cos and sin are made once a token and part.
 // Elements past the rotation are dealt out the same way and left alone. The
-// squares are summed by shuffles inside the head's L lanes. Bound by HBM for
-// long inputs, by latency for short ones: the loads of the next kAhead steps
-// are under way while a step is worked on. Measured at 16384 tokens of
-// 32 + 8 + 8 heads of 128, bf16: 142 us with eight adjacent elements a lane,
-// whose mates came by shuffles, and one step's loads at a time; 107 us with two.
+// squares are summed by shuffles inside the head's L lanes. The loads of the
+// next kAhead steps are under way while a step is worked on. Short inputs are
+// bound by latency (3 us for one token), long ones by HBM and, nearly as much,
+// by instruction issue (186 instructions a step of 512 bytes, 75 % of the issue
+// slots). Measured at 16384 tokens of 32 + 8 + 8 heads of 128, bf16 (403 MB): 84
+// us; 141 with eight adjacent elements a lane, whose mates came by shuffles, and
+// one step's loads at a time. More loads ahead, next tokens' positions ahead and
+// addresses kept as pointers all measured slower: each costs registers, and so
+// the third CTA of an SM.
 template <typename Tag, int L, bool kInterleaved, bool kQ32>
 __global__ void __launch_bounds__(32 * kRopeWarps) gqa_kv_rope_kernel(const RopeParams p) {
   __shared__ unsigned long long turn[kRopeMaxPairs];
