@@ -173,6 +173,7 @@ extern "C" int gqa_kv_norm_rope_append(
        addr(k_weight)) & 15u)
     return kfail(GQA_AV_ERR_UNSUPPORTED,
                  "q, k, v, q_out, the pools and the weights must be 16-byte aligned");
+  if (T == 1) q_stride = k_stride = v_stride = 0;   // of no meaning for a single token
   if ((q_stride | k_stride | v_stride) & 7)
     return kfail(GQA_AV_ERR_UNSUPPORTED, "token strides must be multiples of 8 elements");
   if (T > 1 && (q_stride < static_cast<int64_t>(Hq) * D || k_stride < static_cast<int64_t>(Hkv) * D ||

@@ -70,6 +70,8 @@ __device__ __forceinline__ long long block_scan(long long x, long long* part, lo
 // memory and then maps its own run of tokens, so one launch needs no exchange
 // between CTAs. The token whose row opens a new block writes the table entry:
 // a new block's first row is always a new token. The sums run in 64 bits.
+// Bound by latency: launch, lengths, table or list entry (4.5 us a call for 256
+// requests of one token, 7.2 for 96 requests with 131 thousand tokens).
 __global__ void __launch_bounds__(kTabThreads) gqa_kv_tables_kernel(const TablesParams p) {
   extern __shared__ int32_t tab_smem[];
   int32_t* start = tab_smem;                 // [B] first token of each request

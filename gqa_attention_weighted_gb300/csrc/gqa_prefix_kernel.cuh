@@ -32,6 +32,16 @@
 // D = 256: O fills half of the tensor memory, so there is one stream with two
 // S buffers and key tiles of 64.
 //
+// Bounds and figures. A prefix key costs 2 * 2 * D * rows operations for 4 * D
+// bytes, so about 270 rows make it as much the tensor cores' work as HBM's; own
+// rows are HBM's. Measured (bf16, blocks of 16, 64 + 8 heads of 128): 256
+// sequences behind 32768 rows, no own rows, 242 us, 1135 TFLOP/s (the tensor pipe
+// waits for weights: within a stream scores, weights and next scores follow one
+// another); 32 sequences of 8192 own rows 174 us, 6.15 TB/s; two sequences behind
+// 512 rows (8 + 2 heads of 64) 11 us, a chain of latencies. Key tiles of 128 keep
+// QK at the full rate (at N = 64 it waits for shared memory: 48 cycles where the
+// product takes 32) but leave no tensor memory for a second S.
+//
 // Warps: 0-3 and 4-7 softmax warpgroups (and the units' ends), 8 issues the
 // MMAs from one thread, 9 makes the plan, hands out units and loads queries and
 // K, 10 loads V (a box of a small block costs its issuing warp some time, so K

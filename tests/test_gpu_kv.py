@@ -196,3 +196,19 @@ def test_step_is_captured_into_a_graph(gq):
     assert slots.tolist() == [17 * 8 + 6, 18 * 8 + 7, 0] and pos.tolist() == [6, 7, 8]
     assert lens.tolist() == [1, 7, 9] and left.tolist() == [19]
     assert torch.equal(pools[1].flatten(0, 1)[slots.long()], x)
+
+
+def test_offsets_past_32_bits_and_a_single_token_of_any_stride(gq):
+    dev, H, D, far = "cuda", 8, 128, 40000
+    x = torch.randn((1, 3 * H * D + 4), device=dev).bfloat16()   # a row of no multiple of 8
+    q, k, v = (x[:, i * H * D:(i + 1) * H * D].unflatten(1, (H, D)) for i in range(3))
+    inv = torch.rand(D // 2, device=dev)
+    big = [torch.empty((far, 64, H, D), dtype=torch.bfloat16, device=dev) for _ in "kv"]
+    small = [torch.zeros((1, 64, H, D), dtype=torch.bfloat16, device=dev) for _ in "kv"]
+    outs = []
+    for pools, slot in ((big, far * 64 - 1), (small, 63)):
+        q_out = torch.zeros((1, H, D), device=dev)
+        gq.gqa_kv_norm_rope_append(q, k, v, i32([77]), i32([slot]), inv, q_out, *pools)
+        outs.append([q_out, pools[0].flatten(0, 1)[slot], pools[1].flatten(0, 1)[slot]])
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    assert torch.equal(outs[0][2], v[0])

@@ -103,6 +103,9 @@ CASES = [
     (3, 8, 8, 128, 16, [1000], None, [40, 0, 1]),                # plain multi-head
     (300, 1, 1, 64, 8, [64], [10, 290], [1] * 300),
     (6, 96, 2, 128, 16, [], None, [100, 0, 3, 17, 129, 64]),     # G = 48: two warps of rows
+    (70, 4, 2, 64, 8, [3 * i for i in range(32)], [2 * i for i in range(33)],
+     [i % 5 for i in range(70)]),                                # 32 groups, some without rows
+    (1500, 2, 1, 64, 8, [40], [200, 1400], [i % 11 for i in range(1500)]),
 ]
 
 
@@ -241,3 +244,21 @@ def test_results_do_not_depend_on_earlier_calls(gq, D, G):
     for _ in range(3):
         call(gq, y)
         assert torch.equal(call(gq, x), first)
+
+
+def test_offsets_past_32_bits(gq):
+    # The same rows in a small pool and at the far end of one of 5 GB: equal bits.
+    rng = np.random.default_rng(13)
+    x = make(rng, 3, 16, 8, 128, 64, "bf16", [200], None, [70, 0, 129])
+    near = call(gq, x)
+    nb, far = x["k"].shape[0], 40000
+    big = [torch.empty((far, 64, 8, 128), dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    for b, n in zip(big, "kv"):
+        b[far - nb:] = x[n].cuda()
+    t = {n: i32(x[n]) for n in ("ptab", "plens", "starts", "tab", "lens")}
+    for n in ("ptab", "tab"):
+        t[n] = torch.where((t[n] >= 0) & (t[n] < nb), t[n] + (far - nb), t[n])
+    out = torch.zeros_like(near)
+    gq.gqa_prefix_attn_decode(x["q"].cuda(), *big, t["ptab"], t["plens"], t["starts"], t["tab"],
+                              t["lens"], out)
+    assert torch.equal(out, near)
