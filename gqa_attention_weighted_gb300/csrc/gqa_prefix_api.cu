@@ -93,11 +93,15 @@ PrefixKernel pick_main(int D) {
   return D == 64 ? gqa_prefix_kernel<Tag, 64>
                  : D == 128 ? gqa_prefix_kernel<Tag, 128> : gqa_prefix_kernel<Tag, 256>;
 }
-template <typename Tag>
+template <typename Tag, int U>
 PrefixKernel pick_combine(int D) {
-  return D == 64 ? gqa_prefix_combine_kernel<Tag, 64>
-                 : D == 128 ? gqa_prefix_combine_kernel<Tag, 128>
-                            : gqa_prefix_combine_kernel<Tag, 256>;
+  return D == 64 ? gqa_prefix_combine_kernel<Tag, 64, U>
+                 : D == 128 ? gqa_prefix_combine_kernel<Tag, 128, U>
+                            : gqa_prefix_combine_kernel<Tag, 256, U>;
+}
+template <typename Tag>
+PrefixKernel pick_combine(int D, bool waves) {
+  return waves ? pick_combine<Tag, 4>(D) : pick_combine<Tag, 8>(D);
 }
 int smem_bytes(int D) {
   return D == 64 ? PxShape<64>::SMEM : D == 128 ? PxShape<128>::SMEM : PxShape<256>::SMEM;
@@ -280,8 +284,10 @@ extern "C" int gqa_prefix_attn_decode(
   void* args[] = {&p};
   e = launch_pdl(k, sms, kPxThreads, smem_bytes(D), stream, args);
   if (e != cudaSuccess) return pfail_cuda(e, "attention kernel launch");
-  k = reinterpret_cast<const void*>(bf ? pick_combine<Bf16Tag>(D) : pick_combine<Fp16Tag>(D));
   const int parts = (p.G * (D / 4) + kPxCombineThreads - 1) / kPxCombineThreads;
+  const bool waves = static_cast<long long>(B) * Hkv * parts > 5LL * sms;
+  k = reinterpret_cast<const void*>(bf ? pick_combine<Bf16Tag>(D, waves)
+                                       : pick_combine<Fp16Tag>(D, waves));
   e = launch_pdl(k, B * Hkv * parts, kPxCombineThreads, 0, stream, args);
   if (e != cudaSuccess) {
     cudaMemsetAsync(&p.head->next, 0, sizeof p.head->next, stream);   // the combine's job

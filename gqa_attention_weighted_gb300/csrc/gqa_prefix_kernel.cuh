@@ -1100,10 +1100,13 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 // out row = sum over its slots of 2^(m_s - M) O_s / sum of 2^(m_s - M) l_s, the
 // prefix's splits first, then the sequence's own, with a running maximum. A
 // CTA takes 128 of the (row, 4 columns) of one sequence and KV head, a thread
-// one; the slots come from L2 eight at a time, since a row may have dozens.
+// one. A row may have dozens of slots, and a thread waits for L2 at every step:
+// it takes U slots a step, 8 where all CTAs fit on the SMs at once (five an SM;
+// 16 sequences behind 8192 rows: 25 us, with 4 slots 28), 4 where they come in
+// waves, of which more fit then (256 behind 32768: 295 us, with 8 slots 299).
 constexpr int kPxCombineThreads = 128;
 
-template <typename Tag, int D>
+template <typename Tag, int D, int U>
 __global__ void __launch_bounds__(kPxCombineThreads)
     gqa_prefix_combine_kernel(const __grid_constant__ PrefixParams p) {
   using Shape = PxShape<D>;
@@ -1149,7 +1152,6 @@ __global__ void __launch_bounds__(kPxCombineThreads)
     o1 = reinterpret_cast<const float4*>(p.own_o) + (tile * (D / 4) + c) * p.G + g;
     m1 = p.own_ml + tile * p.G + g;
   }
-  constexpr int U = 8;
   for (int s = 0; s < n0 + n1; s += U) {
     float2 m[U];
     float4 v[U];
