@@ -35,7 +35,7 @@
 // Bounds and figures. A prefix key costs 2 * 2 * D * rows operations for 4 * D
 // bytes, so about 270 rows make it as much the tensor cores' work as HBM's; own
 // rows are HBM's. Measured (bf16, blocks of 16, 64 + 8 heads of 128): 256
-// sequences behind 32768 rows, no own rows, 242 us, 1135 TFLOP/s (the tensor pipe
+// sequences behind 32768 rows, no own rows, 237 us, 1160 TFLOP/s (the tensor pipe
 // waits for weights: within a stream scores, weights and next scores follow one
 // another); 32 sequences of 8192 own rows 174 us, 6.15 TB/s; two sequences behind
 // 512 rows (8 + 2 heads of 64) 11 us, a chain of latencies. Key tiles of 128 keep
@@ -99,7 +99,6 @@ struct PxHeader {
   unsigned status;
   int next;                       // units handed out past the first of each CTA
   int own_tiles;                  // key tiles of a sequence's own unit
-  int pad[61];
   PxGroup group[kPxMaxGroups];
   int own_base[kPxMaxB];          // first own unit (slot) of each sequence
 };
@@ -454,7 +453,10 @@ struct PxPlan {
     // How to cut the prefixes: each lane costs one choice of pairs or single
     // query tiles and of the key tiles a split takes (1 to 8 units a CTA), from
     // the time that the units take if all CTAs stay busy, own units included,
-    // and from the CTA with the most prefix units.
+    // and from the CTA with the most prefix units, the latter 1.3 times: units
+    // that nearly fill the call leave nothing to even out what the costs miss
+    // (256 sequences behind 32768 rows: 289 us, without it 296; at 1.15 as
+    // without, at 1.6 as with).
     const bool pairs = Shape::NS == 2 && (lane & 1);
     float w = 0.0f;                     // key tiles x query tiles (or pairs)
     for (int g = 0; g < p.P; ++g) {
@@ -476,7 +478,7 @@ struct PxPlan {
     const float one = static_cast<float>(chunk) * c + p.c_unit;
     const float all = __fdividef(w * c + units * p.c_unit + own->work * p.c_own, static_cast<float>(n));
     const float rounds = ceilf(__fdividef(units - 0.5f, static_cast<float>(n)));
-    const float est = units <= static_cast<float>(p.prefix_slots) ? fmaxf(all, rounds * one) : INFINITY;
+    const float est = units <= static_cast<float>(p.prefix_slots) ? fmaxf(all, 1.3f * rounds * one) : INFINITY;
     // Costs are positive, so their bit patterns are ordered like them.
     const unsigned best = __reduce_min_sync(0xffffffffu, __float_as_uint(est));
     const int src = __ffs(__ballot_sync(0xffffffffu, __float_as_uint(est) == best)) - 1;
