@@ -99,10 +99,11 @@ def _load() -> ctypes.CDLL:
     lib.gqa_kv_last_error.restype = ctypes.c_char_p
     lib.gqa_prefix_attn_decode.argtypes = [P] * 9 + [I] * 10 + [F, P]
     lib.gqa_prefix_device_status.argtypes = [P, I]
+    lib.gqa_prefix_selftest_wait_timeout.argtypes = [P] * 9 + [I] * 10 + [F, ctypes.c_longlong, I, P]
     lib.gqa_prefix_last_error.argtypes = []
     lib.gqa_prefix_last_error.restype = ctypes.c_char_p
     for f in ("gqa_kv_tables", "gqa_kv_norm_rope_append", "gqa_prefix_attn_decode",
-              "gqa_prefix_device_status"):
+              "gqa_prefix_device_status", "gqa_prefix_selftest_wait_timeout"):
         getattr(lib, f).restype = I
     for f in ("gqa_attn_decode", "gqa_attn_decode_tuned", "gqa_attn_plan", "gqa_attn_device_status"):
         getattr(lib, f).restype = I

@@ -20,8 +20,6 @@
 namespace gqa_av {
 namespace {
 
-constexpr long long kPxTimeoutNs = 2000000000LL;   // 2 s bound on every mbarrier wait
-
 thread_local std::string g_px_error;
 
 int pfail(int status, const char* fmt, ...) {
@@ -209,18 +207,11 @@ cudaError_t launch_pdl(const void* fn, int grid, int block, size_t smem, cudaStr
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
-}  // namespace
-}  // namespace gqa_av
-
-using namespace gqa_av;
-
-extern "C" int gqa_prefix_attn_decode(
-    const void* q, const void* k_pool, const void* v_pool, const int32_t* prefix_table,
-    const int32_t* prefix_lens, const int32_t* group_start, const int32_t* block_table,
-    const int32_t* seq_lens, void* out, int B, int P, int Hq, int Hkv, int D, int kv_dtype,
-    int block_size, int num_blocks, int max_prefix_blocks, int max_blocks, float scale,
-    void* stream_) {
-  g_px_error.clear();
+int decode(const void* q, const void* k_pool, const void* v_pool, const int32_t* prefix_table,
+           const int32_t* prefix_lens, const int32_t* group_start, const int32_t* block_table,
+           const int32_t* seq_lens, void* out, int B, int P, int Hq, int Hkv, int D, int kv_dtype,
+           int block_size, int num_blocks, int max_prefix_blocks, int max_blocks, float scale,
+           long long wait_ns, unsigned withhold_from, cudaStream_t stream) {
   int rc = check_args(q, k_pool, v_pool, prefix_table, prefix_lens, group_start, block_table,
                       seq_lens, out, B, P, Hq, Hkv, D, kv_dtype, block_size, num_blocks,
                       max_prefix_blocks, max_blocks, scale);
@@ -229,7 +220,6 @@ extern "C" int gqa_prefix_attn_decode(
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return pfail_cuda(e, "cudaGetDevice");
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
 
   PrefixParams p;
   p.prefix_table = prefix_table; p.prefix_lens = prefix_lens; p.group_start = group_start;
@@ -257,7 +247,8 @@ extern "C" int gqa_prefix_attn_decode(
   p.c_tile = D == 64 ? 700.0f : 1300.0f;
   p.c_own = D == 64 ? 1400.0f : 2800.0f;
   p.c_unit = 4000.0f;
-  p.timeout_ns = kPxTimeoutNs;
+  p.timeout_ns = wait_ns;
+  p.withhold_from = withhold_from;
 
   const int ns = D == 256 ? 1 : 2;
   const size_t q_tiles = static_cast<size_t>((B + p.TB - 1) / p.TB + std::min(P, B)) * Hkv;
@@ -296,6 +287,42 @@ extern "C" int gqa_prefix_attn_decode(
   return GQA_AV_OK;
 }
 
+}  // namespace
+}  // namespace gqa_av
+
+using namespace gqa_av;
+
+extern "C" int gqa_prefix_attn_decode(
+    const void* q, const void* k_pool, const void* v_pool, const int32_t* prefix_table,
+    const int32_t* prefix_lens, const int32_t* group_start, const int32_t* block_table,
+    const int32_t* seq_lens, void* out, int B, int P, int Hq, int Hkv, int D, int kv_dtype,
+    int block_size, int num_blocks, int max_prefix_blocks, int max_blocks, float scale,
+    void* stream) {
+  g_px_error.clear();
+  return decode(q, k_pool, v_pool, prefix_table, prefix_lens, group_start, block_table, seq_lens,
+                out, B, P, Hq, Hkv, D, kv_dtype, block_size, num_blocks, max_prefix_blocks,
+                max_blocks, scale, kPxTimeoutNs, ~0u, static_cast<cudaStream_t>(stream));
+}
+
+// The K warp issues no query load from number `withhold_from` of each CTA on
+// (nothing of it is in flight), so the MMA warp's wait for it runs out, and
+// then the others' waits; all leave as on any timeout.
+extern "C" int gqa_prefix_selftest_wait_timeout(
+    const void* q, const void* k_pool, const void* v_pool, const int32_t* prefix_table,
+    const int32_t* prefix_lens, const int32_t* group_start, const int32_t* block_table,
+    const int32_t* seq_lens, void* out, int B, int P, int Hq, int Hkv, int D, int kv_dtype,
+    int block_size, int num_blocks, int max_prefix_blocks, int max_blocks, float scale,
+    long long wait_ns, int withhold_from, void* stream) {
+  g_px_error.clear();
+  if (wait_ns < 100000 || wait_ns > kPxTimeoutNs || withhold_from < 0)
+    return pfail(GQA_AV_ERR_INVALID, "wait_ns=%lld must be in [100000, %lld], withhold_from=%d not "
+                 "negative", wait_ns, kPxTimeoutNs, withhold_from);
+  return decode(q, k_pool, v_pool, prefix_table, prefix_lens, group_start, block_table, seq_lens,
+                out, B, P, Hq, Hkv, D, kv_dtype, block_size, num_blocks, max_prefix_blocks,
+                max_blocks, scale, wait_ns, static_cast<unsigned>(withhold_from),
+                static_cast<cudaStream_t>(stream));
+}
+
 extern "C" int gqa_prefix_device_status(void* stream_, int clear) {
   g_px_error.clear();
   int dev = 0;
@@ -303,18 +330,12 @@ extern "C" int gqa_prefix_device_status(void* stream_, int clear) {
   if (e != cudaSuccess) return pfail_cuda(e, "cudaGetDevice");
   e = cudaStreamSynchronize(static_cast<cudaStream_t>(stream_));
   if (e != cudaSuccess) return pfail_cuda(e, "cudaStreamSynchronize");
-  char* base = nullptr;
-  {
-    std::lock_guard<std::mutex> lk(g_px_mu);
-    auto it = g_px_ws.find(dev);
-    if (it != g_px_ws.end()) base = it->second.base;
-  }
-  if (!base) return GQA_AV_OK;
   unsigned word = 0;
-  e = cudaMemcpy(&word, base, sizeof word, cudaMemcpyDeviceToHost);
+  e = cudaMemcpyFromSymbol(&word, px_status, sizeof word);
   if (e != cudaSuccess) return pfail_cuda(e, "reading the status word");
   if (word && clear) {
-    e = cudaMemset(base, 0, sizeof word);
+    const unsigned zero = 0;
+    e = cudaMemcpyToSymbol(px_status, &zero, sizeof zero);
     if (e != cudaSuccess) return pfail_cuda(e, "clearing the status word");
   }
   if (word)

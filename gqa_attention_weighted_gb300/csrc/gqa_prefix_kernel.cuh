@@ -70,6 +70,13 @@ constexpr int kPxMaxB = 4096;
 constexpr int kPxSegs = 2;             // unit descriptors in flight
 constexpr float kPxGrow = 8.0f;        // log2 of the growth of a maximum that is tolerated
 constexpr unsigned kErrPxLoad = 16u, kErrPxMma = 32u, kErrPxSoftmax = 64u;
+constexpr long long kPxTimeoutNs = 2000000000LL;   // bound of every wait; also of the last ones,
+                                                   // for copies and MMAs in flight
+
+// Set by waits that run out, read by gqa_prefix_device_status. One word a device
+// for the life of the process: a workspace may be outgrown while captured graphs
+// still run in it, and what they report must be found.
+__device__ unsigned px_status;
 
 template <int D>
 struct PxShape {
@@ -96,7 +103,6 @@ struct PxGroup {
   int base;           // its first unit
 };
 struct PxHeader {
-  unsigned status;
   int next;                       // units handed out past the first of each CTA
   int own_tiles;                  // key tiles of a sequence's own unit
   PxGroup group[kPxMaxGroups];
@@ -124,6 +130,7 @@ struct alignas(64) PrefixParams {
   int prefix_slots;               // bound on the prefix units
   float c_pair, c_tile, c_own, c_unit;   // plan: cost of a key tile of each kind and of a unit
   long long timeout_ns;
+  unsigned withhold_from;         // self-test: query loads from this one of a CTA on are not issued
 };
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
@@ -634,7 +641,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
   grid_dependency_wait();
   grid_launch_dependents();
   const bool aligned = (base_s & 1023u) == 0;   // the tiles need it; dynamic memory starts so
-  if (!aligned && threadIdx.x == 0) atomicOr(&p.head->status, kErrPxLoad);
+  if (!aligned && threadIdx.x == 0) atomicOr(&px_status, kErrPxLoad);
   // kOwn: the second stream's rows lie in lanes of other warps than the first's
   // where they fit, so that the two softmax warps sit on different schedulers.
   const int own_shift = p.G <= 32 ? 32 : p.G <= 64 ? 64 : 0;
@@ -730,6 +737,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             const int buf = fills % Shape::QBUF;
             ok = warp_poll(qempty0 + 8 * buf, ((fills / Shape::QBUF) & 1) ^ 1, p.timeout_ns);
             if (!ok) break;
+            if (fills >= p.withhold_from) continue;
             const uint32_t bar = qfull0 + 8 * buf;
             if (lane == 16 + buf) held = 1 + ((fills / Shape::QBUF) & 1);
             expect_one(leader, bar, (own ? p.G : p.TB * p.G) * 128 * PARTS);
@@ -764,9 +772,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       if (is_k && blockIdx.x == gridDim.x - 1) plan.write(p, own_plan);
       if (!ok) {
         // This warp's copies in flight land before the CTA leaves.
-        if (lane == 0) atomicOr(&p.head->status, kErrPxLoad);
-        if (held && lane < STAGES) mbar_wait(full0 + 8 * lane, held - 1, p.timeout_ns);
-        if (held && lane >= 16) mbar_wait(qfull0 + 8 * (lane - 16), held - 1, p.timeout_ns);
+        if (lane == 0) atomicOr(&px_status, kErrPxLoad);
+        if (held && lane < STAGES) mbar_wait(full0 + 8 * lane, held - 1, kPxTimeoutNs);
+        if (held && lane >= 16) mbar_wait(qfull0 + 8 * (lane - 16), held - 1, kPxTimeoutNs);
         __syncwarp();
       }
     } else if (aligned && warp == kPxMmaWarp) {
@@ -854,9 +862,9 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         done1 += n1;
       }
       if (!ok) {
-        if (lane == 0) atomicOr(&p.head->status, kErrPxMma);
+        if (lane == 0) atomicOr(&px_status, kErrPxMma);
         commit_one(leader, drain);
-        mbar_wait(drain, 0, p.timeout_ns);
+        mbar_wait(drain, 0, kPxTimeoutNs);
       }
       __syncwarp();
     }
@@ -1087,7 +1095,7 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         }
       }
     }
-    if (!ok && lane == 0) atomicOr(&p.head->status, kErrPxSoftmax);
+    if (!ok && lane == 0) atomicOr(&px_status, kErrPxSoftmax);
   }
   __syncwarp();
   tc_fence_before();

@@ -68,10 +68,28 @@ int gqa_prefix_attn_decode(const void *q, const void *k_pool, const void *v_pool
                            int D, int kv_dtype, int block_size, int num_blocks,
                            int max_prefix_blocks, int max_blocks, float scale, void *stream);
 
-/* Synchronise `stream`, then read the call's device status word (set when a
- * bounded wait inside a kernel runs out): GQA_AV_OK or
- * GQA_AV_ERR_DEVICE_TIMEOUT; with clear != 0 the word is reset. */
+/* Synchronise `stream`, then read the device's status word (set when a bounded
+ * wait inside a kernel runs out, in any call or graph replay on the device):
+ * GQA_AV_OK or GQA_AV_ERR_DEVICE_TIMEOUT; with clear != 0 the word is reset. */
 int gqa_prefix_device_status(void *stream, int clear);
+
+/*
+ * Self-test of that report: the decode call with bounded waits of wait_ns
+ * (100 us to 2 s) instead of 2 s, and with every CTA leaving out its query
+ * loads from number withhold_from on (nothing of them is ever issued). The
+ * waits for them run out, the warps set the status word, wait for their own
+ * copies and products in flight and leave; no GPU fault, trap or hang is
+ * caused. `out` is left unspecified. Returns GQA_AV_OK once launched;
+ * gqa_prefix_device_status then reports GQA_AV_ERR_DEVICE_TIMEOUT if a CTA had
+ * that many query loads (with withhold_from 0: if any sequence has rows).
+ */
+int gqa_prefix_selftest_wait_timeout(const void *q, const void *k_pool, const void *v_pool,
+                                     const int32_t *prefix_table, const int32_t *prefix_lens,
+                                     const int32_t *group_start, const int32_t *block_table,
+                                     const int32_t *seq_lens, void *out, int B, int P, int Hq,
+                                     int Hkv, int D, int kv_dtype, int block_size, int num_blocks,
+                                     int max_prefix_blocks, int max_blocks, float scale,
+                                     long long wait_ns, int withhold_from, void *stream);
 
 /* Message of the calling thread's last error of these calls ("" if none). */
 const char *gqa_prefix_last_error(void);

@@ -89,3 +89,11 @@ def test_oracle_agrees_with_the_contiguous_one():
     one, _ = gqa_prefix.attention(q[:1].astype(np.float64), *pools, np.array([[0]]), [8], None,
                                   np.array([[1, 2]]), [16], 0.3)
     assert np.allclose(one[0], ref[0], atol=1e-12)
+
+
+@pytest.mark.parametrize("wait_ns,withhold", [(99999, 0), (2000000001, 0), (-1, 0), (200000, -1)])
+def test_selftest_host_checks(native, wait_ns, withhold):
+    rc = native.lib.gqa_prefix_selftest_wait_timeout(*CALL.values(), wait_ns, withhold, None)
+    assert rc == 1 and b"wait_ns" in native.lib.gqa_prefix_last_error()
+    rc = native.lib.gqa_prefix_selftest_wait_timeout(*dict(CALL, D=96).values(), 200000, 0, None)
+    assert rc == 2
