@@ -25,7 +25,8 @@ _BINDING = ("gqa_av_decode", "gqa_av_decode_per_head", "gqa_av_decode_tuned",
             "gqa_qk_softmax_decode", "gqa_qk_device_status", "gqa_av_decode_paged",
             "gqa_attn_decode", "gqa_attn_plan", "gqa_attn_device_status",
             "gqa_kv_tables", "gqa_kv_norm_rope_append", "GQA_KV_F32",
-            "gqa_prefix_attn_decode", "gqa_prefix_device_status")
+            "gqa_prefix_attn_decode", "gqa_prefix_device_status",
+            "gqa_prefix_release_graph_workspaces")
 
 
 def __getattr__(name):

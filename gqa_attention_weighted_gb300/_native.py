@@ -99,11 +99,13 @@ def _load() -> ctypes.CDLL:
     lib.gqa_kv_last_error.restype = ctypes.c_char_p
     lib.gqa_prefix_attn_decode.argtypes = [P] * 9 + [I] * 10 + [F, P]
     lib.gqa_prefix_device_status.argtypes = [P, I]
+    lib.gqa_prefix_release_graph_workspaces.argtypes = []
     lib.gqa_prefix_selftest_wait_timeout.argtypes = [P] * 9 + [I] * 10 + [F, ctypes.c_longlong, I, P]
     lib.gqa_prefix_last_error.argtypes = []
     lib.gqa_prefix_last_error.restype = ctypes.c_char_p
     for f in ("gqa_kv_tables", "gqa_kv_norm_rope_append", "gqa_prefix_attn_decode",
-              "gqa_prefix_device_status", "gqa_prefix_selftest_wait_timeout"):
+              "gqa_prefix_device_status", "gqa_prefix_release_graph_workspaces",
+              "gqa_prefix_selftest_wait_timeout"):
         getattr(lib, f).restype = I
     for f in ("gqa_attn_decode", "gqa_attn_decode_tuned", "gqa_attn_plan", "gqa_attn_device_status"):
         getattr(lib, f).restype = I
@@ -496,7 +498,9 @@ def gqa_prefix_attn_decode(q, k_pool, v_pool, prefix_table, prefix_lens, group_s
     group's ``prefix_table[p]`` (group p: ``group_start[p] <= b < group_start[p + 1]``; None: one
     group of all) and to its own ``seq_lens[b]`` rows of ``block_table[b]``. ``prefix_table`` None:
     no shared prefixes; ``block_table`` None: no own rows. q and out are [B,Hq,D] of the pools' type
-    (scale defaults to 1/sqrt(D)); writes and returns ``out``."""
+    (scale defaults to 1/sqrt(D)); writes and returns ``out``. Calls on different streams and
+    replays of different graphs may overlap: each stream, and each capture, has a workspace of its
+    own."""
     num_blocks, block_size, Hkv, D = _pools(k_pool, v_pool)
     dtype = k_pool.dtype
     if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape:
@@ -533,3 +537,9 @@ def gqa_prefix_attn_decode(q, k_pool, v_pool, prefix_table, prefix_lens, group_s
 
 def gqa_prefix_device_status(stream=None, clear: bool = True) -> None:
     _check_prefix(lib.gqa_prefix_device_status(_stream_handle(stream), 1 if clear else 0))
+
+
+def gqa_prefix_release_graph_workspaces() -> None:
+    """Free what captured ``gqa_prefix_attn_decode`` calls hold. No graph that was captured before
+    may be replayed afterwards."""
+    _check_prefix(lib.gqa_prefix_release_graph_workspaces())

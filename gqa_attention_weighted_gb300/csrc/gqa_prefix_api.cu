@@ -11,8 +11,11 @@
 #include <cstdarg>
 #include <cstdio>
 #include <map>
+#include <memory>
 #include <mutex>
-#include <string>
+#include <new>
+#include <tuple>
+#include <vector>
 
 #include "gqa_prefix.h"
 #include "gqa_prefix_kernel.cuh"
@@ -20,15 +23,13 @@
 namespace gqa_av {
 namespace {
 
-thread_local std::string g_px_error;
+thread_local char g_px_error[512];
 
 int pfail(int status, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
+  vsnprintf(g_px_error, sizeof g_px_error, fmt, ap);
   va_end(ap);
-  g_px_error = buf;
   return status;
 }
 
@@ -105,67 +106,125 @@ int smem_bytes(int D) {
   return D == 64 ? PxShape<64>::SMEM : D == 128 ? PxShape<128>::SMEM : PxShape<256>::SMEM;
 }
 
-struct Ws {
+// Workspaces. A call's units, plan and partial results lie in device memory
+// until its combine has run, so calls that may run at the same time must not
+// share a buffer. One belongs to each stream of uncaptured calls (which the
+// stream orders), and one to each stream of a capture into a graph: replays of
+// a graph follow one another, but may overlap with anything else. The latter
+// are kept until the caller says that the graphs are gone: a graph that owns
+// its buffer as a user object tells so by itself, but then each of its launches
+// holds the host up until the one before has ended (measured: 2 us a replay
+// become 13 to 45).
+struct Owner {
+  int dev;
+  const void* stream;
+  unsigned long long capture;    // 0: uncaptured
+  bool operator<(const Owner& o) const {
+    return std::tie(dev, stream, capture) < std::tie(o.dev, o.stream, o.capture);
+  }
+};
+struct Workspace {
+  std::mutex mu;                 // held until a call's kernels are launched: the stream's order
   char* base = nullptr;
   size_t bytes = 0;
+  std::vector<char*> outgrown;   // by a capture, whose earlier calls use them
 };
 std::mutex g_px_mu;
-std::map<int, Ws> g_px_ws;
+std::map<Owner, std::unique_ptr<Workspace>> g_px_ws;
 
-// The device's workspace, grown to `need` bytes. Outgrown buffers are kept: a
-// captured graph may hold their addresses.
-int workspace(int dev, size_t need, cudaStream_t stream, char** out) {
-  std::lock_guard<std::mutex> lk(g_px_mu);
-  Ws& w = g_px_ws[dev];
-  if (w.bytes < need) {
-    cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-    cudaError_t e = cudaStreamIsCapturing(stream, &cs);
-    if (e != cudaSuccess) return pfail_cuda(e, "cudaStreamIsCapturing");
-    if (cs != cudaStreamCaptureStatusNone)
-      return pfail(GQA_AV_ERR_NOMEM,
-                   "workspace must grow to %zu B but the stream is capturing; make one call with "
-                   "the largest shape before capture",
-                   need);
-    const size_t bytes = std::max(need, w.bytes + w.bytes / 2);
-    void* p = nullptr;
-    e = cudaMalloc(&p, bytes);
-    if (e != cudaSuccess) {
-      cudaGetLastError();
-      return pfail(GQA_AV_ERR_NOMEM, "cudaMalloc(%zu) failed: %s", bytes, cudaGetErrorString(e));
-    }
-    e = cudaMemset(p, 0, sizeof(PxHeader));
-    if (e == cudaSuccess) e = cudaDeviceSynchronize();
-    if (e != cudaSuccess) {
-      cudaFree(p);
-      return pfail_cuda(e, "zeroing the workspace header");
-    }
-    w.base = static_cast<char*>(p);
-    w.bytes = bytes;
+// Allocation is allowed while a stream is capturing in this mode of the thread.
+struct RelaxedCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// Grows a workspace, whose lock is held, to `need` bytes. The new one's header
+// is zeroed on return.
+int grow(Workspace* w, bool capturing, size_t need, cudaStream_t stream) {
+  if (w->bytes >= need) return GQA_AV_OK;
+  const size_t bytes = capturing ? need : std::max(need, w->bytes + w->bytes / 2);
+  w->outgrown.reserve(w->outgrown.size() + 1);
+  RelaxedCapture relaxed;
+  void* p = nullptr;
+  cudaError_t e = cudaMalloc(&p, bytes);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return pfail(GQA_AV_ERR_NOMEM, "cudaMalloc(%zu) failed: %s", bytes, cudaGetErrorString(e));
   }
-  *out = w.base;
+  cudaStream_t own = nullptr;    // not the legacy stream: others may be capturing
+  e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
+  if (e == cudaSuccess) {
+    e = cudaMemsetAsync(p, 0, sizeof(PxHeader), own);
+    if (e == cudaSuccess) e = cudaStreamSynchronize(own);
+    cudaStreamDestroy(own);
+  }
+  if (e == cudaSuccess && w->base && !capturing) {
+    e = cudaStreamSynchronize(stream);   // calls under way use the old one
+    if (e == cudaSuccess) cudaFree(w->base);
+  }
+  if (e != cudaSuccess) {
+    cudaFree(p);
+    return pfail_cuda(e, "setting the workspace up");
+  }
+  if (w->base && capturing) w->outgrown.push_back(w->base);
+  w->base = static_cast<char*>(p);
+  w->bytes = bytes;
   return GQA_AV_OK;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 g_px_encode = nullptr;
+// The workspace that a call on `stream` uses. Those of uncaptured calls are
+// never taken away, so a thread remembers its last one.
+int find_workspace(int dev, cudaStream_t stream, bool* capturing, Workspace** out) {
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(stream, &cs);
+  if (e == cudaSuccess && cs == cudaStreamCaptureStatusInvalidated)
+    e = cudaErrorStreamCaptureInvalidated;
+  if (e != cudaSuccess) return pfail_cuda(e, "cudaStreamIsCapturing");
+  *capturing = cs == cudaStreamCaptureStatusActive;
+  static thread_local char per_thread;   // each thread's default stream has the same handle
+  const void* key = stream == cudaStreamPerThread ? static_cast<const void*>(&per_thread)
+                    : stream == cudaStreamLegacy  ? nullptr
+                                                  : static_cast<const void*>(stream);
+  static thread_local Owner last{-1, nullptr, 0};
+  static thread_local Workspace* last_ws = nullptr;
+  if (!*capturing && last.dev == dev && last.stream == key) {
+    *out = last_ws;
+    return GQA_AV_OK;
+  }
+  unsigned long long id = 0;
+  if (*capturing) {
+    e = cudaStreamGetCaptureInfo(stream, &cs, &id, nullptr, nullptr, nullptr, nullptr);
+    if (e != cudaSuccess) return pfail_cuda(e, "cudaStreamGetCaptureInfo");
+  }
+  const Owner owner{dev, key, id};
+  std::lock_guard<std::mutex> lk(g_px_mu);
+  std::unique_ptr<Workspace>& w = g_px_ws[owner];
+  if (!w) w = std::make_unique<Workspace>();
+  *out = w.get();
+  if (!*capturing) {
+    last = owner;
+    last_ws = w.get();
+  }
+  return GQA_AV_OK;
+}
 
 // A map over 16-bit elements: `rank` dimensions, boxes 64 elements wide in the
 // 128-byte swizzle. What lies outside reads as zeros.
 int encode(CUtensorMap* m, const void* x, int rank, const cuuint64_t* dims,
            const cuuint64_t* strides, const cuuint32_t* box, const char* what) {
-  {
-    std::lock_guard<std::mutex> lk(g_px_mu);
-    if (!g_px_encode) {
-      void* f = nullptr;
-      cudaDriverEntryPointQueryResult q;
-      cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
-                                                       cudaEnableDefault, &q);
-      if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !f)
-        return pfail(GQA_AV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-      g_px_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }
-  }
+  static const PFN_cuTensorMapEncodeTiled_v12000 encode_tiled = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
+                                                     cudaEnableDefault, &q);
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(
+        e == cudaSuccess && q == cudaDriverEntryPointSuccess ? f : nullptr);
+  }();
+  if (!encode_tiled)
+    return pfail(GQA_AV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
   const cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = g_px_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(x), dims,
+  CUresult r = encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(x), dims,
                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -211,7 +270,7 @@ int decode(const void* q, const void* k_pool, const void* v_pool, const int32_t*
            const int32_t* prefix_lens, const int32_t* group_start, const int32_t* block_table,
            const int32_t* seq_lens, void* out, int B, int P, int Hq, int Hkv, int D, int kv_dtype,
            int block_size, int num_blocks, int max_prefix_blocks, int max_blocks, float scale,
-           long long wait_ns, unsigned withhold_from, cudaStream_t stream) {
+           long long wait_ns, unsigned withhold_from, cudaStream_t stream) try {
   int rc = check_args(q, k_pool, v_pool, prefix_table, prefix_lens, group_start, block_table,
                       seq_lens, out, B, P, Hq, Hkv, D, kv_dtype, block_size, num_blocks,
                       max_prefix_blocks, max_blocks, scale);
@@ -259,8 +318,12 @@ int decode(const void* q, const void* k_pool, const void* v_pool, const int32_t*
   const size_t at_pm = at_po + prefix_slots * ns * 128 * D * 4;
   const size_t at_oo = at_pm + prefix_slots * ns * 128 * 8;
   const size_t at_om = at_oo + up256(own_slots * p.G * D * 4);
-  char* base = nullptr;
-  if ((rc = workspace(dev, at_om + own_slots * p.G * 8, stream, &base))) return rc;
+  bool capturing = false;
+  Workspace* ws = nullptr;
+  if ((rc = find_workspace(dev, stream, &capturing, &ws))) return rc;
+  std::lock_guard<std::mutex> lk(ws->mu);
+  if ((rc = grow(ws, capturing, at_om + own_slots * p.G * 8, stream))) return rc;
+  char* base = ws->base;
   p.head = reinterpret_cast<PxHeader*>(base);
   p.prefix_o = reinterpret_cast<float*>(base + at_po);
   p.prefix_ml = reinterpret_cast<float2*>(base + at_pm);
@@ -285,6 +348,8 @@ int decode(const void* q, const void* k_pool, const void* v_pool, const int32_t*
     return pfail_cuda(e, "combine kernel launch");
   }
   return GQA_AV_OK;
+} catch (const std::bad_alloc&) {
+  return pfail(GQA_AV_ERR_NOMEM, "out of host memory");
 }
 
 }  // namespace
@@ -298,7 +363,7 @@ extern "C" int gqa_prefix_attn_decode(
     const int32_t* seq_lens, void* out, int B, int P, int Hq, int Hkv, int D, int kv_dtype,
     int block_size, int num_blocks, int max_prefix_blocks, int max_blocks, float scale,
     void* stream) {
-  g_px_error.clear();
+  g_px_error[0] = 0;
   return decode(q, k_pool, v_pool, prefix_table, prefix_lens, group_start, block_table, seq_lens,
                 out, B, P, Hq, Hkv, D, kv_dtype, block_size, num_blocks, max_prefix_blocks,
                 max_blocks, scale, kPxTimeoutNs, ~0u, static_cast<cudaStream_t>(stream));
@@ -313,7 +378,7 @@ extern "C" int gqa_prefix_selftest_wait_timeout(
     const int32_t* seq_lens, void* out, int B, int P, int Hq, int Hkv, int D, int kv_dtype,
     int block_size, int num_blocks, int max_prefix_blocks, int max_blocks, float scale,
     long long wait_ns, int withhold_from, void* stream) {
-  g_px_error.clear();
+  g_px_error[0] = 0;
   if (wait_ns < 100000 || wait_ns > kPxTimeoutNs || withhold_from < 0)
     return pfail(GQA_AV_ERR_INVALID, "wait_ns=%lld must be in [100000, %lld], withhold_from=%d not "
                  "negative", wait_ns, kPxTimeoutNs, withhold_from);
@@ -324,7 +389,7 @@ extern "C" int gqa_prefix_selftest_wait_timeout(
 }
 
 extern "C" int gqa_prefix_device_status(void* stream_, int clear) {
-  g_px_error.clear();
+  g_px_error[0] = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return pfail_cuda(e, "cudaGetDevice");
@@ -344,4 +409,22 @@ extern "C" int gqa_prefix_device_status(void* stream_, int clear) {
   return GQA_AV_OK;
 }
 
-extern "C" const char* gqa_prefix_last_error(void) { return g_px_error.c_str(); }
+extern "C" int gqa_prefix_release_graph_workspaces(void) {
+  g_px_error[0] = 0;
+  std::lock_guard<std::mutex> lk(g_px_mu);
+  RelaxedCapture relaxed;
+  cudaError_t first = cudaSuccess;
+  for (auto it = g_px_ws.begin(); it != g_px_ws.end();) {
+    if (!it->first.capture) {
+      ++it;
+      continue;
+    }
+    cudaError_t e = cudaFree(it->second->base);
+    if (first == cudaSuccess) first = e;
+    for (char* p : it->second->outgrown) cudaFree(p);
+    it = g_px_ws.erase(it);
+  }
+  return first == cudaSuccess ? GQA_AV_OK : pfail_cuda(first, "cudaFree");
+}
+
+extern "C" const char* gqa_prefix_last_error(void) { return g_px_error; }

@@ -41,13 +41,22 @@
  * the pools 16-byte aligned; B <= 4096, Hkv <= 2^14, B * Hkv <= 2^20, P <= 32;
  * num_blocks * block_size below 2^31 and at most 2^26 rows in one table row.
  *
- * Execution: asynchronous on `stream`, no host synchronisation; the lengths
- * and groups are read on the device, so a captured graph follows them. The
- * call keeps its own per-device workspace, grown on demand with cudaMalloc
- * outside stream capture (a buffer that it outgrows is kept until the process
- * ends, since captured graphs may hold it); calls that may overlap on the GPU
- * must not be issued concurrently. Errors: a status code from gqa_av.h; on
- * error nothing is launched and gqa_prefix_last_error() holds a message.
+ * Execution: asynchronous on `stream`; the lengths and groups are read on the
+ * device, so a captured graph follows them. The call keeps workspaces of its
+ * own, allocated with cudaMalloc when they are first needed or too small (the
+ * host then waits for the calls under way on the stream; nothing else
+ * synchronises): one for each stream, and one for each stream of a capture,
+ * which the calls of that capture share. So calls on different streams and
+ * replays of different graphs may overlap, from one host thread or several. Two
+ * executable copies of one captured graph share its workspace and must not
+ * overlap. A stream's workspace outlives the stream, for the next one of the
+ * same handle; a capture's is kept until gqa_prefix_release_graph_workspaces.
+ * Its size: with R = 128 / G sequences a query tile, up to
+ *     (ceil(B / R) + min(P, B)) * Hkv + 2 * SMs
+ * slots of 128 * (D + 2) floats, twice that for D below 256, and (B * Hkv +
+ * 4 * SMs) * G * (D + 2) floats for own rows (46 MB for 64 sequences, 32 + 8
+ * heads of 128). Errors: a status code from gqa_av.h; on error nothing is
+ * launched and gqa_prefix_last_error() holds a message.
  */
 #ifndef GQA_PREFIX_H
 #define GQA_PREFIX_H
@@ -72,6 +81,10 @@ int gqa_prefix_attn_decode(const void *q, const void *k_pool, const void *v_pool
  * wait inside a kernel runs out, in any call or graph replay on the device):
  * GQA_AV_OK or GQA_AV_ERR_DEVICE_TIMEOUT; with clear != 0 the word is reset. */
 int gqa_prefix_device_status(void *stream, int clear);
+
+/* Free the workspaces of all captures. No graph that was captured before the
+ * call may be launched after it. (cudaFree waits for launches under way.) */
+int gqa_prefix_release_graph_workspaces(void);
 
 /*
  * Self-test of that report: the decode call with bounded waits of wait_ns
