@@ -99,11 +99,21 @@ extern "C" int gqa_kv_tables(const int32_t* cached_lens, const int32_t* new_lens
        addr(block_table) | addr(seq_lens) | addr(token_start) | addr(slots) | addr(positions) |
        addr(free_left)) & 3u)
     return kfail(GQA_AV_ERR_INVALID, "pointers must be 4-byte aligned");
-  if (seq_lens == cached_lens || seq_lens == new_lens || free_left == free_count)
-    return kfail(GQA_AV_ERR_INVALID, "seq_lens and free_left must not be inputs of the call");
   int rc = check_pool(block_size, num_blocks);
   if (rc) return rc;
   if (B > kTabMaxB) return kfail(GQA_AV_ERR_UNSUPPORTED, "B=%d is above %d", B, kTabMaxB);
+  // Every CTA reads the inputs, at any time while others write.
+  const struct { const char* name; const int32_t* at; long long n; }
+      ins[] = {{"cached_lens", cached_lens, B}, {"new_lens", new_lens, B}, {"pos_base", pos_base, B},
+               {"free_list", free_list, n_free}, {"free_count", free_count, 1}},
+      outs[] = {{"block_table", block_table, static_cast<long long>(B) * max_blocks},
+                {"seq_lens", seq_lens, B}, {"token_start", token_start, B + 1LL},
+                {"slots", slots, T}, {"positions", positions, T}, {"free_left", free_left, 1}};
+  for (const auto& i : ins)
+    for (const auto& o : outs)
+      if (i.at && o.at && i.n && o.n && addr(i.at) < addr(o.at) + 4 * static_cast<uintptr_t>(o.n) &&
+          addr(o.at) < addr(i.at) + 4 * static_cast<uintptr_t>(i.n))
+        return kfail(GQA_AV_ERR_INVALID, "%s overlaps %s", o.name, i.name);
 
   TablesParams p;
   p.cached = cached_lens; p.fresh = new_lens; p.pos_base = pos_base;

@@ -61,8 +61,8 @@ extern "C" {
  *     seq_lens [B], token_start [B + 1], slots [T], positions [T], free_left [1] int32
  *
  * Negative lengths count as 0. Limits: B <= 8192, num_blocks * block_size
- * < 2^31. T may be 0. seq_lens must not be cached_lens nor free_left be
- * free_count: every CTA reads the inputs while others write.
+ * < 2^31. T may be 0. No output (block_table among them) may overlap an input:
+ * every CTA reads the inputs while others write.
  */
 int gqa_kv_tables(const int32_t *cached_lens, const int32_t *new_lens, const int32_t *pos_base,
                   const int32_t *free_list, const int32_t *free_count, int32_t *block_table,

@@ -86,3 +86,25 @@ def test_binding_rejects_tensors_that_do_not_fit(native):
     x = torch.zeros((3, 2, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="k_pool"):
         native.gqa_kv_norm_rope_append(x, x, x, t[0], t[0], t[0], x, pool, pool)
+
+
+INS = dict(cached=4, new=4, base=4, free=4, count=1)        # entries of each
+OUTS = dict(table=16, seq=4, start=5, slots=8, pos=8, left=1)
+
+
+def apart():
+    """The call's arrays behind one another: nothing overlaps."""
+    a, at = dict(TABLES), FAKE
+    for name, n in (INS | OUTS).items():
+        a[name], at = at, at + 4 * n
+    return a
+
+
+@pytest.mark.parametrize("out", OUTS)
+@pytest.mark.parametrize("inp", INS)
+def test_tables_outputs_must_not_overlap_inputs(native, inp, out):
+    for shift in (0, 4 * (INS[inp] - 1), 4 - 4 * OUTS[out]):   # the same, and by one entry
+        a = apart()
+        a[out] = a[inp] + shift
+        assert native.lib.gqa_kv_tables(*a.values(), None) == 1
+        assert b"overlaps" in native.lib.gqa_kv_last_error(), native.lib.gqa_kv_last_error()
