@@ -390,6 +390,14 @@ def _int32(name: str, t, shape) -> None:
                          f"not {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _on_current_device(**tensors) -> None:
+    """The library works on the current device: its workspaces, launches and SM count."""
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+
+
 def _pools(k_pool: torch.Tensor, v_pool: torch.Tensor):
     shape, dtype = k_pool.shape, k_pool.dtype
     if len(shape) != 4 or v_pool.shape != shape:
@@ -427,6 +435,10 @@ def gqa_kv_tables(cached_lens, new_lens, free_list, free_count, block_table, seq
     _int32("token_start", token_start, (B + 1,))
     _int32("slots", slots, (T,))
     _int32("positions", positions, (T,))
+    _on_current_device(block_table=block_table, cached_lens=cached_lens, new_lens=new_lens,
+                       seq_lens=seq_lens, pos_base=pos_base, free_list=free_list,
+                       free_count=free_count, free_left=free_left, token_start=token_start,
+                       slots=slots, positions=positions)
     _check_kv(lib.gqa_kv_tables(_ptr(cached_lens), _ptr(new_lens), _ptr(pos_base), _ptr(free_list),
                                 _ptr(free_count), _ptr(block_table), _ptr(seq_lens),
                                 _ptr(token_start), _ptr(slots), _ptr(positions), _ptr(free_left),
@@ -475,6 +487,9 @@ def gqa_kv_norm_rope_append(q, k, v, positions, slots, inv_freq, q_out, k_pool, 
         if t is not None and (t.dtype is not dtype or t.shape != (D,) or not t.is_cuda
                               or not t.is_contiguous()):
             raise ValueError(f"{name} must be a contiguous CUDA tensor [D] of the pools' type")
+    _on_current_device(k_pool=k_pool, v_pool=v_pool, q=q, k=k, v=v, q_out=q_out, slots=slots,
+                       positions=positions, inv_freq=inv_freq, q_weight=q_weight,
+                       k_weight=k_weight)
     sec = None if sections is None else (ctypes.c_int * axes)(*[int(n) for n in sections])
     code = _V_DTYPE[dtype]
     _check_kv(lib.gqa_kv_norm_rope_append(
@@ -526,6 +541,11 @@ def gqa_prefix_attn_decode(q, k_pool, v_pool, prefix_table, prefix_lens, group_s
         _int32("block_table", block_table, (B, max_blocks))
     if seq_lens is not None:
         _int32("seq_lens", seq_lens, (B,))
+    _on_current_device(k_pool=k_pool, v_pool=v_pool, q=q, out=out, block_table=block_table,
+                       seq_lens=seq_lens)
+    if P:
+        _on_current_device(prefix_table=prefix_table, prefix_lens=prefix_lens,
+                           group_start=group_start)
     sc = float(D) ** -0.5 if scale is None else float(scale)
     _check_prefix(lib.gqa_prefix_attn_decode(
         _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(prefix_table) if P else None,
