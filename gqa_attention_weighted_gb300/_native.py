@@ -529,6 +529,8 @@ def gqa_prefix_attn_decode(q, k_pool, v_pool, prefix_table, prefix_lens, group_s
     if prefix_table is not None:
         if prefix_table.dim() != 2:
             raise ValueError("prefix_table must be [P, max_prefix_blocks]")
+        if prefix_lens is None:
+            raise ValueError("prefix_table needs prefix_lens")
         P, max_pblocks = prefix_table.shape
         _int32("prefix_table", prefix_table, (P, max_pblocks))
         _int32("prefix_lens", prefix_lens, (P,))

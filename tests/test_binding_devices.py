@@ -75,3 +75,8 @@ def test_a_tensor_on_another_device_is_refused(native, name, elsewhere):
     with pytest.raises(ValueError, match=f"{elsewhere} is on cuda:1"):
         getattr(native, name)(**arguments(name, elsewhere))
     assert native.lib.calls == 0
+
+
+def test_a_prefix_table_needs_its_lengths(native):
+    with pytest.raises(ValueError, match="prefix_lens"):
+        native.gqa_prefix_attn_decode(**dict(arguments("gqa_prefix_attn_decode"), prefix_lens=None))
