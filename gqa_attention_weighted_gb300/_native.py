@@ -383,19 +383,31 @@ def _check_kv(status: int) -> None:
         raise GqaAvError(status, f"{name}: {lib.gqa_kv_last_error().decode()}")
 
 
-def _int32(name: str, t, shape) -> None:
-    """A contiguous CUDA int32 tensor of this shape."""
-    if t.dtype is not torch.int32 or t.shape != shape or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA int32 tensor of shape {tuple(shape)}, "
-                         f"not {t.dtype} {tuple(t.shape)} on {t.device}")
+def _device(name: str, t) -> int:
+    """The device of a call's first tensor. It has to be the current one: the library's launches,
+    workspaces and SM count are that device's."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor, not on {t.device}")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+    return dev
 
 
-def _on_current_device(**tensors) -> None:
-    """The library works on the current device: its workspaces, launches and SM count."""
-    dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is cuda:{dev}")
+def _refuse(name: str, t, dev: int, must: str) -> None:
+    """Raises for a tensor that is not on ``dev`` or not what it ``must`` be."""
+    at = t.get_device()
+    if at >= 0 and at != dev:
+        raise ValueError(f"{name} is on cuda:{at}, the current device is cuda:{dev}")
+    raise ValueError(f"{name} must be {must}, not {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _int32(name: str, t, shape, dev: int) -> None:
+    """A contiguous int32 tensor of this shape on device ``dev``."""
+    if (t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
+        _refuse(name, t, dev, f"a contiguous CUDA int32 tensor of shape {tuple(shape)}")
 
 
 def _pools(k_pool: torch.Tensor, v_pool: torch.Tensor):
@@ -405,10 +417,11 @@ def _pools(k_pool: torch.Tensor, v_pool: torch.Tensor):
                          f"{tuple(shape)} and {tuple(v_pool.shape)}")
     if dtype not in _V_DTYPE or v_pool.dtype is not dtype:
         raise ValueError("k_pool and v_pool must both be bfloat16 or both float16")
-    if not (k_pool.is_cuda and v_pool.is_cuda and k_pool.is_contiguous()
-            and v_pool.is_contiguous()):
-        raise ValueError("k_pool and v_pool must be contiguous CUDA tensors")
-    return shape
+    dev = _device("k_pool", k_pool)
+    for name, t in (("k_pool", k_pool), ("v_pool", v_pool)):
+        if t.get_device() != dev or not t.is_contiguous():
+            _refuse(name, t, dev, "a contiguous CUDA tensor")
+    return shape, dev
 
 
 def gqa_kv_tables(cached_lens, new_lens, free_list, free_count, block_table, seq_lens, token_start,
@@ -423,22 +436,19 @@ def gqa_kv_tables(cached_lens, new_lens, free_list, free_count, block_table, seq
                          "dimension")
     B, max_blocks = block_table.shape
     T, n_free = slots.shape[0], free_list.shape[0]
-    _int32("block_table", block_table, (B, max_blocks))
-    _int32("cached_lens", cached_lens, (B,))
-    _int32("new_lens", new_lens, (B,))
-    _int32("seq_lens", seq_lens, (B,))
+    dev = _device("block_table", block_table)
+    _int32("block_table", block_table, (B, max_blocks), dev)
+    _int32("cached_lens", cached_lens, (B,), dev)
+    _int32("new_lens", new_lens, (B,), dev)
+    _int32("seq_lens", seq_lens, (B,), dev)
     if pos_base is not None:
-        _int32("pos_base", pos_base, (B,))
-    _int32("free_list", free_list, (n_free,))
-    _int32("free_count", free_count, (1,))
-    _int32("free_left", free_left, (1,))
-    _int32("token_start", token_start, (B + 1,))
-    _int32("slots", slots, (T,))
-    _int32("positions", positions, (T,))
-    _on_current_device(block_table=block_table, cached_lens=cached_lens, new_lens=new_lens,
-                       seq_lens=seq_lens, pos_base=pos_base, free_list=free_list,
-                       free_count=free_count, free_left=free_left, token_start=token_start,
-                       slots=slots, positions=positions)
+        _int32("pos_base", pos_base, (B,), dev)
+    _int32("free_list", free_list, (n_free,), dev)
+    _int32("free_count", free_count, (1,), dev)
+    _int32("free_left", free_left, (1,), dev)
+    _int32("token_start", token_start, (B + 1,), dev)
+    _int32("slots", slots, (T,), dev)
+    _int32("positions", positions, (T,), dev)
     _check_kv(lib.gqa_kv_tables(_ptr(cached_lens), _ptr(new_lens), _ptr(pos_base), _ptr(free_list),
                                 _ptr(free_count), _ptr(block_table), _ptr(seq_lens),
                                 _ptr(token_start), _ptr(slots), _ptr(positions), _ptr(free_left),
@@ -454,7 +464,7 @@ def gqa_kv_norm_rope_append(q, k, v, positions, slots, inv_freq, q_out, k_pool, 
     ``positions`` ([T], or [axes,T] with ``sections`` pairs an axis) times ``inv_freq``, queries to
     ``q_out`` (float32 or the input type), keys and values to rows ``slots`` of the pools. q, k and
     v may be views of one packed projection. Returns ``q_out``."""
-    num_blocks, block_size, Hkv, D = _pools(k_pool, v_pool)
+    (num_blocks, block_size, Hkv, D), dev = _pools(k_pool, v_pool)
     dtype = k_pool.dtype
     if q.dim() != 3:
         raise ValueError("q must be [T,Hq,D], k and v [T,Hkv,D]")
@@ -466,30 +476,28 @@ def gqa_kv_norm_rope_append(q, k, v, positions, slots, inv_freq, q_out, k_pool, 
                          f"{tuple(k_pool.shape)}")
     strides = []
     for name, t, heads in (("q", q, Hq), ("k", k, Hkv), ("v", v, Hkv)):
-        if t.dtype is not dtype or not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor of the pools' type")
+        if t.dtype is not dtype or t.get_device() != dev:
+            _refuse(name, t, dev, "a CUDA tensor of the pools' type")
         st = t.stride()
         if T and (st[2] != 1 or (heads > 1 and st[1] != D)):
             raise ValueError(f"a token's heads must be contiguous in {name}")
         strides.append(st[0])
     q32 = q_out.dtype is torch.float32
-    if not (q32 or q_out.dtype is dtype) or not q_out.is_cuda or not q_out.is_contiguous():
-        raise ValueError("q_out must be a contiguous CUDA tensor, float32 or of the pools' type")
-    _int32("slots", slots, (T,))
+    if (not (q32 or q_out.dtype is dtype) or q_out.get_device() != dev
+            or not q_out.is_contiguous()):
+        _refuse("q_out", q_out, dev, "a contiguous CUDA tensor, float32 or of the pools' type")
+    _int32("slots", slots, (T,), dev)
     axes = 1 if positions.dim() == 1 else positions.shape[0]
-    _int32("positions", positions, (T,) if positions.dim() == 1 else (axes, T))
-    if (inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or not inv_freq.is_cuda
-            or not inv_freq.is_contiguous()):
-        raise ValueError("inv_freq must be a contiguous CUDA float32 tensor of one dimension")
+    _int32("positions", positions, (T,) if positions.dim() == 1 else (axes, T), dev)
+    if (inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1
+            or inv_freq.get_device() != dev or not inv_freq.is_contiguous()):
+        _refuse("inv_freq", inv_freq, dev, "a contiguous CUDA float32 tensor of one dimension")
     if sections is not None and len(sections) != axes:
         raise ValueError(f"{len(sections)} sections for {axes} position axes")
     for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None and (t.dtype is not dtype or t.shape != (D,) or not t.is_cuda
+        if t is not None and (t.dtype is not dtype or t.shape != (D,) or t.get_device() != dev
                               or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous CUDA tensor [D] of the pools' type")
-    _on_current_device(k_pool=k_pool, v_pool=v_pool, q=q, k=k, v=v, q_out=q_out, slots=slots,
-                       positions=positions, inv_freq=inv_freq, q_weight=q_weight,
-                       k_weight=k_weight)
+            _refuse(name, t, dev, f"a contiguous CUDA tensor [{D}] of the pools' type")
     sec = None if sections is None else (ctypes.c_int * axes)(*[int(n) for n in sections])
     code = _V_DTYPE[dtype]
     _check_kv(lib.gqa_kv_norm_rope_append(
@@ -516,15 +524,15 @@ def gqa_prefix_attn_decode(q, k_pool, v_pool, prefix_table, prefix_lens, group_s
     (scale defaults to 1/sqrt(D)); writes and returns ``out``. Calls on different streams and
     replays of different graphs may overlap: each stream, and each capture, has a workspace of its
     own."""
-    num_blocks, block_size, Hkv, D = _pools(k_pool, v_pool)
+    (num_blocks, block_size, Hkv, D), dev = _pools(k_pool, v_pool)
     dtype = k_pool.dtype
     if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape:
         raise ValueError(f"q and out must be [B,Hq,{D}], not {tuple(q.shape)} and "
                          f"{tuple(out.shape)}")
     B, Hq = q.shape[:2]
-    if (q.dtype is not dtype or out.dtype is not dtype
-            or not (q.is_cuda and out.is_cuda and q.is_contiguous() and out.is_contiguous())):
-        raise ValueError("q and out must be contiguous CUDA tensors of the pools' type")
+    for name, t in (("q", q), ("out", out)):
+        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            _refuse(name, t, dev, "a contiguous CUDA tensor of the pools' type")
     P = max_pblocks = max_blocks = 0
     if prefix_table is not None:
         if prefix_table.dim() != 2:
@@ -532,22 +540,17 @@ def gqa_prefix_attn_decode(q, k_pool, v_pool, prefix_table, prefix_lens, group_s
         if prefix_lens is None:
             raise ValueError("prefix_table needs prefix_lens")
         P, max_pblocks = prefix_table.shape
-        _int32("prefix_table", prefix_table, (P, max_pblocks))
-        _int32("prefix_lens", prefix_lens, (P,))
+        _int32("prefix_table", prefix_table, (P, max_pblocks), dev)
+        _int32("prefix_lens", prefix_lens, (P,), dev)
         if group_start is not None:
-            _int32("group_start", group_start, (P + 1,))
+            _int32("group_start", group_start, (P + 1,), dev)
     if block_table is not None:
         if block_table.dim() != 2:
             raise ValueError("block_table must be [B, max_blocks]")
         max_blocks = block_table.shape[1]
-        _int32("block_table", block_table, (B, max_blocks))
+        _int32("block_table", block_table, (B, max_blocks), dev)
     if seq_lens is not None:
-        _int32("seq_lens", seq_lens, (B,))
-    _on_current_device(k_pool=k_pool, v_pool=v_pool, q=q, out=out, block_table=block_table,
-                       seq_lens=seq_lens)
-    if P:
-        _on_current_device(prefix_table=prefix_table, prefix_lens=prefix_lens,
-                           group_start=group_start)
+        _int32("seq_lens", seq_lens, (B,), dev)
     sc = float(D) ** -0.5 if scale is None else float(scale)
     _check_prefix(lib.gqa_prefix_attn_decode(
         _ptr(q), _ptr(k_pool), _ptr(v_pool), _ptr(prefix_table) if P else None,
