@@ -299,11 +299,14 @@ int decode(const void* q, const void* k_pool, const void* v_pool, const int32_t*
   if (s2 > FLT_MAX) return pfail(GQA_AV_ERR_UNSUPPORTED, "scale=%g is too large", (double)scale);
   p.qscale = std::max(static_cast<float>(s2), FLT_MIN);
   p.negate = scale < 0.0f;
-  // Cost model of the plan, in SM cycles: a key tile of 64 KiB streams from
-  // HBM in about 2800 (all SMs together); its products take 1024 a query tile
-  // at D >= 128 (the softmax as long at D = 64) and a little more measured.
-  p.c_pair = D == 64 ? 1200.0f : 2300.0f;
-  p.c_tile = D == 64 ? 700.0f : 1300.0f;
+  // Costs of the plan, in SM cycles. Prefix key tiles as measured on 256
+  // sequences behind 32768 rows, 64 + 8 heads, one unit a CTA of all key tiles:
+  // 0.83 us a tile at D = 128 (1.63 for two query tiles), 0.76 (1.50) at D = 64,
+  // 0.78 at D = 256 (tiles of 64 keys), at 1.9 GHz; the products of one take
+  // 1024. Own tiles come from HBM, all SMs together: 64 KiB in 2800 (32 KiB at
+  // D = 64). A unit's start and end cost about 2 us beyond its tiles.
+  p.c_pair = D == 64 ? 2850.0f : 3100.0f;
+  p.c_tile = D == 64 ? 1450.0f : D == 128 ? 1580.0f : 1480.0f;
   p.c_own = D == 64 ? 1400.0f : 2800.0f;
   p.c_unit = 4000.0f;
   p.timeout_ns = wait_ns;

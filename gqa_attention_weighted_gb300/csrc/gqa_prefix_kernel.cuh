@@ -458,12 +458,13 @@ struct PxPlan {
     const int longest = __reduce_max_sync(0xffffffffu, tiles);
     if (longest == 0) return;
     // How to cut the prefixes: each lane costs one choice of pairs or single
-    // query tiles and of the key tiles a split takes (1 to 8 units a CTA), from
-    // the time that the units take if all CTAs stay busy, own units included,
-    // and from the CTA with the most prefix units, the latter 1.3 times: units
-    // that nearly fill the call leave nothing to even out what the costs miss
-    // (256 sequences behind 32768 rows: 289 us, without it 296; at 1.15 as
-    // without, at 1.6 as with).
+    // query tiles and of the key tiles a split takes, from the time that the
+    // units take if all CTAs stay busy, own units included, and from the CTA with
+    // the most prefix units. The cuts aim at 1 to 8 units a CTA; those with more
+    // units than slots (one a query tile and two a CTA) are left out, so long
+    // prefixes behind few query tiles have 1 or 2 to choose from. On 51 batches,
+    // listed and drawn ones, the choice is 2.6 % slower than the best choice
+    // measured, on average, at worst 22 % (18.4 us for 14.9: a small batch).
     const bool pairs = Shape::NS == 2 && (lane & 1);
     float w = 0.0f;                     // key tiles x query tiles (or pairs)
     for (int g = 0; g < p.P; ++g) {
@@ -485,7 +486,7 @@ struct PxPlan {
     const float one = static_cast<float>(chunk) * c + p.c_unit;
     const float all = __fdividef(w * c + units * p.c_unit + own->work * p.c_own, static_cast<float>(n));
     const float rounds = ceilf(__fdividef(units - 0.5f, static_cast<float>(n)));
-    const float est = units <= static_cast<float>(p.prefix_slots) ? fmaxf(all, 1.3f * rounds * one) : INFINITY;
+    const float est = units <= static_cast<float>(p.prefix_slots) ? fmaxf(all, rounds * one) : INFINITY;
     // Costs are positive, so their bit patterns are ordered like them.
     const unsigned best = __reduce_min_sync(0xffffffffu, __float_as_uint(est));
     const int src = __ffs(__ballot_sync(0xffffffffu, __float_as_uint(est) == best)) - 1;
