@@ -6,7 +6,6 @@
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
-#include <string>
 
 #include "gqa_kv.h"
 #include "gqa_kv_kernel.cuh"
@@ -14,15 +13,13 @@
 namespace gqa_av {
 namespace {
 
-thread_local std::string g_kv_error;
+thread_local char g_kv_error[512];   // no allocation: nothing here can throw
 
 int kfail(int status, const char* fmt, ...) {
-  char buf[512];
   va_list ap;
   va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
+  vsnprintf(g_kv_error, sizeof g_kv_error, fmt, ap);
   va_end(ap);
-  g_kv_error = buf;
   return status;
 }
 
@@ -87,7 +84,7 @@ extern "C" int gqa_kv_tables(const int32_t* cached_lens, const int32_t* new_lens
                              int32_t* token_start, int32_t* slots, int32_t* positions,
                              int32_t* free_left, int B, int T, int max_blocks, int n_free,
                              int block_size, int num_blocks, void* stream) {
-  g_kv_error.clear();
+  g_kv_error[0] = 0;
   if (B <= 0 || T < 0 || max_blocks <= 0 || n_free < 0)
     return kfail(GQA_AV_ERR_INVALID,
                  "B=%d and max_blocks=%d must be positive, T=%d and n_free=%d not negative", B,
@@ -143,7 +140,7 @@ extern "C" int gqa_kv_norm_rope_append(
     float weight_offset, int interleaved, const int32_t* slots, void* q_out, int q_out_dtype,
     void* k_pool, void* v_pool, int T, int Hq, int Hkv, int D, int rot_dim, int kv_dtype,
     int block_size, int num_blocks, void* stream) {
-  g_kv_error.clear();
+  g_kv_error[0] = 0;
   if (T < 0 || Hq <= 0 || Hkv <= 0 || D <= 0)
     return kfail(GQA_AV_ERR_INVALID, "T=%d must not be negative and Hq=%d Hkv=%d D=%d positive", T,
                  Hq, Hkv, D);
@@ -230,4 +227,4 @@ extern "C" int gqa_kv_norm_rope_append(
   return GQA_AV_OK;
 }
 
-extern "C" const char* gqa_kv_last_error(void) { return g_kv_error.c_str(); }
+extern "C" const char* gqa_kv_last_error(void) { return g_kv_error; }
