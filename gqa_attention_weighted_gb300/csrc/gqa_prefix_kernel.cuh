@@ -846,8 +846,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
             pv(0, j);
           }
         } else {
-          // Every unit's phase of both ofree barriers is waited for, here or by pv.
-          if (n1 == 0) ok = warp_poll(ofree0 + 8, unit_no & 1, p.timeout_ns);
+          // Every unit's phase of both ofree barriers is waited for, here or by
+          // pv, but for an own unit without a second stream, the call's last:
+          // nothing arrives for it (below).
+          if (n1 == 0 && mode == kSplit) ok = warp_poll(ofree0 + 8, unit_no & 1, p.timeout_ns);
           // The streams in turn: the PV of a tile, then the QK of the next. One
           // site for each product keeps the code small.
 #pragma unroll 1
@@ -1090,7 +1092,10 @@ __global__ void __launch_bounds__(kPxThreads, 1)
         if (mode == kSplit) {
           mbar_arrive(ofree0);
           mbar_arrive(ofree0 + 8);
-        } else {
+        } else if (dry || mine > 0) {
+          // Warps of a stream that has nothing to do wait for nothing. Were they
+          // to arrive, they could complete this phase before the MMA warp has
+          // seen the one before, and its wait, for a parity, would never end.
           mbar_arrive(ofree0 + 8 * w);
           mbar_arrive(ofree0 + 8 * w);
         }
