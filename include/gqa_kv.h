@@ -60,7 +60,8 @@ extern "C" {
  *     block_table [B, max_blocks] int32, updated in place
  *     seq_lens [B], token_start [B + 1], slots [T], positions [T], free_left [1] int32
  *
- * Negative lengths count as 0. Limits: B <= 8192, num_blocks * block_size
+ * Negative lengths count as 0; token starts and lengths that pass 2^31 - 1 are
+ * held there (such requests are not served). Limits: B <= 8192, num_blocks * block_size
  * < 2^31. T may be 0. No output (block_table among them) may overlap an input:
  * every CTA reads the inputs while others write.
  */
@@ -90,8 +91,8 @@ int gqa_kv_tables(const int32_t *cached_lens, const int32_t *new_lens, const int
  * order, for example time, height and width; NULL with n_axes = 1 means one
  * axis for all pairs. Queries go to q_out; rotated keys and the values (as
  * they are) go to row slots[t] of the pools, and nowhere when slots[t] is
- * outside [0, num_blocks * block_size) (padding: -1). Of tokens that share a
- * slot any one may win.
+ * outside [0, num_blocks * block_size) (padding: -1). A row that several tokens
+ * name as their slot ends up with pieces of any of them.
  *
  *     q [T, Hq, D], k and v [T, Hkv, D]  kv_dtype; a token's heads are
  *         contiguous, tokens lie q_stride, k_stride, v_stride elements apart

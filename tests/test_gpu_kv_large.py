@@ -24,3 +24,10 @@ def test_tables_of_large_batches(gq, B):  # noqa: F811
         at += held[b]
     run_tables(gq, cached, new, perm[at:], need - 7, table, int(new.sum()) + 33, bs, nb,
                rng.integers(0, 10000, size=B))
+
+
+def test_lengths_near_the_largest(gq):  # noqa: F811
+    # Far past what the table holds: not served, nothing written, the others as usual.
+    big = 2 ** 31 - 1
+    run_tables(gq, [big, 5, big - 16, big - 5], [0, 2, 1, 3], [1, 2, 3], 3,
+               [[0, 0], [1, 2], [3, 4], [5, 6]], 6, 16, 8)
