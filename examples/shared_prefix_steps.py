@@ -91,7 +91,7 @@ def main(steps=40, B=32, Hq=32, Hkv=8, D=128, block=16, prefix_rows=2000):
     batch = PagedSteps(B, Hq, Hkv, D, block, prefix_rows, max_rows=steps + 8)
     batch.prefill_prefix(draw(prefix_rows))
     qkv = draw(B)
-    batch.step(qkv)                              # sets the workspace up before capture
+    batch.step(qkv)                              # loads the kernels before capture
     batch.reset()
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):

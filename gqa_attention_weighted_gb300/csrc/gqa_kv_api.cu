@@ -208,9 +208,12 @@ extern "C" int gqa_kv_norm_rope_append(
   int lanes = 4;
   while (lanes * 8 < D) lanes *= 2;
   const int steps = (Hq + 2 * Hkv + 32 / lanes - 1) / (32 / lanes);
-  // A token's heads go to one warp when the tokens alone fill the GPU (8 CTAs
-  // of 8 warps an SM); with fewer tokens they are cut into parts, down to one
-  // step a warp, since a single warp's chain of loads is all latency.
+  // A token's heads go to one warp when there are tokens for 8 CTAs of 8 warps an
+  // SM; with fewer they are cut into parts, down to one step a warp, since a
+  // single warp's chain of loads is all latency. That is more than fit at a time:
+  // registers leave 3 CTAs an SM (2 with separate halves and fp32 queries), so
+  // mid-size calls run in waves (4097 tokens of 16 + 1 + 1 heads: 1025 CTAs, 2.2
+  // waves, 24.5 us).
   const long long room = static_cast<long long>(sms) * 8 * kRopeWarps;
   p.chunks = static_cast<int>(std::min<long long>(steps, std::max<long long>(1, room / T)));
   p.iters = (steps + p.chunks - 1) / p.chunks;

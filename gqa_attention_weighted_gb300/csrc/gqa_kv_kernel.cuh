@@ -202,8 +202,9 @@ __device__ __forceinline__ void pair_rotation(unsigned long long turn64, int pos
 // slots). Measured at 16384 tokens of 32 + 8 + 8 heads of 128, bf16 (403 MB): 84
 // us; 141 with eight adjacent elements a lane, whose mates came by shuffles, and
 // one step's loads at a time. More loads ahead, next tokens' positions ahead and
-// addresses kept as pointers all measured slower: each costs registers, and so
-// the third CTA of an SM.
+// addresses kept as pointers all measured slower: each costs registers, and with
+// more than 80 the third CTA of an SM (separate halves with fp32 queries take 86
+// to 88 and run two).
 template <typename Tag, int L, bool kInterleaved, bool kQ32>
 __global__ void __launch_bounds__(32 * kRopeWarps) gqa_kv_rope_kernel(const RopeParams p) {
   __shared__ unsigned long long turn[kRopeMaxPairs];

@@ -24,6 +24,13 @@
 //                 from shared memory (MN-major), O in tensor memory.
 // m moves only when a row's maximum has grown by more than 2^8 (then O and l
 // are rescaled), so O is rarely touched; weights stay below 2^8.
+// Rounding the weights to 16 bits lets one product make O (two halves of a weight
+// would take two) and costs half a step a weight: against 64 bits the error is
+// 1.0 to 1.4 times that of a plain form with fp32 weights, whose last rounding is
+// the larger part (bf16 0.0017 to 0.0023 of the output's norm for 0.0017, most
+// where many keys share the weight; fp16 0.00028 for 0.00021). l sums them
+// unrounded: the roundings of many weights average out, so rounding them there
+// too would only take more instructions.
 //
 // D <= 128: two streams (S, O and a softmax warpgroup each) work in turn, so
 // the tensor core multiplies for one while the other makes weights. The
@@ -33,12 +40,14 @@
 // S buffers and key tiles of 64.
 //
 // Bounds and figures. A prefix key costs 2 * 2 * D * rows operations for 4 * D
-// bytes, so about 270 rows make it as much the tensor cores' work as HBM's; own
+// bytes, so about 290 rows make it as much the tensor cores' work as HBM's; own
 // rows are HBM's. Measured (bf16, blocks of 16, 64 + 8 heads of 128): 256
-// sequences behind 32768 rows, no own rows, 237 us, 1160 TFLOP/s (the tensor pipe
-// waits for weights: within a stream scores, weights and next scores follow one
-// another); 32 sequences of 8192 own rows 174 us, 6.15 TB/s; two sequences behind
-// 512 rows (8 + 2 heads of 64) 11 us, a chain of latencies. Key tiles of 128 keep
+// sequences behind 32768 rows, no own rows, 239 us, 1150 TFLOP/s (128 units of one
+// query tile, so 24 of the 152 SMs idle; the others' tensor pipes are active 55 %
+// of the time: within a stream scores, weights and next scores follow one another,
+// 1580 cycles a key tile for 1024 of products; the combine takes 17 us); 32
+// sequences of 8192 own rows 174 us, 6.15 TB/s; two sequences behind 512 rows (8 +
+// 2 heads of 64) 12 us, a chain of latencies. Key tiles of 128 keep
 // QK at the full rate (at N = 64 it waits for shared memory: 48 cycles where the
 // product takes 32) but leave no tensor memory for a second S.
 //
@@ -772,7 +781,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
       }
       if (is_k && blockIdx.x == gridDim.x - 1) plan.write(p, own_plan);
       if (!ok) {
-        // This warp's copies in flight land before the CTA leaves.
+        // This warp's copies in flight land before the CTA leaves (a wait for a
+        // stage that the other loader has filled since takes its full 2 s).
         if (lane == 0) atomicOr(&px_status, kErrPxLoad);
         if (held && lane < STAGES) mbar_wait(full0 + 8 * lane, held - 1, kPxTimeoutNs);
         if (held && lane >= 16) mbar_wait(qfull0 + 8 * (lane - 16), held - 1, kPxTimeoutNs);
@@ -1119,7 +1129,8 @@ __global__ void __launch_bounds__(kPxThreads, 1)
 // one. A row may have dozens of slots, and a thread waits for L2 at every step:
 // it takes U slots a step, 8 where all CTAs fit on the SMs at once (five an SM;
 // 16 sequences behind 8192 rows: 25 us, with 4 slots 28), 4 where they come in
-// waves, of which more fit then (256 behind 32768: 295 us, with 8 slots 299).
+// waves, of which more fit then (256 behind 32768, pairs cut in 5: 295 us, with 8
+// slots 299; uncut, as the plan has it now, 289 with 4).
 constexpr int kPxCombineThreads = 128;
 
 template <typename Tag, int D, int U>
