@@ -1,22 +1,17 @@
 // Host side of the C ABI declared in include/gqa_prefix.h: argument checks, the
 // call's workspace, tensor maps and dispatch to the attention and combine
 // kernels.
-#include <cuda.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
-#include <map>
-#include <memory>
 #include <mutex>
 #include <new>
-#include <tuple>
-#include <vector>
 
+#include "gqa_paged_host.h"
 #include "gqa_prefix.h"
 #include "gqa_prefix_kernel.cuh"
 
@@ -106,132 +101,7 @@ int smem_bytes(int D) {
   return D == 64 ? PxShape<64>::SMEM : D == 128 ? PxShape<128>::SMEM : PxShape<256>::SMEM;
 }
 
-// Workspaces. A call's units, plan and partial results lie in device memory
-// until its combine has run, so calls that may run at the same time must not
-// share a buffer. One belongs to each stream of uncaptured calls (which the
-// stream orders), and one to each stream of a capture into a graph: replays of
-// a graph follow one another, but may overlap with anything else. The latter
-// are kept until the caller says that the graphs are gone: a graph that owns
-// its buffer as a user object tells so by itself, but then each of its launches
-// holds the host up until the one before has ended (measured: 2 us a replay
-// become 13 to 45).
-struct Owner {
-  int dev;
-  const void* stream;
-  unsigned long long capture;    // 0: uncaptured
-  bool operator<(const Owner& o) const {
-    return std::tie(dev, stream, capture) < std::tie(o.dev, o.stream, o.capture);
-  }
-};
-struct Workspace {
-  std::mutex mu;                 // held until a call's kernels are launched: the stream's order
-  char* base = nullptr;
-  size_t bytes = 0;
-  std::vector<char*> outgrown;   // by a capture, whose earlier calls use them
-};
-std::mutex g_px_mu;
-std::map<Owner, std::unique_ptr<Workspace>> g_px_ws;
-
-// Allocation is allowed while a stream is capturing in this mode of the thread.
-struct RelaxedCapture {
-  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
-  RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
-  ~RelaxedCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
-};
-
-// Grows a workspace, whose lock is held, to `need` bytes. The new one's header
-// is zeroed on return.
-int grow(Workspace* w, bool capturing, size_t need, cudaStream_t stream) {
-  if (w->bytes >= need) return GQA_AV_OK;
-  const size_t bytes = capturing ? need : std::max(need, w->bytes + w->bytes / 2);
-  w->outgrown.reserve(w->outgrown.size() + 1);
-  RelaxedCapture relaxed;
-  void* p = nullptr;
-  cudaError_t e = cudaMalloc(&p, bytes);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return pfail(GQA_AV_ERR_NOMEM, "cudaMalloc(%zu) failed: %s", bytes, cudaGetErrorString(e));
-  }
-  cudaStream_t own = nullptr;    // not the legacy stream: others may be capturing
-  e = cudaStreamCreateWithFlags(&own, cudaStreamNonBlocking);
-  if (e == cudaSuccess) {
-    e = cudaMemsetAsync(p, 0, sizeof(PxHeader), own);
-    if (e == cudaSuccess) e = cudaStreamSynchronize(own);
-    cudaStreamDestroy(own);
-  }
-  if (e == cudaSuccess && w->base && !capturing) {
-    e = cudaStreamSynchronize(stream);   // calls under way use the old one
-    if (e == cudaSuccess) cudaFree(w->base);
-  }
-  if (e != cudaSuccess) {
-    cudaFree(p);
-    return pfail_cuda(e, "setting the workspace up");
-  }
-  if (w->base && capturing) w->outgrown.push_back(w->base);
-  w->base = static_cast<char*>(p);
-  w->bytes = bytes;
-  return GQA_AV_OK;
-}
-
-// The workspace that a call on `stream` uses. Those of uncaptured calls are
-// never taken away, so a thread remembers its last one.
-int find_workspace(int dev, cudaStream_t stream, bool* capturing, Workspace** out) {
-  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  cudaError_t e = cudaStreamIsCapturing(stream, &cs);
-  if (e == cudaSuccess && cs == cudaStreamCaptureStatusInvalidated)
-    e = cudaErrorStreamCaptureInvalidated;
-  if (e != cudaSuccess) return pfail_cuda(e, "cudaStreamIsCapturing");
-  *capturing = cs == cudaStreamCaptureStatusActive;
-  static thread_local char per_thread;   // each thread's default stream has the same handle
-  const void* key = stream == cudaStreamPerThread ? static_cast<const void*>(&per_thread)
-                    : stream == cudaStreamLegacy  ? nullptr
-                                                  : static_cast<const void*>(stream);
-  static thread_local Owner last{-1, nullptr, 0};
-  static thread_local Workspace* last_ws = nullptr;
-  if (!*capturing && last.dev == dev && last.stream == key) {
-    *out = last_ws;
-    return GQA_AV_OK;
-  }
-  unsigned long long id = 0;
-  if (*capturing) {
-    e = cudaStreamGetCaptureInfo(stream, &cs, &id, nullptr, nullptr, nullptr, nullptr);
-    if (e != cudaSuccess) return pfail_cuda(e, "cudaStreamGetCaptureInfo");
-  }
-  const Owner owner{dev, key, id};
-  std::lock_guard<std::mutex> lk(g_px_mu);
-  std::unique_ptr<Workspace>& w = g_px_ws[owner];
-  if (!w) w = std::make_unique<Workspace>();
-  *out = w.get();
-  if (!*capturing) {
-    last = owner;
-    last_ws = w.get();
-  }
-  return GQA_AV_OK;
-}
-
-// A map over 16-bit elements: `rank` dimensions, boxes 64 elements wide in the
-// 128-byte swizzle. What lies outside reads as zeros.
-int encode(CUtensorMap* m, const void* x, int rank, const cuuint64_t* dims,
-           const cuuint64_t* strides, const cuuint32_t* box, const char* what) {
-  static const PFN_cuTensorMapEncodeTiled_v12000 encode_tiled = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000,
-                                                     cudaEnableDefault, &q);
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(
-        e == cudaSuccess && q == cudaDriverEntryPointSuccess ? f : nullptr);
-  }();
-  if (!encode_tiled)
-    return pfail(GQA_AV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-  const cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = encode_tiled(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, rank, const_cast<void*>(x), dims,
-                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS)
-    return pfail(GQA_AV_ERR_UNSUPPORTED, "cuTensorMapEncodeTiled (%s) failed (%d)", what, (int)r);
-  return GQA_AV_OK;
-}
+using PrefixWorkspaces = Workspaces<sizeof(PxHeader), pfail>;
 
 int encode_maps(PrefixParams* p, const void* q, const void* k_pool, const void* v_pool, int D) {
   const cuuint64_t d = D, G = p->G, Hkv = p->Hkv, rows = static_cast<cuuint64_t>(p->bs) * p->num_blocks;
@@ -242,29 +112,12 @@ int encode_maps(PrefixParams* p, const void* q, const void* k_pool, const void* 
   const cuuint64_t kd[3] = {d, Hkv, rows};
   const cuuint64_t ks[2] = {d * 2, Hkv * d * 2};
   const cuuint32_t kb[3] = {64, 1, static_cast<cuuint32_t>(p->R)};
-  int rc = encode(&p->q_tile_map, q, 4, qd, qs, tile, "q");
-  if (!rc) rc = encode(&p->q_one_map, q, 4, qd, qs, one, "q");
-  if (!rc) rc = encode(&p->k_map, k_pool, 3, kd, ks, kb, "K");
-  if (!rc) rc = encode(&p->v_map, v_pool, 3, kd, ks, kb, "V");
+  int rc = encode_map(pfail, &p->q_tile_map, q, 4, qd, qs, tile, "q");
+  if (!rc) rc = encode_map(pfail, &p->q_one_map, q, 4, qd, qs, one, "q");
+  if (!rc) rc = encode_map(pfail, &p->k_map, k_pool, 3, kd, ks, kb, "K");
+  if (!rc) rc = encode_map(pfail, &p->v_map, v_pool, 3, kd, ks, kb, "V");
   return rc;
 }
-
-cudaError_t launch_pdl(const void* fn, int grid, int block, size_t smem, cudaStream_t stream,
-                       void** args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(block);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelExC(&cfg, fn, args);
-}
-
-size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 int decode(const void* q, const void* k_pool, const void* v_pool, const int32_t* prefix_table,
            const int32_t* prefix_lens, const int32_t* group_start, const int32_t* block_table,
@@ -286,11 +139,7 @@ int decode(const void* q, const void* k_pool, const void* v_pool, const int32_t*
   p.B = B; p.P = P; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.TB = 128 / p.G;
   p.bs = block_size; p.num_blocks = num_blocks;
   p.max_pblocks = max_prefix_blocks; p.max_blocks = max_blocks;
-  // Division by the block size as a product: with shift = 28 + ceil(log2(bs)) the
-  // rounded-up factor is below 2^30 and off by less than 2^-28 bs, relatively to
-  // 2^shift, which a dividend below 2^26 does not notice.
-  for (p.bs_shift = 28; (1LL << (p.bs_shift - 28)) < block_size;) ++p.bs_shift;
-  p.bs_mul = static_cast<unsigned>(((1ULL << p.bs_shift) + block_size - 1) / block_size);
+  block_divisor(block_size, &p.bs_mul, &p.bs_shift);
   const int keys = D == 256 ? PxShape<256>::KEYS : PxShape<128>::KEYS;
   for (p.R = 8; p.R < keys && block_size % (2 * p.R) == 0;) p.R *= 2;
   // log2(e) in the scale; a scale of 0 becomes the smallest normal number, which
@@ -323,9 +172,9 @@ int decode(const void* q, const void* k_pool, const void* v_pool, const int32_t*
   const size_t at_om = at_oo + up256(own_slots * p.G * D * 4);
   bool capturing = false;
   Workspace* ws = nullptr;
-  if ((rc = find_workspace(dev, stream, &capturing, &ws))) return rc;
+  if ((rc = PrefixWorkspaces::find(dev, stream, &capturing, &ws))) return rc;
   std::lock_guard<std::mutex> lk(ws->mu);
-  if ((rc = grow(ws, capturing, at_om + own_slots * p.G * 8, stream))) return rc;
+  if ((rc = PrefixWorkspaces::grow(ws, capturing, at_om + own_slots * p.G * 8, stream))) return rc;
   char* base = ws->base;
   p.head = reinterpret_cast<PxHeader*>(base);
   p.prefix_o = reinterpret_cast<float*>(base + at_po);
@@ -414,20 +263,7 @@ extern "C" int gqa_prefix_device_status(void* stream_, int clear) {
 
 extern "C" int gqa_prefix_release_graph_workspaces(void) {
   g_px_error[0] = 0;
-  std::lock_guard<std::mutex> lk(g_px_mu);
-  RelaxedCapture relaxed;
-  cudaError_t first = cudaSuccess;
-  for (auto it = g_px_ws.begin(); it != g_px_ws.end();) {
-    if (!it->first.capture) {
-      ++it;
-      continue;
-    }
-    cudaError_t e = cudaFree(it->second->base);
-    if (first == cudaSuccess) first = e;
-    for (char* p : it->second->outgrown) cudaFree(p);
-    it = g_px_ws.erase(it);
-  }
-  return first == cudaSuccess ? GQA_AV_OK : pfail_cuda(first, "cudaFree");
+  return PrefixWorkspaces::release_captured();
 }
 
 extern "C" const char* gqa_prefix_last_error(void) { return g_px_error; }
