@@ -9,8 +9,11 @@ the decode score step before it (include/gqa_qk.h):
 
 and both fused in one pass over the KV cache (include/gqa_attn.h). Around them
 for a paged cache: block tables, slots, and the norm, rotation and cache write of
-a step's tokens (include/gqa_kv.h), and decode attention over the paged cache for
-sequences that share prefixes (include/gqa_prefix.h).
+a step's tokens, forks, accepted drafts and release (include/gqa_kv.h), and decode
+attention over the paged cache for sequences that share prefixes
+(include/gqa_prefix.h). For several new tokens a sequence: causal attention of
+packed prompts and attention of drafted trees over the paged cache
+(include/gqa_prompt.h).
 
 ``workloads`` (seeded inputs) imports without the CUDA library; the binding
 functions below need the built library and raise ImportError without it.
@@ -26,7 +29,10 @@ _BINDING = ("gqa_av_decode", "gqa_av_decode_per_head", "gqa_av_decode_tuned",
             "gqa_attn_decode", "gqa_attn_plan", "gqa_attn_device_status",
             "gqa_kv_tables", "gqa_kv_norm_rope_append", "GQA_KV_F32",
             "gqa_prefix_attn_decode", "gqa_prefix_device_status",
-            "gqa_prefix_release_graph_workspaces")
+            "gqa_prefix_release_graph_workspaces",
+            "KvPools", "gqa_kv_fork", "gqa_kv_keep", "gqa_kv_release",
+            "gqa_prompt_attn", "gqa_tree_attn", "gqa_prompt_device_status",
+            "gqa_prompt_release_graph_workspaces")
 
 
 def __getattr__(name):

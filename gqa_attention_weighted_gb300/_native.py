@@ -95,6 +95,9 @@ def _load() -> ctypes.CDLL:
     lib.gqa_kv_tables.argtypes = [P] * 11 + [I] * 6 + [P]
     lib.gqa_kv_norm_rope_append.argtypes = [P, P, P, L, L, L, P, ctypes.POINTER(I), I, P, P, P, F,
                                             F, I, P, P, I, P, P, *[I] * 8, P]
+    lib.gqa_kv_fork.argtypes = [P, I, L, *[P] * 9, *[I] * 6, P]
+    lib.gqa_kv_keep.argtypes = [P, I, L, *[P] * 6, *[I] * 5, P]
+    lib.gqa_kv_release.argtypes = [*[P] * 7, *[I] * 5, P]
     lib.gqa_kv_last_error.argtypes = []
     lib.gqa_kv_last_error.restype = ctypes.c_char_p
     lib.gqa_prefix_attn_decode.argtypes = [P] * 9 + [I] * 10 + [F, P]
@@ -103,6 +106,18 @@ def _load() -> ctypes.CDLL:
     lib.gqa_prefix_selftest_wait_timeout.argtypes = [P] * 9 + [I] * 10 + [F, ctypes.c_longlong, I, P]
     lib.gqa_prefix_last_error.argtypes = []
     lib.gqa_prefix_last_error.restype = ctypes.c_char_p
+    lib.gqa_prompt_attn.argtypes = [P, L, *[P] * 7, *[I] * 9, F, P]
+    lib.gqa_tree_attn.argtypes = [P, L, *[P] * 5, I, *[P] * 3, *[I] * 9, F, P]
+    lib.gqa_prompt_device_status.argtypes = [P, I]
+    lib.gqa_prompt_release_graph_workspaces.argtypes = []
+    lib.gqa_prompt_selftest_wait_timeout.argtypes = [P, L, *[P] * 7, *[I] * 9, F,
+                                                     ctypes.c_longlong, I, P]
+    lib.gqa_prompt_last_error.argtypes = []
+    lib.gqa_prompt_last_error.restype = ctypes.c_char_p
+    for f in ("gqa_kv_fork", "gqa_kv_keep", "gqa_kv_release",
+              "gqa_prompt_attn", "gqa_tree_attn", "gqa_prompt_device_status",
+              "gqa_prompt_release_graph_workspaces", "gqa_prompt_selftest_wait_timeout"):
+        getattr(lib, f).restype = I
     for f in ("gqa_kv_tables", "gqa_kv_norm_rope_append", "gqa_prefix_attn_decode",
               "gqa_prefix_device_status", "gqa_prefix_release_graph_workspaces",
               "gqa_prefix_selftest_wait_timeout"):
@@ -508,6 +523,121 @@ def gqa_kv_norm_rope_append(q, k, v, positions, slots, inv_freq, q_out, k_pool, 
     return q_out
 
 
+# ------------------------------------------------- forks, drafts, release
+class KvPools:
+    """The K and V pools of all layers (any order), each [num_blocks, block_size, ...] and all of one
+    shape and type, as gqa_kv_fork and gqa_kv_keep take them. A server makes it once: it holds the
+    tensors and what the library needs of them."""
+
+    def __init__(self, pools):
+        self.pools = pools = tuple(pools)
+        if not pools or pools[0].dim() < 3:
+            raise ValueError("pools must be tensors [num_blocks, block_size, ...], one at least")
+        shape, dtype = pools[0].shape, pools[0].dtype
+        self.device = _device("pools[0]", pools[0])
+        for i, t in enumerate(pools):
+            if (t.shape != shape or t.dtype is not dtype or t.get_device() != self.device
+                    or not t.is_contiguous()):
+                _refuse(f"pools[{i}]", t, self.device,
+                        f"a contiguous CUDA {dtype} tensor of shape {tuple(shape)}")
+        self.num_blocks, self.block_size = shape[:2]
+        row = 1
+        for n in shape[2:]:
+            row *= n
+        self.row_bytes = row * pools[0].element_size()
+        self.array = (ctypes.c_void_p * len(pools))(*[t.data_ptr() for t in pools])
+
+    def args(self):
+        if self.device != torch.cuda.current_device():
+            raise ValueError(f"the pools are on cuda:{self.device}, the current device is "
+                             f"cuda:{torch.cuda.current_device()}")
+        return self.array, len(self.pools), self.row_bytes
+
+
+def gqa_kv_fork(pools, parent, child, block_table, seq_lens, shares, free_list, free_count,
+                fork_block, free_left, stream=None) -> None:
+    """Row ``child[f]`` of ``block_table`` becomes a continuation of row ``parent[f]``: full blocks
+    are shared (``shares`` += 1), a partial one is copied in all ``pools`` (a KvPools, or the
+    tensors) into a block off the end of ``free_list[:free_count]``. ``seq_lens`` of the children,
+    ``fork_block`` (the block of the copy, -1: none needed, -2: not served) and ``free_left`` are
+    written."""
+    if not isinstance(pools, KvPools):
+        pools = KvPools(pools)
+    array, n_pools, row_bytes = pools.args()
+    dev = pools.device
+    if block_table.dim() != 2 or free_list.dim() != 1 or parent.dim() != 1:
+        raise ValueError("block_table must be [B, max_blocks], free_list and parent of one dimension")
+    B, max_blocks = block_table.shape
+    N, n_free = parent.shape[0], free_list.shape[0]
+    _int32("block_table", block_table, (B, max_blocks), dev)
+    _int32("parent", parent, (N,), dev)
+    _int32("child", child, (N,), dev)
+    _int32("seq_lens", seq_lens, (B,), dev)
+    _int32("shares", shares, (pools.num_blocks,), dev)
+    _int32("free_list", free_list, (n_free,), dev)
+    _int32("free_count", free_count, (1,), dev)
+    _int32("fork_block", fork_block, (N,), dev)
+    _int32("free_left", free_left, (1,), dev)
+    _check_kv(lib.gqa_kv_fork(array, n_pools, row_bytes, _ptr(parent), _ptr(child),
+                              _ptr(block_table), _ptr(seq_lens), _ptr(shares), _ptr(free_list),
+                              _ptr(free_count), _ptr(fork_block), _ptr(free_left), N, B, max_blocks,
+                              n_free, pools.block_size, pools.num_blocks, _stream_handle(stream)))
+
+
+def gqa_kv_keep(pools, cached_lens, accepted, accepted_count, block_table, seq_lens, kept_lens,
+                stream=None) -> torch.Tensor:
+    """Moves the rows of accepted drafts together in all ``pools`` (a KvPools, or the tensors): row
+    ``cached_lens[b] + i`` gets what row ``cached_lens[b] + accepted[b, i]`` held, for the leading
+    numbers of ``accepted[b, :accepted_count[b]]`` that ascend and lie below ``seq_lens[b]``.
+    Writes and returns ``kept_lens``: the cached rows and the kept ones."""
+    if not isinstance(pools, KvPools):
+        pools = KvPools(pools)
+    array, n_pools, row_bytes = pools.args()
+    dev = pools.device
+    if block_table.dim() != 2 or accepted.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks], accepted [B, W]")
+    B, max_blocks = block_table.shape
+    W = accepted.shape[1]
+    _int32("block_table", block_table, (B, max_blocks), dev)
+    _int32("cached_lens", cached_lens, (B,), dev)
+    _int32("accepted", accepted, (B, W), dev)
+    _int32("accepted_count", accepted_count, (B,), dev)
+    _int32("seq_lens", seq_lens, (B,), dev)
+    _int32("kept_lens", kept_lens, (B,), dev)
+    _check_kv(lib.gqa_kv_keep(array, n_pools, row_bytes, _ptr(cached_lens), _ptr(accepted),
+                              _ptr(accepted_count), _ptr(block_table), _ptr(seq_lens),
+                              _ptr(kept_lens), B, W, max_blocks, pools.block_size,
+                              pools.num_blocks, _stream_handle(stream)))
+    return kept_lens
+
+
+def gqa_kv_release(block_table, old_lens, new_lens, shares, free_list, free_count, free_left,
+                   block_size: int, num_blocks=None, stream=None) -> None:
+    """Cuts row b of ``block_table`` from ``old_lens[b]`` rows to ``new_lens[b]`` (0: it has ended).
+    Its blocks past the new end lose an owner (``shares`` -= 1); those whose last owner let go are
+    appended to ``free_list[:free_count]``, and ``free_left`` gets the new count. ``shares`` [
+    num_blocks] may be None where no block is shared; ``num_blocks`` is needed then."""
+    if block_table.dim() != 2 or free_list.dim() != 1:
+        raise ValueError("block_table must be [B, max_blocks], free_list of one dimension")
+    if shares is None and num_blocks is None:
+        raise ValueError("num_blocks is needed without shares")
+    B, max_blocks = block_table.shape
+    n_free = free_list.shape[0]
+    num_blocks = int(shares.shape[0] if num_blocks is None else num_blocks)
+    dev = _device("block_table", block_table)
+    _int32("block_table", block_table, (B, max_blocks), dev)
+    _int32("old_lens", old_lens, (B,), dev)
+    _int32("new_lens", new_lens, (B,), dev)
+    if shares is not None:
+        _int32("shares", shares, (num_blocks,), dev)
+    _int32("free_list", free_list, (n_free,), dev)
+    _int32("free_count", free_count, (1,), dev)
+    _int32("free_left", free_left, (1,), dev)
+    _check_kv(lib.gqa_kv_release(_ptr(block_table), _ptr(old_lens), _ptr(new_lens), _ptr(shares),
+                                 _ptr(free_list), _ptr(free_count), _ptr(free_left), B, max_blocks,
+                                 n_free, int(block_size), num_blocks, _stream_handle(stream)))
+
+
 # ------------------------------------------- attention with shared prefixes
 def _check_prefix(status: int) -> None:
     if status != GQA_AV_OK:
@@ -568,3 +698,85 @@ def gqa_prefix_release_graph_workspaces() -> None:
     """Free what captured ``gqa_prefix_attn_decode`` calls hold. No graph that was captured before
     may be replayed afterwards."""
     _check_prefix(lib.gqa_prefix_release_graph_workspaces())
+
+
+# -------------------------------- attention of prompts and of drafted tokens
+def _check_prompt(status: int) -> None:
+    if status != GQA_AV_OK:
+        name = lib.gqa_av_status_string(status).decode()
+        raise GqaAvError(status, f"{name}: {lib.gqa_prompt_last_error().decode()}")
+
+
+def _packed_attn(q, k_pool, v_pool, token_start, cached_lens, block_table, seq_lens, out):
+    """The checks of both calls; the arguments around the mask, and B, T, ... of the library's."""
+    (num_blocks, block_size, Hkv, D), dev = _pools(k_pool, v_pool)
+    dtype = k_pool.dtype
+    if q.dim() != 3 or q.shape[2] != D or out.shape != q.shape:
+        raise ValueError(f"q and out must be [T,Hq,{D}], not {tuple(q.shape)} and "
+                         f"{tuple(out.shape)}")
+    T, Hq = q.shape[:2]
+    if q.dtype is not dtype or q.get_device() != dev:
+        _refuse("q", q, dev, "a CUDA tensor of the pools' type")
+    st = q.stride()
+    if T and (st[2] != 1 or (Hq > 1 and st[1] != D)):
+        raise ValueError("a token's heads must be contiguous in q")
+    if out.dtype is not dtype or out.get_device() != dev or not out.is_contiguous():
+        _refuse("out", out, dev, "a contiguous CUDA tensor of the pools' type")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_blocks]")
+    B, max_blocks = block_table.shape
+    _int32("block_table", block_table, (B, max_blocks), dev)
+    _int32("token_start", token_start, (B + 1,), dev)
+    if cached_lens is not None:
+        _int32("cached_lens", cached_lens, (B,), dev)
+    if seq_lens is not None:
+        _int32("seq_lens", seq_lens, (B,), dev)
+    return (dev, (_ptr(q), st[0], _ptr(k_pool), _ptr(v_pool), _ptr(token_start), _ptr(cached_lens)),
+            (_ptr(block_table), _ptr(seq_lens), _ptr(out), B, T, Hq, Hkv, D, _V_DTYPE[dtype],
+             block_size, num_blocks, max_blocks))
+
+
+def gqa_prompt_attn(q, k_pool, v_pool, token_start, cached_lens, block_table, seq_lens, out,
+                    scale=None, stream=None) -> torch.Tensor:
+    """Causal attention of packed prompts, or chunks of them, over a paged cache that holds their
+    rows: token ``token_start[b] + i`` is row ``cached_lens[b] + i`` of sequence b (None: 0) and
+    attends to the rows up to itself that are below ``seq_lens[b]`` (None: all) of
+    ``block_table[b]``. q is [T,Hq,D] of the pools' type, a view of a packed projection or not
+    (scale defaults to 1/sqrt(D)); writes and returns ``out``, whose rows past the last sequence
+    are left as they are. Calls on different streams and replays of different graphs may overlap."""
+    dev, before, after = _packed_attn(q, k_pool, v_pool, token_start, cached_lens, block_table,
+                                      seq_lens, out)
+    sc = float(q.shape[2]) ** -0.5 if scale is None else float(scale)
+    _check_prompt(lib.gqa_prompt_attn(*before, *after, sc, _stream_handle(stream)))
+    return out
+
+
+def gqa_tree_attn(q, k_pool, v_pool, token_start, cached_lens, tree_mask, block_table, seq_lens,
+                  out, scale=None, stream=None) -> torch.Tensor:
+    """Attention of drafted tokens over a paged cache that holds their rows: token
+    ``token_start[b] + i`` attends to the ``cached_lens[b]`` rows of ``block_table[b]`` and to the
+    drafted rows behind them, row j where bit j % 32 of ``tree_mask[t, j // 32]`` is set (itself
+    among them), all below ``seq_lens[b]`` (None: all). tree_mask is [T,words] int32; the rest as
+    for gqa_prompt_attn."""
+    if cached_lens is None:
+        raise ValueError("gqa_tree_attn needs cached_lens")
+    dev, before, after = _packed_attn(q, k_pool, v_pool, token_start, cached_lens, block_table,
+                                      seq_lens, out)
+    if tree_mask.dim() != 2:
+        raise ValueError("tree_mask must be [T, words]")
+    words = tree_mask.shape[1]
+    _int32("tree_mask", tree_mask, (q.shape[0], words), dev)
+    sc = float(q.shape[2]) ** -0.5 if scale is None else float(scale)
+    _check_prompt(lib.gqa_tree_attn(*before, _ptr(tree_mask), words, *after, sc,
+                                    _stream_handle(stream)))
+    return out
+
+
+def gqa_prompt_device_status(stream=None, clear: bool = True) -> None:
+    _check_prompt(lib.gqa_prompt_device_status(_stream_handle(stream), 1 if clear else 0))
+
+
+def gqa_prompt_release_graph_workspaces() -> None:
+    """Free what captured ``gqa_prompt_attn`` and ``gqa_tree_attn`` calls hold. No graph that was
+    captured before may be replayed afterwards."""
+    _check_prompt(lib.gqa_prompt_release_graph_workspaces())

@@ -19,7 +19,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIBRARY = os.path.join(PKG, "libgqa_av.so")
 
 SOURCES = ["gqa_av_api.cu", "gqa_av_bf16.cu", "gqa_av_fp16.cu", "gqa_av_noalloc.cu", "gqa_qk_api.cu",
-           "gqa_attn_api.cu", "gqa_kv_api.cu", "gqa_prefix_api.cu"]
+           "gqa_attn_api.cu", "gqa_kv_api.cu", "gqa_prefix_api.cu", "gqa_prompt_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC",
                      "-diag-suppress", "1160", "-I", INCLUDE, "-I", CSRC]

@@ -1,5 +1,6 @@
 // Host side of the C ABI declared in include/gqa_kv.h: argument checks and
-// dispatch of the block-table and the norm + rotation + cache-write kernels.
+// dispatch of the block-table, the norm + rotation + cache-write and the fork,
+// keep and release kernels.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -9,6 +10,7 @@
 
 #include "gqa_kv.h"
 #include "gqa_kv_kernel.cuh"
+#include "gqa_kv_pages.cuh"
 
 namespace gqa_av {
 namespace {
@@ -40,18 +42,68 @@ int check_pool(int block_size, int num_blocks) {
 }
 
 cudaError_t launch(const void* fn, int grid, int block, size_t smem, cudaStream_t stream,
-                   void** args) {
+                   void** args, int cluster = 1) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(block);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+// A run of n bytes of device memory, by name.
+struct Range {
+  const char* name;
+  const void* at;
+  unsigned long long n;
+};
+bool meet(const Range& a, const Range& b) {
+  return a.at && b.at && a.n && b.n && addr(a.at) < addr(b.at) + b.n && addr(b.at) < addr(a.at) + a.n;
+}
+
+// Pools of one layout, given by their rows' bytes.
+int check_pools(void* const* pools, int n_pools, int64_t row_bytes, int block_size, int num_blocks) {
+  if (n_pools < 0 || row_bytes <= 0 || (n_pools && !pools))
+    return kfail(GQA_AV_ERR_INVALID, "n_pools=%d must not be negative, row_bytes=%lld positive and "
+                 "pools given", n_pools, static_cast<long long>(row_bytes));
+  if (n_pools > kPagePools)
+    return kfail(GQA_AV_ERR_UNSUPPORTED, "n_pools=%d is above %d", n_pools, kPagePools);
+  if (row_bytes % 16 || row_bytes > (1 << 20))
+    return kfail(GQA_AV_ERR_UNSUPPORTED, "row_bytes=%lld must be a multiple of 16, at most 2^20",
+                 static_cast<long long>(row_bytes));
+  const int rc = check_pool(block_size, num_blocks);
+  if (rc) return rc;
+  for (int i = 0; i < n_pools; ++i) {
+    if (!pools[i]) return kfail(GQA_AV_ERR_INVALID, "pools[%d] is NULL", i);
+    if (addr(pools[i]) & 15u)
+      return kfail(GQA_AV_ERR_UNSUPPORTED, "pools[%d] must be 16-byte aligned", i);
+  }
+  // Rows that are moved twice would be lost.
+  uintptr_t at[kPagePools];
+  for (int i = 0; i < n_pools; ++i) at[i] = addr(pools[i]);
+  std::sort(at, at + n_pools);
+  const unsigned long long bytes = static_cast<unsigned long long>(row_bytes) * block_size * num_blocks;
+  for (int i = 1; i < n_pools; ++i)
+    if (at[i] - at[i - 1] < bytes) return kfail(GQA_AV_ERR_INVALID, "two pools overlap");
+  return GQA_AV_OK;
+}
+
+// Tables and lengths of the calls below: their sizes.
+int check_rows(int B, int max_blocks, int block_size) {
+  if (B <= 0 || max_blocks <= 0)
+    return kfail(GQA_AV_ERR_INVALID, "B=%d and max_blocks=%d must be positive", B, max_blocks);
+  if (B > kPageMaxB) return kfail(GQA_AV_ERR_UNSUPPORTED, "B=%d is above %d", B, kPageMaxB);
+  if (block_size > 0 && static_cast<long long>(max_blocks) * block_size > 0x7fffffffLL)
+    return kfail(GQA_AV_ERR_UNSUPPORTED, "a table row of 2^31 or more cache rows");
+  return GQA_AV_OK;
 }
 
 using RopeKernel = void (*)(RopeParams);
@@ -227,6 +279,161 @@ extern "C" int gqa_kv_norm_rope_append(
   e = launch(reinterpret_cast<const void*>(fn), grid, 32 * kRopeWarps, 0,
              static_cast<cudaStream_t>(stream), args);
   if (e != cudaSuccess) return kfail_cuda(e, "norm and rotation kernel launch");
+  return GQA_AV_OK;
+}
+
+extern "C" int gqa_kv_fork(void* const* pools, int n_pools, int64_t row_bytes,
+                           const int32_t* parent, const int32_t* child, int32_t* block_table,
+                           int32_t* seq_lens, int32_t* shares, const int32_t* free_list,
+                           const int32_t* free_count, int32_t* fork_block, int32_t* free_left,
+                           int N, int B, int max_blocks, int n_free, int block_size,
+                           int num_blocks, void* stream) {
+  g_kv_error[0] = 0;
+  if (N < 0 || n_free < 0)
+    return kfail(GQA_AV_ERR_INVALID, "N=%d and n_free=%d must not be negative", N, n_free);
+  int rc = check_pools(pools, n_pools, row_bytes, block_size, num_blocks);
+  if (!rc) rc = check_rows(B, max_blocks, block_size);
+  if (rc) return rc;
+  if (N > kPageMaxB) return kfail(GQA_AV_ERR_UNSUPPORTED, "N=%d is above %d", N, kPageMaxB);
+  if (!block_table || !seq_lens || !shares || !free_count || !free_left ||
+      (N && (!parent || !child || !fork_block)) || (n_free && !free_list))
+    return kfail(GQA_AV_ERR_INVALID, "a required pointer is NULL");
+  if ((addr(parent) | addr(child) | addr(block_table) | addr(seq_lens) | addr(shares) |
+       addr(free_list) | addr(free_count) | addr(fork_block) | addr(free_left)) & 3u)
+    return kfail(GQA_AV_ERR_INVALID, "pointers must be 4-byte aligned");
+  // Every CTA reads the inputs, at any time while others write.
+  const unsigned long long n4 = 4ull * N, rows = 4ull * B * max_blocks;
+  const Range ins[] = {{"parent", parent, n4}, {"child", child, n4},
+                       {"free_list", free_list, 4ull * n_free}, {"free_count", free_count, 4}};
+  const Range outs[] = {{"block_table", block_table, rows}, {"seq_lens", seq_lens, 4ull * B},
+                        {"shares", shares, 4ull * num_blocks}, {"fork_block", fork_block, n4},
+                        {"free_left", free_left, 4}};
+  constexpr int kOuts = sizeof outs / sizeof outs[0];
+  for (int o = 0; o < kOuts; ++o) {
+    for (const Range& i : ins)
+      if (meet(i, outs[o])) return kfail(GQA_AV_ERR_INVALID, "%s overlaps %s", outs[o].name, i.name);
+    for (int q = 0; q < o; ++q)
+      if (meet(outs[q], outs[o]))
+        return kfail(GQA_AV_ERR_INVALID, "%s overlaps %s", outs[o].name, outs[q].name);
+  }
+
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return kfail_cuda(e, "cudaGetDevice");
+  ForkParams p;
+  std::copy(pools, pools + n_pools, reinterpret_cast<void**>(p.pools.at));
+  p.parent = parent; p.child = child; p.table = block_table; p.seq_lens = seq_lens;
+  p.shares = shares; p.free_list = free_list; p.free_count = free_count;
+  p.fork_block = fork_block; p.free_left = free_left;
+  p.row_bytes = row_bytes; p.n_pools = n_pools; p.N = N; p.B = B; p.max_blocks = max_blocks;
+  p.n_free = n_free; p.bs = block_size; p.num_blocks = num_blocks;
+  const size_t smem = 8 * (static_cast<size_t>(B) + N);
+  const void* fn = reinterpret_cast<const void*>(gqa_kv_fork_kernel);
+  if (smem > 40960) {   // within the default limit otherwise
+    e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 16 * kPageMaxB);
+    if (e != cudaSuccess) return kfail_cuda(e, "cudaFuncSetAttribute");
+  }
+  // Two CTAs an SM where every warp has a piece to copy, fewer with fewer pieces.
+  const long long pieces =
+      ((block_size - 1) * static_cast<long long>(row_bytes) + kForkPiece - 1) / kForkPiece;
+  const long long ctas = (static_cast<long long>(N) * n_pools * pieces + 15) / 16;
+  const int grid = static_cast<int>(std::min<long long>(2LL * sms, std::max<long long>(1, std::max<long long>(N, ctas))));
+  void* args[] = {&p};
+  e = launch(fn, grid, kForkThreads, smem, static_cast<cudaStream_t>(stream), args);
+  if (e != cudaSuccess) return kfail_cuda(e, "fork kernel launch");
+  return GQA_AV_OK;
+}
+
+extern "C" int gqa_kv_keep(void* const* pools, int n_pools, int64_t row_bytes,
+                           const int32_t* cached_lens, const int32_t* accepted,
+                           const int32_t* accepted_count, const int32_t* block_table,
+                           const int32_t* seq_lens, int32_t* kept_lens, int B, int W,
+                           int max_blocks, int block_size, int num_blocks, void* stream) {
+  g_kv_error[0] = 0;
+  if (W < 0) return kfail(GQA_AV_ERR_INVALID, "W=%d must not be negative", W);
+  int rc = check_pools(pools, n_pools, row_bytes, block_size, num_blocks);
+  if (!rc) rc = check_rows(B, max_blocks, block_size);
+  if (rc) return rc;
+  if (!n_pools) return kfail(GQA_AV_ERR_INVALID, "no pools");
+  if (W > (1 << 20)) return kfail(GQA_AV_ERR_UNSUPPORTED, "W=%d is above 2^20", W);
+  if (!cached_lens || !accepted_count || !block_table || !seq_lens || !kept_lens || (W && !accepted))
+    return kfail(GQA_AV_ERR_INVALID, "a required pointer is NULL");
+  if ((addr(cached_lens) | addr(accepted) | addr(accepted_count) | addr(block_table) |
+       addr(seq_lens) | addr(kept_lens)) & 3u)
+    return kfail(GQA_AV_ERR_INVALID, "pointers must be 4-byte aligned");
+  const Range out = {"kept_lens", kept_lens, 4ull * B};
+  for (const Range& i : {Range{"cached_lens", cached_lens, 4ull * B},
+                         Range{"accepted", accepted, 4ull * B * W},
+                         Range{"accepted_count", accepted_count, 4ull * B},
+                         Range{"block_table", block_table, 4ull * B * max_blocks},
+                         Range{"seq_lens", seq_lens, 4ull * B}})
+    if (meet(i, out)) return kfail(GQA_AV_ERR_INVALID, "kept_lens overlaps %s", i.name);
+
+  KeepParams p;
+  std::copy(pools, pools + n_pools, reinterpret_cast<void**>(p.pools.at));
+  p.cached = cached_lens; p.accepted = accepted; p.count = accepted_count; p.table = block_table;
+  p.seq_lens = seq_lens; p.kept = kept_lens;
+  p.row_bytes = row_bytes; p.n_pools = n_pools; p.B = B; p.W = W; p.max_blocks = max_blocks;
+  p.bs = block_size; p.num_blocks = num_blocks;
+  p.parts = static_cast<int>((row_bytes + 511) / 512);
+  const long long tasks = static_cast<long long>(B) * n_pools * p.parts;
+  const long long grid = (tasks + kKeepWarps - 1) / kKeepWarps;
+  if (grid > 0x7fffffffLL)
+    return kfail(GQA_AV_ERR_UNSUPPORTED, "B=%d requests in %d pools of rows of %lld bytes are too many",
+                 B, n_pools, static_cast<long long>(row_bytes));
+  void* args[] = {&p};
+  cudaError_t e = launch(reinterpret_cast<const void*>(gqa_kv_keep_kernel), static_cast<int>(grid),
+                         32 * kKeepWarps, 0, static_cast<cudaStream_t>(stream), args);
+  if (e != cudaSuccess) return kfail_cuda(e, "keep kernel launch");
+  return GQA_AV_OK;
+}
+
+extern "C" int gqa_kv_release(const int32_t* block_table, const int32_t* old_lens,
+                              const int32_t* new_lens, int32_t* shares, int32_t* free_list,
+                              const int32_t* free_count, int32_t* free_left, int B,
+                              int max_blocks, int n_free, int block_size, int num_blocks,
+                              void* stream) {
+  g_kv_error[0] = 0;
+  if (n_free < 0) return kfail(GQA_AV_ERR_INVALID, "n_free=%d must not be negative", n_free);
+  int rc = check_pool(block_size, num_blocks);
+  if (!rc) rc = check_rows(B, max_blocks, block_size);
+  if (rc) return rc;
+  const long long most = static_cast<long long>(B) * max_blocks;
+  if (most >= 1 << 30)
+    return kfail(GQA_AV_ERR_UNSUPPORTED, "B * max_blocks = %lld must be below 2^30", most);
+  if (!block_table || !old_lens || !new_lens || !free_count || !free_left || (n_free && !free_list))
+    return kfail(GQA_AV_ERR_INVALID, "a required pointer is NULL");
+  if ((addr(block_table) | addr(old_lens) | addr(new_lens) | addr(shares) | addr(free_list) |
+       addr(free_count) | addr(free_left)) & 3u)
+    return kfail(GQA_AV_ERR_INVALID, "pointers must be 4-byte aligned");
+  const Range ins[] = {{"block_table", block_table, 4ull * B * max_blocks},
+                       {"old_lens", old_lens, 4ull * B}, {"new_lens", new_lens, 4ull * B},
+                       {"free_count", free_count, 4}};
+  const Range outs[] = {{"shares", shares, 4ull * num_blocks}, {"free_list", free_list, 4ull * n_free},
+                        {"free_left", free_left, 4}};
+  for (int o = 0; o < 3; ++o) {
+    for (const Range& i : ins)
+      if (meet(i, outs[o])) return kfail(GQA_AV_ERR_INVALID, "%s overlaps %s", outs[o].name, i.name);
+    for (int q = 0; q < o; ++q)
+      if (meet(outs[q], outs[o]))
+        return kfail(GQA_AV_ERR_INVALID, "%s overlaps %s", outs[o].name, outs[q].name);
+  }
+
+  ReleaseParams p;
+  p.table = block_table; p.old_lens = old_lens; p.new_lens = new_lens; p.shares = shares;
+  p.free_list = free_list; p.free_count = free_count; p.free_left = free_left;
+  p.B = B; p.max_blocks = max_blocks; p.n_free = n_free; p.bs = block_size;
+  p.num_blocks = num_blocks;
+  const void* fn = reinterpret_cast<const void*>(gqa_kv_release_kernel);
+  const size_t smem = 4 * (2 * static_cast<size_t>(B) + 1 + kReleaseCache);
+  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       4 * (2 * kPageMaxB + 1 + kReleaseCache));
+  if (e != cudaSuccess) return kfail_cuda(e, "cudaFuncSetAttribute");
+  const int ctas = most > 4 * kReleaseThreads ? kReleaseCluster : 1;
+  void* args[] = {&p};
+  e = launch(fn, ctas, kReleaseThreads, smem, static_cast<cudaStream_t>(stream), args, ctas);
+  if (e != cudaSuccess) return kfail_cuda(e, "release kernel launch");
   return GQA_AV_OK;
 }
 

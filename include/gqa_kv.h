@@ -1,7 +1,8 @@
 /*
  * gqa_kv.h -- C ABI of the GB300 (sm_103a) steps that feed a paged KV cache:
- * block tables and slots from request lengths, and the norm, rotation and
- * cache write of a step's new tokens. The cache is the one that
+ * block tables and slots from request lengths, the norm, rotation and cache
+ * write of a step's new tokens, and what happens to a request's blocks later
+ * (forks, accepted drafts, release). The cache is the one that
  * gqa_av_decode_paged (gqa_av.h) and gqa_prefix_attn_decode (gqa_prefix.h)
  * read: pools [num_blocks, block_size, Hkv, D], row c of sequence b in block
  * block_table[b][c / block_size]. A slot is a row of the flattened pool,
@@ -122,6 +123,104 @@ int gqa_kv_norm_rope_append(const void *q, const void *k, const void *v, int64_t
                             void *q_out, int q_out_dtype, void *k_pool, void *v_pool, int T,
                             int Hq, int Hkv, int D, int rot_dim, int kv_dtype, int block_size,
                             int num_blocks, void *stream);
+
+/*
+ * The calls below handle blocks that requests share. shares[x] counts the
+ * owners of block x beyond the first: 0 for a block that gqa_kv_tables handed
+ * out, one more for every fork that shares it, one less for every owner that
+ * releases it, and back to the free list when the last one does. `pools` is an
+ * array in HOST memory of n_pools device pointers: the K and V pools of all
+ * layers (their order does not matter), each [num_blocks, block_size,
+ * row_bytes] bytes; a pool may not be named twice. Limits: n_pools <= 256,
+ * row_bytes a multiple of 16 and at most 2^20, pools 16-byte aligned, B <= 8192,
+ * max_blocks * block_size and num_blocks * block_size below 2^31.
+ */
+
+/*
+ * Fork requests: fork f makes row child[f] of the block table a continuation of
+ * row parent[f]. With L = seq_lens[parent[f]] (clamped to what a table row can
+ * hold), the child gets the parent's L / block_size full blocks (shares += 1
+ * each) and, where L ends inside a block, a block of its own with a copy of the
+ * parent's L % block_size rows in every pool; seq_lens[child[f]] = L. The parent
+ * keeps its partial block. Blocks for the copies come off the end of free_list
+ * (free_count[0] entries) in the order of the forks that need one:
+ *
+ *     fork_block[f] = free_list[free_count[0] - 1 - (forks before f that need one)].
+ *
+ * fork_block[f] is -1 when no copy is needed, and -2 when the fork is not served
+ * (its child's row, length and everything else are left as they are): a row
+ * outside [0, B), a child that is a parent of any fork or that an earlier fork
+ * names too, or no free block. free_left[0] = free_count[0] - the blocks taken.
+ * Table entries and list entries outside [0, num_blocks) are handed on, but
+ * nothing is counted or copied for them (a negative list entry is handed on as
+ * 2^31 - 1). Entries of the child's row past its blocks are kept. Two served
+ * forks must not get one block (a free list that names it twice).
+ *
+ *     parent, child [N] int32 (a parent may have several children)
+ *     block_table [B, max_blocks], seq_lens [B], shares [num_blocks] int32, updated in place
+ *     free_list [n_free], free_count [1] int32; free_count is clamped to [0, n_free]
+ *     fork_block [N], free_left [1] int32
+ *
+ * N <= 8192 and may be 0. No output may overlap an input or another output.
+ */
+int gqa_kv_fork(void *const *pools, int n_pools, int64_t row_bytes, const int32_t *parent,
+                const int32_t *child, int32_t *block_table, int32_t *seq_lens, int32_t *shares,
+                const int32_t *free_list, const int32_t *free_count, int32_t *fork_block,
+                int32_t *free_left, int N, int B, int max_blocks, int n_free, int block_size,
+                int num_blocks, void *stream);
+
+/*
+ * Keep accepted drafts: request b holds cached_lens[b] rows and, behind them,
+ * drafted rows up to seq_lens[b]. accepted[b][i], i < accepted_count[b], are the
+ * accepted drafts' numbers, counted from cached_lens[b], in ascending order (a
+ * path of a tree whose tokens are numbered parents first). In every pool
+ *
+ *     row cached_lens[b] + i = what row cached_lens[b] + accepted[b][i] held,   0 <= i < n_b,
+ *     kept_lens[b] = cached_lens[b] + n_b,
+ *
+ * where n_b is the length of the longest leading part of the accepted numbers
+ * that ascend strictly, are not negative and lie below seq_lens[b] (and within
+ * W and the table's row). Rows from kept_lens[b] on are left as they are;
+ * gqa_kv_release takes their blocks. A row whose table entry lies outside
+ * [0, num_blocks) is neither read nor written. No two requests may share a block
+ * that holds drafted rows (a fork copies partial blocks, so none do).
+ *
+ *     cached_lens, accepted_count, seq_lens [B], accepted [B, W], block_table [B, max_blocks] int32
+ *     kept_lens [B] int32; must not overlap an input
+ *
+ * Negative cached_lens count as 0. W <= 2^20 and may be 0; n_pools >= 1.
+ */
+int gqa_kv_keep(void *const *pools, int n_pools, int64_t row_bytes, const int32_t *cached_lens,
+                const int32_t *accepted, const int32_t *accepted_count, const int32_t *block_table,
+                const int32_t *seq_lens, int32_t *kept_lens, int B, int W, int max_blocks,
+                int block_size, int num_blocks, void *stream);
+
+/*
+ * Release blocks: row b of the block table is cut from old_lens[b] rows to
+ * new_lens[b] (0: the request has ended). Its blocks of the columns from
+ * blocks(new_lens[b]) to blocks(old_lens[b]) lose an owner, blocks(n) =
+ * ceil(n / block_size). With k_x the number of such entries of the whole table
+ * that name block x: if k_x <= shares[x], shares[x] -= k_x; else the last owner
+ * is gone, shares[x] = 0 and x goes to the end of the free list. The blocks that
+ * go there follow one another in the order of their first such entries, row
+ * after row and column after column:
+ *
+ *     free_list[free_count[0] + i] = the i-th of them,   free_left[0] = free_count[0] + their number
+ *
+ * (those past n_free are dropped, and free_left is at most n_free). Entries outside
+ * [0, num_blocks) are skipped. shares NULL: no block is shared, every entry goes
+ * back, and no two entries may name one block. The block table itself is kept.
+ *
+ *     block_table [B, max_blocks], old_lens, new_lens [B] int32 (new_lens is clamped to [0, old_lens])
+ *     shares [num_blocks] int32 (not negative) and free_list [n_free] int32, updated in place
+ *     free_count, free_left [1] int32; free_count is clamped to [0, n_free]
+ *
+ * B * max_blocks < 2^30. No output may overlap an input or another output.
+ */
+int gqa_kv_release(const int32_t *block_table, const int32_t *old_lens, const int32_t *new_lens,
+                   int32_t *shares, int32_t *free_list, const int32_t *free_count,
+                   int32_t *free_left, int B, int max_blocks, int n_free, int block_size,
+                   int num_blocks, void *stream);
 
 /* Message of the calling thread's last error of these calls ("" if none). */
 const char *gqa_kv_last_error(void);
