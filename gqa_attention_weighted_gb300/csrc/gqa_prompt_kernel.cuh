@@ -64,9 +64,10 @@ namespace gqa_av {
 
 constexpr int kPtThreads = 384;
 // Registers a thread: 168 at launch (65536 / 384, rounded down to 8); the last
-// warpgroup gives some to the softmax warpgroups: 2 * 128 * 184 + 128 * 136 =
-// 384 * 168.
-constexpr int kPtSoftmaxRegs = 184, kPtAuxRegs = 136;
+// warpgroup gives some to the softmax warpgroups, whose threads hold a row's 128
+// scores: 2 * 128 * 208 + 128 * 88 = 384 * 168. (At 184 they spill, which costs more
+// than reading the scores twice.)
+constexpr int kPtSoftmaxRegs = 208, kPtAuxRegs = 88;
 constexpr int kPtMmaWarp = 8, kPtKWarp = 9, kPtVWarp = 10, kPtCleanWarp = 11;
 constexpr int kPtMaxB = 8192;          // 16 bytes of the plan's shared memory each
 constexpr int kPtSegs = 2;             // unit descriptors in flight
@@ -92,8 +93,9 @@ struct PtShape {
   static constexpr int STAGE = KEYS * D * 2;           // bytes of a K or V stage
   static constexpr int QBYTES = 128 * D * 2;
   static constexpr int QBUF = NS;                      // query buffers
-  static constexpr int STAGES = D == 64 ? 11 : 5;
-  static constexpr int TILES_BYTES = QBUF * QBYTES + STAGES * STAGE;
+  static constexpr int KST = D == 64 ? 5 : 2;          // stages of K, and of V, which is held longer
+  static constexpr int VST = D == 64 ? 6 : 3;
+  static constexpr int TILES_BYTES = QBUF * QBYTES + (KST + VST) * STAGE;
   static constexpr int MISC = D == 64 ? 2048 : 1024;   // barriers, units
   static constexpr int SMEM = TILES_BYTES + MISC + 2048;
   static constexpr uint32_t S_COL = KEYS;              // tensor-memory columns of an S buffer
@@ -174,11 +176,6 @@ __device__ __forceinline__ PtShare pt_share(const PromptParams& p, const PtUnit&
   }
   return s;
 }
-
-// Positions of tile i's K and V in the unit's run of 2 n stages, about the
-// order of their first use: K0 K1 V0 K2 V1 ... K(n-1) V(n-2) V(n-1).
-__device__ __forceinline__ int pt_k_pos(int i) { return i == 0 ? 0 : 2 * i - 1; }
-__device__ __forceinline__ int pt_v_pos(int i, int n) { return min(2 * i + 2, 2 * n - 1); }
 
 // Bits c = 0 .. n - 1 of 32.
 __device__ __forceinline__ uint32_t below32(int n) {
@@ -386,7 +383,8 @@ template <typename Tag, int D>
 __global__ void __launch_bounds__(kPtThreads, 1)
     gqa_prompt_kernel(const __grid_constant__ PromptParams p) {
   using Shape = PtShape<D>;
-  constexpr int NS = Shape::NS, KEYS = Shape::KEYS, STAGES = Shape::STAGES, PARTS = Shape::PARTS;
+  constexpr int NS = Shape::NS, KEYS = Shape::KEYS, PARTS = Shape::PARTS;
+  constexpr int KST = Shape::KST, VST = Shape::VST;
   // fp16 weights are scaled by 2^6 (at most 2^14 with the growth allowance), so
   // that small ones keep their bits; the sum carries the same factor.
   constexpr float kOff = std::is_same<Tag, Fp16Tag>::value ? 6.0f : 0.0f;
@@ -396,14 +394,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Shape::TILES_BYTES);
-  const uint32_t full0 = smem_addr(bars), empty0 = full0 + 8 * STAGES;
-  const uint32_t qfull0 = empty0 + 8 * STAGES, qempty0 = qfull0 + 16;
+  const uint32_t kfull0 = smem_addr(bars), kempty0 = kfull0 + 8 * KST;
+  const uint32_t vfull0 = kempty0 + 8 * KST, vempty0 = vfull0 + 8 * VST;
+  const uint32_t qfull0 = vempty0 + 8 * VST, qempty0 = qfull0 + 16;
   const uint32_t sfull0 = qempty0 + 16, pfull0 = sfull0 + 16;   // a stream's, or an S buffer's
   const uint32_t ofull0 = pfull0 + 16, ofree0 = ofull0 + 16, pvdone = ofree0 + 16;
   const uint32_t meet = pvdone + 8, drain = meet + 8, clean0 = drain + 8;
   const uint32_t issued0 = clean0 + 8 * kPtCleans;
   const uint32_t ufull0 = issued0 + 8 * kPtCleans, uempty0 = ufull0 + 8 * kPtSegs;
-  constexpr int kBars = 2 * STAGES + 15 + 2 * kPtCleans + 2 * kPtSegs;
+  constexpr int kBars = 2 * (KST + VST) + 15 + 2 * kPtCleans + 2 * kPtSegs;
   struct Seg {
     PtUnit u;
     int kv;
@@ -415,7 +414,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   float2* ml = reinterpret_cast<float2*>(smem + Shape::TILES_BYTES + Shape::MISC);   // [2][128]
   static_assert(8 * (kBars + 1) + sizeof(Seg) * kPtSegs + 24 <= Shape::MISC,
                 "shared memory besides the tiles");
-  static_assert(kPtCleans > STAGES && 16 * (kPtMaxB + 1) + 4 * kPtBuckets + 128 <= Shape::TILES_BYTES,
+  static_assert(kPtCleans > VST && 16 * (kPtMaxB + 1) + 4 * kPtBuckets + 128 <= Shape::TILES_BYTES,
                 "barriers of cleared tiles; the plan's memory");
 
   if (warp == kPtMmaWarp) {
@@ -426,10 +425,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) {
-      mbar_init(full0 + 8 * i, 1);
-      mbar_init(empty0 + 8 * i, 1);
-    }
+    for (int i = 0; i < 2 * (KST + VST); ++i) mbar_init(kfull0 + 8 * i, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(qfull0 + 8 * i, 1);
       mbar_init(qempty0 + 8 * i, 1);
@@ -467,7 +463,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     if (threadIdx.x == 0) atomicExch(&p.head->ready, 1u);
   }
   const uint32_t tmem = uniform(*tmem_slot);
-  const uint32_t qbuf_s = base_s, ring_s = base_s + Shape::QBUF * Shape::QBYTES;
+  const uint32_t qbuf_s = base_s, k_s = base_s + Shape::QBUF * Shape::QBYTES;
+  const uint32_t v_s = k_s + KST * Shape::STAGE;
   const bool aligned = (base_s & 1023u) == 0;   // the tiles need it; dynamic memory starts so
   if (!aligned && threadIdx.x == 0) atomicOr(&pt_status, kErrPtLoad);
 
@@ -480,7 +477,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const uint64_t policy = evict_first_policy();
       const int nch = KEYS / p.R;              // boxes of one 64-column part of a tile
       const int oob = p.num_blocks * p.bs;
-      unsigned base = 0, fills = 0, cleans = 0;
+      const int stages = is_k ? KST : VST;
+      const uint32_t full0 = is_k ? kfull0 : vfull0, empty0 = is_k ? kempty0 : vempty0;
+      const uint32_t ring_s = is_k ? k_s : v_s;
+      int stage = 0;
+      uint32_t parity = 0;                     // of the stage's next fill
+      unsigned fills = 0, cleans = 0;
       // Lane s: 1 + parity of this warp's last copy into stage s (0: none yet);
       // lane 16 + s: into query buffer s.
       unsigned held = 0;
@@ -552,11 +554,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int first_clean = uniform(pt_share<D>(p, u).full) / KEYS - uniform(u.t0);
         for (int i = 0; i < n && ok; ++i) {
           const int ahead = row_of(i + 1);
-          const unsigned at = base + (is_k ? pt_k_pos(i) : pt_v_pos(i, n)), stage = at % STAGES;
-          if (!(ok = warp_poll(empty0 + 8 * stage, ((at / STAGES) & 1) ^ 1, p.timeout_ns))) break;
+          if (!(ok = warp_poll(empty0 + 8 * stage, parity ^ 1, p.timeout_ns))) break;
           const uint32_t bar = full0 + 8 * stage, dst = ring_s + stage * Shape::STAGE;
           expect_one(leader, bar, Shape::STAGE);
-          if (lane == stage) held = 1 + ((at / STAGES) & 1);
+          if (lane == stage) held = 1 + parity;
           for (int c = 0; c < nch; ++c) {
             const int r = __shfl_sync(0xffffffffu, row, c);
 #pragma unroll
@@ -571,22 +572,21 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (lane == 0) mbar_arrive(issued0 + 8 * (cleans % kPtCleans));
             ++cleans;
           }
+          if (++stage == stages) stage = 0, parity ^= 1;
           row = ahead;
         }
-        base += 2 * n;
         if (is_k) next = __shfl_sync(0xffffffffu, claim, 0);
       }
       if (!ok) {
-        // This warp's copies in flight land before the CTA leaves (a wait for a
-        // stage that the other loader has filled since takes its full 2 s).
+        // This warp's copies in flight land before the CTA leaves.
         if (lane == 0) atomicOr(&pt_status, kErrPtLoad);
-        if (held && lane < STAGES) mbar_wait(full0 + 8 * lane, held - 1, kPtTimeoutNs);
+        if (held && lane < stages) mbar_wait(full0 + 8 * lane, held - 1, kPtTimeoutNs);
         if (held && lane >= 16) mbar_wait(qfull0 + 8 * (lane - 16), held - 1, kPtTimeoutNs);
         __syncwarp();
       }
     } else if (aligned && warp == kPtCleanWarp) {
       // ------------------------------------------------------ V's masked rows
-      unsigned base = 0, cleans = 0;
+      unsigned tiles = 0, cleans = 0;          // V tiles before the unit's
       bool ok = true;
       for (unsigned unit_no = 0; ok; ++unit_no) {
         const int seg = unit_no % kPtSegs;
@@ -602,11 +602,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const PtShare sh = pt_share<D>(p, u);
         const int n = u.tiles;
         for (int i = max(0, sh.full / KEYS - u.t0); i < n; ++i, ++cleans) {
-          const unsigned at = base + pt_v_pos(i, n), stage = at % STAGES;
+          const unsigned stage = (tiles + i) % VST;
           ok = warp_poll(issued0 + 8 * (cleans % kPtCleans), (cleans / kPtCleans) & 1, p.timeout_ns) &&
-               warp_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns);
+               warp_poll(vfull0 + 8 * stage, (tiles + i) / VST & 1, p.timeout_ns);
           if (!ok) break;
-          uint8_t* v = smem + Shape::QBUF * Shape::QBYTES + stage * Shape::STAGE;
+          uint8_t* v = smem + (v_s - base_s) + stage * Shape::STAGE;
           const int c0 = (u.t0 + i) * KEYS;
           const int from = max(0, sh.full - c0), to = min(KEYS, u.lim - c0);   // masked for some
           bool wrote = false;
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(clean0 + 8 * (cleans % kPtCleans));
         }
-        base += 2 * n;
+        tiles += n;
       }
       if (!ok && lane == 0) atomicOr(&pt_status, kErrPtClean);
       __syncwarp();
@@ -645,7 +645,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       // ---------------------------------------------------------- MMA issue
       const uint32_t leader = elect_one();
       constexpr uint32_t qk_idesc = px_idesc<Tag>(KEYS, false), pv_idesc = px_idesc<Tag>(D, true);
-      unsigned base = 0, fills = 0, cleans = 0, done0 = 0, done1 = 0;
+      // Everything here runs in uniform registers: counters that step and wrap,
+      // no division, no value out of shared memory that the warp has not agreed on.
+      // (With ring positions taken modulo the stages, the code around the products
+      // took longer than they did.)
+      const uint64_t q_desc = smem_desc(qbuf_s, 16, 1024, 2), k_desc = smem_desc(k_s, 16, 1024, 2);
+      const uint64_t v_desc = smem_desc(v_s, KEYS * 128, 1024, 2);
+      int kst = 0, vst = 0;                          // stages, and the parity of their fills
+      uint32_t kpar = 0, vpar = 0;
+      uint32_t ppar0 = 0, ppar1 = 0;                 // of the streams' weights (or S buffers')
+      int fills = 0, cleans = 0, sbuf = 0;           // one stream: the S buffer of the next scores
       // The softmax warps have run through their code once (below).
       bool ok = warp_poll(ofree0, 0, p.timeout_ns) && warp_poll(ofree0 + 8, 0, p.timeout_ns);
       for (unsigned unit_no = 0; ok; ++unit_no) {
@@ -656,53 +665,64 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (lane == 0) mbar_arrive(uempty0 + 8 * seg);
         if (u.ntok == 0) break;
         const PtShare sh = pt_share<D>(p, u);
-        const bool pair = uniform(sh.pair);
+        const int pair = uniform(sh.pair);
         const int n0 = uniform(sh.n0), n1 = uniform(sh.n1), n = uniform(u.tiles);
-        const int first_clean = max(0, uniform(sh.full) / KEYS - uniform(u.t0));
-        auto tile_of = [&](int w, int j) { return NS == 1 || pair ? j : 2 * j + w; };
-        auto s_of = [&](int w, unsigned tile_no) {
-          return tmem + Shape::S_COL * (NS == 2 ? w : tile_no & 1);
+        const int first_clean = uniform(max(0, sh.full / KEYS - u.t0));
+        // Waits of the scores' product, which come before those of the PV that goes
+        // first: each takes its time even when it is over.
+        auto await_k = [&](int w, int j) {
+          const int fill = fills + (pair ? w : 0);
+          if (j == 0)
+            ok = ok && warp_poll(qfull0 + (NS == 2 ? 8 * (fill & 1) : 0),
+                                 (NS == 2 ? fill >> 1 : fill) & 1, p.timeout_ns);
+          if (pair && w && j < n0) return;           // the first stream's, too
+          ok = ok && warp_poll(kfull0 + 8 * kst, kpar, p.timeout_ns);
         };
-        auto qk = [&](int w, int j) {
-          const int i = tile_of(w, j);
-          const unsigned at = base + pt_k_pos(i), stage = at % STAGES;
-          const unsigned fill = fills + (pair ? w : 0), buf = fill % Shape::QBUF;
-          if (j == 0) ok = ok && warp_poll(qfull0 + 8 * buf, (fill / Shape::QBUF) & 1, p.timeout_ns);
-          ok = ok && warp_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns);
+        auto qk = [&](int w, int j, int s_no) {
           if (!ok) return;
+          const int fill = fills + (pair ? w : 0), buf = NS == 2 ? fill & 1 : 0;
           tc_fence_after();
-          const unsigned no = (w ? done1 : done0) + j;
-          const uint64_t a = smem_desc(qbuf_s + buf * Shape::QBYTES, 16, 1024, 2);
-          const uint64_t b = smem_desc(ring_s + stage * Shape::STAGE, 16, 1024, 2);
+          const uint64_t a = q_desc + static_cast<uint64_t>(buf * (Shape::QBYTES >> 4));
+          const uint64_t b = k_desc + static_cast<uint64_t>(kst * (Shape::STAGE >> 4));
+          const uint32_t s_tmem = tmem + Shape::S_COL * s_no;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(leader, s_of(w, no), a + (uint64_t)((kk / 4 * 128 * 128 + kk % 4 * 32) >> 4),
+            mma_ss(leader, s_tmem, a + (uint64_t)((kk / 4 * 128 * 128 + kk % 4 * 32) >> 4),
                    b + (uint64_t)((kk / 4 * KEYS * 128 + kk % 4 * 32) >> 4), qk_idesc, kk > 0);
+          commit_one(leader, sfull0 + 8 * s_no);
           // A pair's second stream is the last to use a stage: it has the more tiles.
-          if (!pair || w == 1) commit_one(leader, empty0 + 8 * stage);
-          if (pair ? j == (w ? n1 : n0) - 1 : i == n - 1) commit_one(leader, qempty0 + 8 * buf);
-          commit_one(leader, sfull0 + 8 * (NS == 2 ? w : no & 1));
-        };
-        auto pv = [&](int w, int j) {
-          const int i = tile_of(w, j);
-          const unsigned at = base + pt_v_pos(i, n), stage = at % STAGES;
-          const unsigned no = (w ? done1 : done0) + j;
-          ok = ok && warp_poll(pfull0 + 8 * (NS == 2 ? w : no & 1), (NS == 2 ? no : no >> 1) & 1,
-                               p.timeout_ns);
-          if (j == 0) ok = ok && warp_poll(ofree0 + 8 * w, unit_no & 1, p.timeout_ns);
-          ok = ok && warp_poll(full0 + 8 * stage, (at / STAGES) & 1, p.timeout_ns);
-          if (i >= first_clean) {
-            const unsigned c = cleans + i - first_clean;
-            ok = ok && warp_poll(clean0 + 8 * (c % kPtCleans), (c / kPtCleans) & 1, p.timeout_ns);
+          if (!pair || w) {
+            commit_one(leader, kempty0 + 8 * kst);
+            if (++kst == KST) kst = 0, kpar ^= 1;
           }
+          if (pair ? j == (w ? n1 : n0) - 1 : (NS == 2 ? 2 * j + w : j) == n - 1)
+            commit_one(leader, qempty0 + 8 * buf);
+        };
+        auto pv = [&](int w, int j, int s_no) {
+          const int i = NS == 1 || pair ? j : 2 * j + w;
+          if (j == 0) ok = ok && warp_poll(ofree0 + 8 * w, unit_no & 1, p.timeout_ns);
+          if (!(pair && w && j < n0)) {
+            ok = ok && warp_poll(vfull0 + 8 * vst, vpar, p.timeout_ns);
+            if (i >= first_clean) {
+              const int c = cleans + i - first_clean;
+              ok = ok && warp_poll(clean0 + 8 * (c % kPtCleans), c / kPtCleans & 1, p.timeout_ns);
+            }
+          }
+          ok = ok && warp_poll(pfull0 + 8 * s_no, s_no ? ppar1 : ppar0, p.timeout_ns);
+          if (s_no) ppar1 ^= 1;
+          else ppar0 ^= 1;
           if (!ok) return;
           tc_fence_after();
-          const uint64_t b = smem_desc(ring_s + stage * Shape::STAGE, KEYS * 128, 1024, 2);
+          const uint64_t b = v_desc + static_cast<uint64_t>(vst * (Shape::STAGE >> 4));
+          const uint32_t p_tmem = tmem + Shape::S_COL * s_no, o_tmem = tmem + Shape::O_COL0 + w * D;
 #pragma unroll
           for (int kk = 0; kk < KEYS / 16; ++kk)
-            mma_ts(leader, tmem + Shape::O_COL0 + w * D, s_of(w, no) + 8 * kk,
-                   b + (uint64_t)(kk * (2048 >> 4)), pv_idesc, j > 0 || kk > 0);
-          if (!pair || w == 1) commit_one(leader, empty0 + 8 * stage);
+            mma_ts(leader, o_tmem, p_tmem + 8 * kk, b + (uint64_t)(kk * (2048 >> 4)), pv_idesc,
+                   j > 0 || kk > 0);
+          if (!pair || w) {
+            commit_one(leader, vempty0 + 8 * vst);
+            if (++vst == VST) vst = 0, vpar ^= 1;
+          }
           if (NS == 1) commit_one(leader, pvdone);
           if (j == (w ? n1 : n0) - 1) commit_one(leader, ofull0 + 8 * w);
         };
@@ -710,26 +730,29 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (n0 == 0) ok = warp_poll(ofree0, unit_no & 1, p.timeout_ns);
         if (NS == 2 && n1 == 0) ok = ok && warp_poll(ofree0 + 8, unit_no & 1, p.timeout_ns);
         if constexpr (NS == 1) {
-          if (n > 0) qk(0, 0);
-          for (int j = 0; j < n && ok; ++j) {
-            if (j + 1 < n) qk(0, j + 1);
-            pv(0, j);
+#pragma unroll 1
+          for (int j = -1; j < n && ok; ++j) {
+            if (j + 1 < n) {
+              await_k(0, j + 1);
+              qk(0, j + 1, sbuf);
+            }
+            if (j >= 0) pv(0, j, sbuf ^ 1);
+            sbuf ^= 1;
           }
+          sbuf ^= 1;   // n scores, n + 1 steps
         } else {
           // The streams in turn: the PV of a tile, then the QK of the next. One
           // site for each product keeps the code small.
 #pragma unroll 1
           for (int t = -2; t < 2 * max(n0, n1) && ok; ++t) {
             const int w = t & 1, j = t >> 1, cnt = w ? n1 : n0;
-            if (j >= 0 && j < cnt) pv(w, j);
-            if (j + 1 < cnt) qk(w, j + 1);
+            if (j + 1 < cnt) await_k(w, j + 1);
+            if (j >= 0 && j < cnt) pv(w, j, w);
+            if (j + 1 < cnt) qk(w, j + 1, w);
           }
         }
-        base += 2 * n;
         fills += n > 0 ? 1 + pair : 0;
         cleans += max(0, n - first_clean);
-        done0 += n0;
-        done1 += n1;
       }
       if (!ok) {
         if (lane == 0) atomicOr(&pt_status, kErrPtMma);
@@ -803,19 +826,16 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             tmem_wait_st();
           }
+          float s[KEYS];
+#pragma unroll
+          for (int c0 = 0; c0 < KEYS; c0 += 32) tmem_ld32(s_addr + c0, s + c0);
+          tmem_wait_ld();
+          hold<KEYS>(s);
           float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-          for (int c0 = 0; c0 < KEYS; c0 += 64) {
-            float s[64];
-            tmem_ld32(s_addr + c0, s);
-            tmem_ld32(s_addr + c0 + 32, s + 32);
-            tmem_wait_ld();
-            hold<64>(s);
 #pragma unroll
-            for (int c = 0; c < 64; c += 8)
+          for (int c = 0; c < KEYS; c += 8)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
-          }
+            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
           const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
           if (j == 0) {
             m = top == -INFINITY ? -1e30f : top;   // nothing finite yet: weights of 0
@@ -845,18 +865,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           }
           const float shift = kOff - m, qscale = p.qscale;
           float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 1
+#pragma unroll
           for (int c0 = 0; c0 < KEYS; c0 += 64) {
-            float s[64];
             uint32_t w16[32];
-            tmem_ld32(s_addr + c0, s);
-            tmem_ld32(s_addr + c0 + 32, s + 32);
-            tmem_wait_ld();
-            hold<64>(s);
 #pragma unroll
             for (int c = 0; c < 64; c += 2) {
               float a, b;
-              fma2(s[c], s[c + 1], qscale, qscale, shift, shift, a, b);
+              fma2(s[c0 + c], s[c0 + c + 1], qscale, qscale, shift, shift, a, b);
               a = ex2(a);
               b = ex2(b);
               add2(sum[c & 2], sum[(c & 2) + 1], a, b);
