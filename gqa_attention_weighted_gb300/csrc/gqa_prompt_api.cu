@@ -146,18 +146,18 @@ int attend(const Call& c, bool tree, long long wait_ns, unsigned withhold_from,
   p.timeout_ns = wait_ns;
   p.withhold_from = withhold_from;
 
-  // Items: query tiles, one more a sequence than its tokens fill. Slots: the plan
-  // cuts work into at most 2 chunks an SM, and an item into one more part than it
-  // has chunks, at least 1.5 (gqa_prompt_kernel.cuh).
+  // Items: query tiles, one more a sequence than its tokens fill. Slots: a chunk is
+  // at least a quarter of an SM's share of the work, so all chunks are at most 4 an
+  // SM, and an item that is cut has more than one and takes less than one more.
   const int ns = c.D == 256 ? 1 : 2;
   const long long items = (c.T + p.TB - 1) / p.TB + std::min(c.B, c.T);
-  const long long slots = std::min(4LL * sms, 2LL * sms + items * c.Hkv);
-  if ((items + 4LL * sms) * c.Hkv > 0x7fffffffLL)
+  const long long slots = std::min(8LL * sms, 4LL * sms + items * c.Hkv);
+  if ((items + 8LL * sms) * c.Hkv > 0x7fffffffLL)
     return ptfail(GQA_AV_ERR_UNSUPPORTED, "T=%d tokens of %d KV heads are too many for one call",
                   c.T, c.Hkv);
   const size_t at_splits = up256(sizeof(PtHeader));
-  const size_t at_units = at_splits + up256(4 * static_cast<size_t>(sms) * sizeof(PtSplit));
-  const size_t at_ml = at_units + up256(static_cast<size_t>(items + 4 * sms) * sizeof(PtUnit));
+  const size_t at_units = at_splits + up256(8 * static_cast<size_t>(sms) * sizeof(PtSplit));
+  const size_t at_ml = at_units + up256(static_cast<size_t>(items + 8 * sms) * sizeof(PtUnit));
   const size_t at_o = at_ml + static_cast<size_t>(slots) * ns * 128 * 8;
   bool capturing = false;
   Workspace* ws = nullptr;

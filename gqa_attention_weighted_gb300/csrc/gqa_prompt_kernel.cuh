@@ -10,9 +10,8 @@
 //
 // Items and units. An item is one query tile or a pair of them; it needs the
 // key tiles up to its last visible row. Long items are cut along the keys into
-// units of at most 1.5 chunks, where the chunk is half of what an SM gets if all
-// work is spread evenly; other items are one unit each and write their output
-// themselves. Units are handed out heaviest first, each for every KV head. The
+// units of at most a chunk where that evens the SMs out; other items are one unit
+// each and write their output themselves. Units are handed out heaviest first, each for every KV head. The
 // lengths live on the device, so the first CTA to arrive makes the list while
 // the others set up; who was first shows in a ticket, so no CTA waits for one
 // that has not started. Where an item was cut, its units write their
@@ -74,6 +73,13 @@ constexpr int kPtSegs = 2;             // unit descriptors in flight
 constexpr int kPtCleans = 16;          // barriers of cleared V tiles; more than stages
 constexpr int kPtBuckets = 256;        // of unit costs
 constexpr int kPtMinChunk = 4;         // key tiles
+constexpr int kPtCosts = 16384;        // items whose costs the plan keeps
+// Chunks that the plan tries: 1.1 of an SM's share times 2^(-0.0929 i), i < 24, so
+// down to a quarter of it. In key tiles (0.75 us): a unit's start and end; 8 rows
+// of a partial result, written and read; the step that joins them.
+constexpr float kPtTopChunk = 1.1f, kPtChunkStep = 0.0929f;
+constexpr float kPtUnitCost = 3.0f, kPtRowCost = 0.14f, kPtJoinCost = 4.0f;
+constexpr int kPtDeep = 4096;          // mean rows that make a batch deep
 constexpr float kPtGrow = 8.0f;        // log2 of the growth of a maximum that is tolerated
 constexpr unsigned kErrPtPlan = 8u, kErrPtLoad = 16u, kErrPtMma = 32u, kErrPtSoftmax = 64u,
                    kErrPtClean = 128u;
@@ -242,11 +248,15 @@ __device__ __noinline__ void pt_plan(const PromptParams& p, int* mem) {
   int* part = offs + kPtBuckets;       // [12]
   unsigned long long* work = reinterpret_cast<unsigned long long*>(
       (reinterpret_cast<uintptr_t>(part + kPtThreads / 32) + 7) & ~static_cast<uintptr_t>(7));
-  int* most = reinterpret_cast<int*>(work + 1);
+  unsigned long long* best = work + 1;   // estimate and chunk
+  int* most = reinterpret_cast<int*>(work + 3);   // work[2]: tokens times rows
   int* n_slots = most + 1;
   int* n_splits = most + 2;
+  int* costs = most + 3;               // [kPtCosts] of the first items
   if (tid == 0) {
     *work = 0;
+    *best = ~0ull;
+    work[2] = 0;
     *most = *n_slots = *n_splits = 0;
   }
   for (int i = tid; i < kPtBuckets; i += kPtThreads) offs[i] = 0;
@@ -261,23 +271,30 @@ __device__ __noinline__ void pt_plan(const PromptParams& p, int* mem) {
     if (b <= p.B) tok[b] = s;
   }
   __syncthreads();
-  // Pairs where that leaves an SM two units at least; a tree's rows are few and
-  // its keys many, so it always pairs.
-  const int qt = (tok[p.B] - tok[0]) / p.TB;
-  const int pairs = Shape::NS == 2 &&
-                    (p.tree_mask || static_cast<long long>(qt) * p.Hkv >= 4 * gridDim.x);
+  unsigned long long sum = 0;
+  for (int b = tid; b < p.B; b += kPtThreads) {
+    const int n = tok[b + 1] - tok[b];
+    const int c0 = p.cached_lens ? min(max(p.cached_lens[b], 0), cap) : 0;
+    cached[b] = c0;
+    len[b] = p.seq_lens ? min(max(p.seq_lens[b], 0), cap) : min(c0 + n, cap);
+    sum += static_cast<unsigned long long>(n) * len[b];
+  }
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((tid & 31) == 0) atomicAdd(work + 2, sum);
+  __syncthreads();
+  // Pairs, which read a key once for twice the rows, where that leaves an SM two
+  // items at least, or where there are few items because the keys are many: those
+  // are cut in any case (512 tokens behind 16384 rows, 32 + 8 heads of 128: 140 us,
+  // single query tiles 158; 2048 tokens alone, pairs 74 us and single ones 58).
+  const int tokens = tok[p.B] - tok[0];
+  const bool many = static_cast<long long>(tokens / p.TB) * p.Hkv >= 4 * gridDim.x;
+  const bool deep = work[2] >= static_cast<unsigned long long>(tokens) * kPtDeep;
+  const int pairs = Shape::NS == 2 && (many || deep);
   const int TI = p.TB << pairs;
   carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPtThreads) {
     const int b = b0 + tid;
-    int n = 0;
-    if (b < p.B) {
-      n = tok[b + 1] - tok[b];
-      const int c0 = p.cached_lens ? min(max(p.cached_lens[b], 0), cap) : 0;
-      cached[b] = c0;
-      len[b] = p.seq_lens ? min(max(p.seq_lens[b], 0), cap) : min(c0 + n, cap);
-    }
-    const int items = (n + TI - 1) / TI;
+    const int items = b < p.B ? (tok[b + 1] - tok[b] + TI - 1) / TI : 0;
     const int upto = pt_scan<false>(items, &carry, part);
     if (b < p.B) item[b] = upto - items;
   }
@@ -304,11 +321,14 @@ __device__ __noinline__ void pt_plan(const PromptParams& p, int* mem) {
     return u.tiles << (u.ntok > p.TB);
   };
   // Work, in key tiles times query tiles.
-  unsigned long long sum = 0;
+  sum = 0;
   int top = 0;
   PtUnit u;
+  // A cost and the item's rows, in eights.
+  auto pack = [&](int c) { return c | (u.ntok * p.G + 7) / 8 << 24; };
   for (int i = tid; i < n_items; i += kPtThreads) {
     const int c = find(i, u);
+    if (i < kPtCosts) costs[i] = pack(c);
     sum += c;
     top = max(top, c);
   }
@@ -319,21 +339,64 @@ __device__ __noinline__ void pt_plan(const PromptParams& p, int* mem) {
     atomicMax(most, top);
   }
   __syncthreads();
-  // At most 2 CTAs' worth of chunks in all, and an item that is cut has more than
-  // 1.5 chunks: s <= cost / chunk + 1 slots each are at most 2 + 2 / 1.5 an SM, and
-  // one more an item than 2 an SM.
-  const unsigned long long fair = *work * p.Hkv / (2 * gridDim.x) + 1;
-  const int chunk = max(kPtMinChunk, static_cast<int>(min(fair, 1ull << 28)));
-  const int whole = chunk + chunk / 2;
-  const int max_unit = max(1, min(*most, whole));
-  auto cuts = [&](int c) { return c > whole ? (c + chunk - 1) / chunk : 1; };
+  auto packed = [&](int i) { return i < kPtCosts ? costs[i] : pack(find(i, u)); };
+  auto cost = [&](int i) { return packed(i) & 0xffffff; };
+  top = *most;
+  const float fair = static_cast<float>(*work) * static_cast<float>(p.Hkv) /
+                     static_cast<float>(gridDim.x);   // of an SM
+  // How to cut: not at all where items are small beside what an SM gets; else each
+  // warp tries two chunks, from 1.1 of the fair share down to a quarter of it, and
+  // the one with the smallest estimate is taken. Units above half a chunk come in
+  // rounds, the SMs with the most of them take as many of mean size, and smaller
+  // units fill the others up to the fair share; then a unit's start and end, and
+  // the partial results' way to memory and back.
+  // (Chunks of half the share whatever the items: 9 sequences of up to 32768 rows,
+  // 16 + 1 heads of 256, had SMs with 117 tiles where the mean is 84.)
+  int chunk = max(top, 1);
+  if (top > kPtMinChunk && 4.0f * static_cast<float>(top) > fair) {
+    for (int k = 0; k < 2; ++k) {
+      const int no = 2 * (tid >> 5) + k;
+      const int c = min(max(static_cast<int>(fair * kPtTopChunk * exp2f(-kPtChunkStep * no)) + 1,
+                            kPtMinChunk), top);
+      int units = 0, large = 0, big = 0, rows = 0;
+      float load = 0.0f;
+      for (int i = tid & 31; i < n_items; i += 32) {
+        const int both = packed(i), x = both & 0xffffff, s = max(1, (x + c - 1) / c), each = (x + s - 1) / s;
+        units += s;
+        rows += s > 1 ? s * (both >> 24) : 0;
+        big = max(big, each);
+        if (2 * each > c) {
+          large += s;
+          load += static_cast<float>(x);
+        }
+      }
+      units = __reduce_add_sync(0xffffffffu, units);
+      large = __reduce_add_sync(0xffffffffu, large);
+      big = __reduce_max_sync(0xffffffffu, big);
+      for (int o = 16; o; o >>= 1) load += __shfl_xor_sync(0xffffffffu, load, o);
+      const float sms = static_cast<float>(gridDim.x), heads = static_cast<float>(p.Hkv);
+      const float rounds = ceilf(static_cast<float>(large) * heads / sms);
+      const float most = fmaxf(rounds * load / static_cast<float>(max(large, 1)), static_cast<float>(big));
+      rows = __reduce_add_sync(0xffffffffu, rows);
+      const float est = fmaxf(most, fair) + (rows ? kPtJoinCost : 0.0f) +
+                        (kPtUnitCost * static_cast<float>(units) + kPtRowCost * static_cast<float>(rows)) *
+                            heads / sms;
+      if ((tid & 31) == 0)
+        atomicMin(best, static_cast<unsigned long long>(__float_as_uint(est)) << 32 |
+                            static_cast<unsigned>(c));
+    }
+    __syncthreads();
+    chunk = static_cast<int>(*best & 0xffffffffu);
+  }
+  const int max_unit = max(1, min(top, chunk));
+  auto cuts = [&](int c) { return max(1, (c + chunk - 1) / chunk); };
   auto bucket = [&](int c, int s) {     // heaviest first
     const int each = (c + s - 1) / s;
     return kPtBuckets - 1 -
            static_cast<int>(static_cast<long long>(min(each, max_unit)) * (kPtBuckets - 1) / max_unit);
   };
   for (int i = tid; i < n_items; i += kPtThreads) {
-    const int c = find(i, u), s = cuts(c);
+    const int c = cost(i), s = cuts(c);
     atomicAdd(&offs[bucket(c, s)], s);
   }
   __syncthreads();
@@ -345,8 +408,8 @@ __device__ __noinline__ void pt_plan(const PromptParams& p, int* mem) {
   }
   __syncthreads();
   for (int i = tid; i < n_items; i += kPtThreads) {
-    const int c = find(i, u), s = cuts(c);   // at most the tiles
-    const int at = atomicAdd(&offs[bucket(c, s)], s);
+    const int s = cuts(find(i, u));   // at most the tiles
+    const int at = atomicAdd(&offs[bucket(cost(i), s)], s);
     if (s > 1) {
       u.slot = atomicAdd(n_slots, s);
       p.splits[atomicAdd(n_splits, 1)] = {u.tok, u.ntok, u.slot, s};
@@ -414,7 +477,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   float2* ml = reinterpret_cast<float2*>(smem + Shape::TILES_BYTES + Shape::MISC);   // [2][128]
   static_assert(8 * (kBars + 1) + sizeof(Seg) * kPtSegs + 24 <= Shape::MISC,
                 "shared memory besides the tiles");
-  static_assert(kPtCleans > VST && 16 * (kPtMaxB + 1) + 4 * kPtBuckets + 128 <= Shape::TILES_BYTES,
+  static_assert(kPtCleans > VST && 16 * (kPtMaxB + 1) + 4 * (kPtBuckets + kPtCosts) + 128 <= Shape::TILES_BYTES,
                 "barriers of cleared tiles; the plan's memory");
 
   if (warp == kPtMmaWarp) {

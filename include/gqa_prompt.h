@@ -58,7 +58,7 @@
  * waits for the calls under way on the stream; nothing else synchronises). Calls
  * on different streams and replays of different graphs may overlap; two
  * executable copies of one captured graph must not. A capture's workspace is
- * kept until gqa_prompt_release_graph_workspaces. Its size: up to 4 * SMs slots
+ * kept until gqa_prompt_release_graph_workspaces. Its size: up to 8 * SMs slots
  * of 128 * (D + 2) floats (twice that for D below 256) for rows whose keys were
  * cut, and 32 bytes an item of 128 / G tokens. Errors: a status code from
  * gqa_av.h; on error nothing is launched and gqa_prompt_last_error() holds a
