@@ -151,6 +151,7 @@ int attend(const Call& c, bool tree, long long wait_ns, unsigned withhold_from,
   // SM, and an item that is cut has more than one and takes less than one more.
   const int ns = c.D == 256 ? 1 : 2;
   const long long items = (c.T + p.TB - 1) / p.TB + std::min(c.B, c.T);
+  p.small = c.B <= kPtSmall && items <= kPtSmall;
   const long long slots = std::min(8LL * sms, 4LL * sms + items * c.Hkv);
   if ((items + 8LL * sms) * c.Hkv > 0x7fffffffLL)
     return ptfail(GQA_AV_ERR_UNSUPPORTED, "T=%d tokens of %d KV heads are too many for one call",

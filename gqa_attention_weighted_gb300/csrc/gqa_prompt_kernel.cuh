@@ -70,7 +70,8 @@ constexpr int kPtSoftmaxRegs = 208, kPtAuxRegs = 88;
 constexpr int kPtMmaWarp = 8, kPtKWarp = 9, kPtVWarp = 10, kPtCleanWarp = 11;
 constexpr int kPtMaxB = 8192;          // 16 bytes of the plan's shared memory each
 constexpr int kPtSegs = 2;             // unit descriptors in flight
-constexpr int kPtCleans = 16;          // barriers of cleared V tiles; more than stages
+constexpr int kPtCleans = 8;           // barriers of cleared V tiles; more than stages
+constexpr int kPtSmall = 32;           // sequences and items of a small batch: a lane each
 constexpr int kPtBuckets = 256;        // of unit costs
 constexpr int kPtMinChunk = 4;         // key tiles
 constexpr int kPtCosts = 16384;        // items whose costs the plan keeps
@@ -118,14 +119,14 @@ struct alignas(16) PtUnit {
   int t0, tiles;
   int slot;           // of the partial result, or -1: the unit is a whole item
 };
-struct PtSplit {      // an item that was cut
+struct alignas(16) PtSplit {   // an item that was cut
   int tok, ntok, slot, splits;
 };
 // Zeroed when the workspace is made, and by the last CTA of each call.
 struct PtHeader {
   unsigned ticket, ready, next, done, left;
   int units;                      // times KV heads
-  int splits;                     // items that were cut
+  int splits, parts;              // items that were cut, and their slots
 };
 
 struct alignas(64) PromptParams {
@@ -146,7 +147,7 @@ struct alignas(64) PromptParams {
   int R;                          // rows of a K or V box: gcd(bs, KEYS)
   float qscale;                   // |scale| * log2(e)
   int negate;                     // scale < 0
-  int slots;                      // bound on the slots, times KV heads
+  int small;                      // at most kPtSmall sequences and items: no list of units
   long long timeout_ns;
   unsigned withhold_from;         // self-test: query loads from this one of a CTA on are not issued
 };
@@ -234,6 +235,195 @@ __device__ __forceinline__ int pt_scan(int x, int* carry, int* part) {
   return pt_join<MAX>(x, before);
 }
 
+// Pairs of query tiles, which read a key once for twice the rows, where that
+// leaves an SM two items at least, or where there are few items because the keys
+// are many: those are cut in any case (512 tokens behind 16384 rows, 32 + 8 heads of
+// 128: 140 us, single query tiles 158; 2048 tokens alone, pairs 74 us and single
+// ones 58). `rows` is the sum of the tokens' sequences' rows.
+template <int D>
+__device__ __forceinline__ bool pt_pairs(const PromptParams& p, int tokens, float rows) {
+  const bool many = static_cast<long long>(tokens / p.TB) * p.Hkv >= 4 * gridDim.x;
+  return PtShape<D>::NS == 2 && (many || rows >= static_cast<float>(tokens) * kPtDeep);
+}
+// Whether anything is cut: not where items are small beside what an SM gets.
+__device__ __forceinline__ bool pt_worth(int top, float fair) {
+  return top > kPtMinChunk && 4.0f * static_cast<float>(top) > fair;
+}
+// How to cut: chunks are tried from 1.1 of the fair share down to a quarter of it,
+// and the one with the smallest estimate is taken. Units above half a chunk come
+// in rounds, the SMs with the most of them take as many of mean size, and smaller
+// units fill the others up to the fair share; then a unit's start and end, and the
+// partial results' way to memory and back. (Chunks of half the share whatever the
+// items: 9 sequences of up to 32768 rows, 16 + 1 heads of 256, had SMs with 117
+// tiles where the mean is 84.)
+__device__ __forceinline__ int pt_chunk(int no, float fair, int top) {
+  return min(max(static_cast<int>(fair * kPtTopChunk * exp2f(-kPtChunkStep * no)) + 1, kPtMinChunk), top);
+}
+// ceil(x / c), at least 1.
+__device__ __forceinline__ int pt_cuts(int x, int c) {
+  int s = __float2int_rz(__fdividef(static_cast<float>(x), static_cast<float>(c)));
+  s += static_cast<long long>(s) * c < x;      // the quotient is off by 1 at most
+  s -= s > 0 && static_cast<long long>(s - 1) * c >= x;
+  return max(s, 1);
+}
+struct PtTry {
+  int units = 0, large = 0, big = 0, rows = 0;
+  float load = 0.0f;
+  __device__ __forceinline__ void add(int packed, int c) {
+    const int x = packed & 0xffffff, s = pt_cuts(x, c);
+    const float each = __fdividef(static_cast<float>(x), static_cast<float>(s));
+    units += s;
+    rows += s > 1 ? s * (packed >> 24) : 0;
+    big = max(big, __float2int_ru(each));
+    if (2.0f * each > static_cast<float>(c)) {
+      large += s;
+      load += static_cast<float>(x);
+    }
+  }
+  __device__ __forceinline__ float estimate(float fair, int hkv) const {
+    const float sms = static_cast<float>(gridDim.x), per = static_cast<float>(hkv) / sms;
+    const float rounds = ceilf(static_cast<float>(large) * per - 1e-4f);
+    const float most = fmaxf(__fdividef(rounds * load, static_cast<float>(max(large, 1))),
+                             static_cast<float>(big));
+    return fmaxf(most, fair) + (rows ? kPtJoinCost : 0.0f) +
+           (kPtUnitCost * static_cast<float>(units) + kPtRowCost * static_cast<float>(rows)) * per;
+  }
+};
+// Item k of a sequence: tokens tok .. tok + n - 1 behind c0 rows, len rows in all.
+template <int D>
+__device__ __forceinline__ int pt_item(const PromptParams& p, int b, int k, int TI, int tok, int n,
+                                       int c0, int len, PtUnit& u) {   // its cost
+  u.b = b;
+  u.tok = tok + k * TI;
+  u.ntok = min(TI, n - k * TI);
+  u.base = p.tree_mask ? c0 : c0 + k * TI;
+  u.lim = min(p.tree_mask ? c0 + n : u.base + u.ntok, len);
+  u.t0 = 0;
+  u.tiles = (u.lim + PtShape<D>::KEYS - 1) / PtShape<D>::KEYS;
+  u.slot = -1;
+  return u.tiles << (u.ntok > p.TB);
+}
+// A cost and the item's rows, in eights.
+__device__ __forceinline__ int pt_pack(const PromptParams& p, const PtUnit& u, int cost) {
+  return cost | (u.ntok * p.G + 7) / 8 << 24;
+}
+
+// The plan of a small batch, by the K warp of every CTA for itself: a lane holds a
+// sequence, then an item, heaviest first. Its code runs once a call and is fetched
+// cold, so it is kept short; what it saves is the way of the plan from one CTA to
+// the others (61 tokens alone, 8 + 2 heads of 64: see below).
+template <int D>
+struct PtSmallPlan {
+  PtUnit u;             // this lane's item
+  int cuts, upto;       // its units, and all up to it
+  int units, splits, parts;
+
+  __device__ __forceinline__ void make(const PromptParams& p) {
+    const int lane = threadIdx.x & 31;
+    const int cap = p.max_blocks * p.bs;
+    int tok = 0, end = 0, c0 = 0, len = 0;
+    if (lane < p.B) {
+      tok = min(max(p.token_start[lane], 0), p.T);
+      end = min(max(p.token_start[lane + 1], 0), p.T);
+      c0 = p.cached_lens ? p.cached_lens[lane] : 0;
+      len = p.seq_lens ? p.seq_lens[lane] : 0;
+    }
+    if (p.B > 1) {   // starts not below their predecessors
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, tok, o);
+        if (lane >= o) tok = max(tok, y);
+      }
+    }
+    end = max(end, tok);
+    const int n = lane < p.B ? end - tok : 0;
+    c0 = min(max(c0, 0), cap);
+    len = min(max(p.seq_lens ? len : c0 + n, 0), cap);
+    const int tokens = __reduce_add_sync(0xffffffffu, n);
+    float rows = static_cast<float>(n) * static_cast<float>(len);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) rows += __shfl_xor_sync(0xffffffffu, rows, o);
+    const int TI = p.TB << pt_pairs<D>(p, tokens, rows);
+    const int items = (n + TI - 1) / TI;
+    const int incl = warp_incl_sum(items), total = __shfl_sync(0xffffffffu, incl, 31);
+    int b = 0;
+#pragma unroll 1
+    for (int i = 0; i < p.B; ++i) b += __shfl_sync(0xffffffffu, incl, i) <= lane;
+    const int from = b & 31, k = lane - (__shfl_sync(0xffffffffu, incl, from) - __shfl_sync(0xffffffffu, items, from));
+    tok = __shfl_sync(0xffffffffu, tok, from);
+    const int nb = __shfl_sync(0xffffffffu, n, from);
+    c0 = __shfl_sync(0xffffffffu, c0, from);
+    len = __shfl_sync(0xffffffffu, len, from);
+    u.ntok = u.tiles = 0;
+    int cost = 0;
+    if (lane < total) cost = pt_item<D>(p, b, k, TI, tok, nb, c0, len, u);
+    const int top = __reduce_max_sync(0xffffffffu, cost);
+    const float fair = static_cast<float>(__reduce_add_sync(0xffffffffu, cost)) *
+                       static_cast<float>(p.Hkv) / static_cast<float>(gridDim.x);
+    int chunk = max(top, 1);
+    if (pt_worth(top, fair)) {
+      const int mine = pt_pack(p, u, cost), c = pt_chunk(min(lane, 23), fair, top);
+      PtTry x;
+#pragma unroll 1
+      for (int i = 0; i < total; ++i) x.add(__shfl_sync(0xffffffffu, mine, i), c);
+      // Estimates are positive, so their bit patterns are ordered like them.
+      const unsigned est = __float_as_uint(x.estimate(fair, p.Hkv));
+      const unsigned best = __reduce_min_sync(0xffffffffu, est);
+      chunk = __shfl_sync(0xffffffffu, c, __ffs(__ballot_sync(0xffffffffu, est == best)) - 1);
+    }
+    cuts = lane < total ? pt_cuts(cost, chunk) : 0;
+    if (total > 1) {   // heaviest units first: lane r takes the item of rank r
+      const int each = lane < total ? cost / cuts : -1;
+      int rank = 0, src = 0;
+#pragma unroll 1
+      for (int i = 0; i < 32; ++i) {
+        const int y = __shfl_sync(0xffffffffu, each, i);
+        rank += y > each || (y == each && i < lane);
+      }
+#pragma unroll 1
+      for (int i = 0; i < 32; ++i) src = __shfl_sync(0xffffffffu, rank, i) == lane ? i : src;
+      u.b = __shfl_sync(0xffffffffu, u.b, src);
+      u.tok = __shfl_sync(0xffffffffu, u.tok, src);
+      u.ntok = __shfl_sync(0xffffffffu, u.ntok, src);
+      u.base = __shfl_sync(0xffffffffu, u.base, src);
+      u.lim = __shfl_sync(0xffffffffu, u.lim, src);
+      u.tiles = __shfl_sync(0xffffffffu, u.tiles, src);
+      cuts = __shfl_sync(0xffffffffu, cuts, src);
+    }
+    upto = warp_incl_sum(cuts);
+    units = __shfl_sync(0xffffffffu, upto, 31) * p.Hkv;
+    const int cut = cuts > 1 ? cuts : 0, slots = warp_incl_sum(cut);
+    u.slot = slots - cut;
+    parts = __shfl_sync(0xffffffffu, slots, 31);
+  }
+  // For the joining warps: the items that were cut.
+  __device__ __forceinline__ void publish(PtSplit* list, int* count) {
+    const int lane = threadIdx.x & 31;
+    const unsigned cut = __ballot_sync(0xffffffffu, cuts > 1);
+    if (cuts > 1) list[__popc(cut & ((1u << lane) - 1u))] = {u.tok, u.ntok, u.slot, cuts};
+    if (lane == 0) {
+      count[0] = __popc(cut);
+      count[1] = parts;
+    }
+  }
+  // Unit rec (heads aside): words lane 0-7 of its record in each lane's return value.
+  __device__ __forceinline__ int word(int rec) const {
+    const int lane = threadIdx.x & 31;
+    const int i = __ffs(__ballot_sync(0xffffffffu, rec < upto) | 0x80000000u) - 1;
+    const int s = __shfl_sync(0xffffffffu, cuts, i);
+    const int k = rec - (__shfl_sync(0xffffffffu, upto, i) - s);
+    const int tiles = __shfl_sync(0xffffffffu, u.tiles, i), each = tiles / max(s, 1);
+    const int more = tiles - each * s;
+    const int slot = __shfl_sync(0xffffffffu, u.slot, i);
+    int w = __shfl_sync(0xffffffffu, u.b, i);
+    const int tok = __shfl_sync(0xffffffffu, u.tok, i), ntok = __shfl_sync(0xffffffffu, u.ntok, i);
+    const int base = __shfl_sync(0xffffffffu, u.base, i), lim = __shfl_sync(0xffffffffu, u.lim, i);
+    w = lane == 1 ? tok : lane == 2 ? ntok : lane == 3 ? base : lane == 4 ? lim : w;
+    w = lane == 5 ? k * each + min(k, more) : lane == 6 ? each + (k < more) : w;
+    return lane == 7 ? (s > 1 ? slot + k : -1) : w;
+  }
+};
+
 // Made by all threads of one CTA from the lengths, in the shared memory of the
 // tiles (`mem`), which nothing uses yet.
 template <int D>
@@ -282,14 +472,7 @@ __device__ __noinline__ void pt_plan(const PromptParams& p, int* mem) {
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if ((tid & 31) == 0) atomicAdd(work + 2, sum);
   __syncthreads();
-  // Pairs, which read a key once for twice the rows, where that leaves an SM two
-  // items at least, or where there are few items because the keys are many: those
-  // are cut in any case (512 tokens behind 16384 rows, 32 + 8 heads of 128: 140 us,
-  // single query tiles 158; 2048 tokens alone, pairs 74 us and single ones 58).
-  const int tokens = tok[p.B] - tok[0];
-  const bool many = static_cast<long long>(tokens / p.TB) * p.Hkv >= 4 * gridDim.x;
-  const bool deep = work[2] >= static_cast<unsigned long long>(tokens) * kPtDeep;
-  const int pairs = Shape::NS == 2 && (many || deep);
+  const int pairs = pt_pairs<D>(p, tok[p.B] - tok[0], static_cast<float>(work[2]));
   const int TI = p.TB << pairs;
   carry = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPtThreads) {
@@ -310,25 +493,15 @@ __device__ __noinline__ void pt_plan(const PromptParams& p, int* mem) {
       else hi = mid;
     }
     const int k = i - item[lo];
-    u.b = lo;
-    u.tok = tok[lo] + k * TI;
-    u.ntok = min(TI, tok[lo + 1] - u.tok);
-    u.base = p.tree_mask ? cached[lo] : cached[lo] + k * TI;
-    u.lim = min(p.tree_mask ? u.base + (tok[lo + 1] - tok[lo]) : u.base + u.ntok, len[lo]);
-    u.t0 = 0;
-    u.tiles = (u.lim + Shape::KEYS - 1) / Shape::KEYS;
-    u.slot = -1;
-    return u.tiles << (u.ntok > p.TB);
+    return pt_item<D>(p, lo, k, TI, tok[lo], tok[lo + 1] - tok[lo], cached[lo], len[lo], u);
   };
   // Work, in key tiles times query tiles.
   sum = 0;
   int top = 0;
   PtUnit u;
-  // A cost and the item's rows, in eights.
-  auto pack = [&](int c) { return c | (u.ntok * p.G + 7) / 8 << 24; };
   for (int i = tid; i < n_items; i += kPtThreads) {
     const int c = find(i, u);
-    if (i < kPtCosts) costs[i] = pack(c);
+    if (i < kPtCosts) costs[i] = pt_pack(p, u, c);
     sum += c;
     top = max(top, c);
   }
@@ -339,57 +512,36 @@ __device__ __noinline__ void pt_plan(const PromptParams& p, int* mem) {
     atomicMax(most, top);
   }
   __syncthreads();
-  auto packed = [&](int i) { return i < kPtCosts ? costs[i] : pack(find(i, u)); };
+  auto packed = [&](int i) {
+    if (i < kPtCosts) return costs[i];
+    const int c = find(i, u);
+    return pt_pack(p, u, c);
+  };
   auto cost = [&](int i) { return packed(i) & 0xffffff; };
   top = *most;
   const float fair = static_cast<float>(*work) * static_cast<float>(p.Hkv) /
                      static_cast<float>(gridDim.x);   // of an SM
-  // How to cut: not at all where items are small beside what an SM gets; else each
-  // warp tries two chunks, from 1.1 of the fair share down to a quarter of it, and
-  // the one with the smallest estimate is taken. Units above half a chunk come in
-  // rounds, the SMs with the most of them take as many of mean size, and smaller
-  // units fill the others up to the fair share; then a unit's start and end, and
-  // the partial results' way to memory and back.
-  // (Chunks of half the share whatever the items: 9 sequences of up to 32768 rows,
-  // 16 + 1 heads of 256, had SMs with 117 tiles where the mean is 84.)
   int chunk = max(top, 1);
-  if (top > kPtMinChunk && 4.0f * static_cast<float>(top) > fair) {
-    for (int k = 0; k < 2; ++k) {
-      const int no = 2 * (tid >> 5) + k;
-      const int c = min(max(static_cast<int>(fair * kPtTopChunk * exp2f(-kPtChunkStep * no)) + 1,
-                            kPtMinChunk), top);
-      int units = 0, large = 0, big = 0, rows = 0;
-      float load = 0.0f;
-      for (int i = tid & 31; i < n_items; i += 32) {
-        const int both = packed(i), x = both & 0xffffff, s = max(1, (x + c - 1) / c), each = (x + s - 1) / s;
-        units += s;
-        rows += s > 1 ? s * (both >> 24) : 0;
-        big = max(big, each);
-        if (2 * each > c) {
-          large += s;
-          load += static_cast<float>(x);
-        }
-      }
-      units = __reduce_add_sync(0xffffffffu, units);
-      large = __reduce_add_sync(0xffffffffu, large);
-      big = __reduce_max_sync(0xffffffffu, big);
-      for (int o = 16; o; o >>= 1) load += __shfl_xor_sync(0xffffffffu, load, o);
-      const float sms = static_cast<float>(gridDim.x), heads = static_cast<float>(p.Hkv);
-      const float rounds = ceilf(static_cast<float>(large) * heads / sms);
-      const float most = fmaxf(rounds * load / static_cast<float>(max(large, 1)), static_cast<float>(big));
-      rows = __reduce_add_sync(0xffffffffu, rows);
-      const float est = fmaxf(most, fair) + (rows ? kPtJoinCost : 0.0f) +
-                        (kPtUnitCost * static_cast<float>(units) + kPtRowCost * static_cast<float>(rows)) *
-                            heads / sms;
+  if (pt_worth(top, fair)) {
+    for (int k = 0; k < 2; ++k) {   // two chunks a warp
+      const int c = pt_chunk(2 * (tid >> 5) + k, fair, top);
+      PtTry x;
+      for (int i = tid & 31; i < n_items; i += 32) x.add(packed(i), c);
+      x.units = __reduce_add_sync(0xffffffffu, x.units);
+      x.large = __reduce_add_sync(0xffffffffu, x.large);
+      x.big = __reduce_max_sync(0xffffffffu, x.big);
+      x.rows = __reduce_add_sync(0xffffffffu, x.rows);
+      for (int o = 16; o; o >>= 1) x.load += __shfl_xor_sync(0xffffffffu, x.load, o);
+      // Estimates are positive, so their bit patterns are ordered like them.
       if ((tid & 31) == 0)
-        atomicMin(best, static_cast<unsigned long long>(__float_as_uint(est)) << 32 |
+        atomicMin(best, static_cast<unsigned long long>(__float_as_uint(x.estimate(fair, p.Hkv))) << 32 |
                             static_cast<unsigned>(c));
     }
     __syncthreads();
     chunk = static_cast<int>(*best & 0xffffffffu);
   }
   const int max_unit = max(1, min(top, chunk));
-  auto cuts = [&](int c) { return max(1, (c + chunk - 1) / chunk); };
+  auto cuts = [&](int c) { return pt_cuts(c, chunk); };
   auto bucket = [&](int c, int s) {     // heaviest first
     const int each = (c + s - 1) / s;
     return kPtBuckets - 1 -
@@ -426,6 +578,7 @@ __device__ __noinline__ void pt_plan(const PromptParams& p, int* mem) {
   if (tid == 0) {
     p.head->units = carry * p.Hkv;
     p.head->splits = *n_splits;
+    p.head->parts = *n_slots;
   }
 }
 
@@ -471,12 +624,18 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     int kv;
   };
   Seg* segs = reinterpret_cast<Seg*>(bars + ((kBars + 1) & ~1));
-  int* odd = reinterpret_cast<int*>(segs + kPtSegs);   // [4] unit's V held values that are not finite
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(odd + 4);
+  // Read 16 bytes at a time: behind records of multiples of 16.
+  PtSplit* cut_list = reinterpret_cast<PtSplit*>(segs + kPtSegs);   // [kPtSmall] of a small batch
+  int* odd = reinterpret_cast<int*>(cut_list + kPtSmall);   // [4] unit's V held values that are not finite
+  int* cut_count = odd + 4;            // items of cut_list, and their slots
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(cut_count + 2);
   unsigned* ticket = tmem_slot + 1;
   float2* ml = reinterpret_cast<float2*>(smem + Shape::TILES_BYTES + Shape::MISC);   // [2][128]
-  static_assert(8 * (kBars + 1) + sizeof(Seg) * kPtSegs + 24 <= Shape::MISC,
+  static_assert(8 * ((kBars + 1) & ~1) + sizeof(Seg) * kPtSegs + 32 + sizeof(PtSplit) * kPtSmall <= Shape::MISC,
                 "shared memory besides the tiles");
+  static_assert(Shape::TILES_BYTES % 16 == 0 && sizeof(Seg) % 16 == 0 && sizeof(PtSplit) == 16 &&
+                    alignof(PtSplit) == 16,
+                "16-byte records");
   static_assert(kPtCleans > VST && 16 * (kPtMaxB + 1) + 4 * (kPtBuckets + kPtCosts) + 128 <= Shape::TILES_BYTES,
                 "barriers of cleared tiles; the plan's memory");
 
@@ -513,7 +672,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
-  if (threadIdx.x == 0) *ticket = atomicAdd(&p.head->ticket, 1u);
+  if (threadIdx.x == 0) *ticket = p.small ? 1u : atomicAdd(&p.head->ticket, 1u);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -551,7 +710,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       unsigned held = 0;
       bool ok = true;
       int next = blockIdx.x, total = 0;
-      if (is_k) {
+      PtSmallPlan<D> plan;
+      if (is_k && p.small) {
+        plan.make(p);
+        plan.publish(cut_list, cut_count);
+        total = plan.units;
+      } else if (is_k) {
         // The plan is ready when its maker says so.
         const uint64_t since = global_timer_ns();
         while (ok && !*reinterpret_cast<volatile unsigned*>(&p.head->ready))
@@ -568,7 +732,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           // The record by eight lanes; heads are innermost.
           const int rec = next / p.Hkv;
           int word = 0;
-          if (next < total && lane < 8) word = __ldcg(reinterpret_cast<const int*>(p.units + rec) + lane);
+          if (p.small) word = next < total ? plan.word(rec) : 0;
+          else if (next < total && lane < 8) word = __ldcg(reinterpret_cast<const int*>(p.units + rec) + lane);
           if (!(ok = warp_poll(uempty0 + 8 * seg, ((unit_no / kPtSegs) & 1) ^ 1, p.timeout_ns))) break;
           if (lane < 8) reinterpret_cast<int*>(&s.u)[lane] = word;
           if (lane == 8) s.kv = next - rec * p.Hkv;
@@ -834,9 +999,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     bool ok = aligned;
     // Rows of a query tile are token after token, a token's heads together.
     const int x = r / p.G, g = r - x * p.G;
-    // The first round takes no unit: one key tile of whatever lies in S, run
-    // through while the plan is made, so that the instructions are in the
-    // caches when the first scores arrive. Its weights go to S, which no product
+    // The first round takes no unit: one key tile of whatever lies in S and a
+    // unit's end without rows, run through while the plan is made, so that the
+    // instructions are in the caches when the first scores arrive. Its weights go to S, which no product
     // has written yet: the MMA warp waits for all warps' ofree of this round
     // before its first one.
     for (unsigned round = 0; ok; ++round) {
@@ -857,9 +1022,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const int n0 = sh.n0, n1 = sh.n1;
       const int mine = w ? n1 : n0;
       const int tx = x + (sh.pair ? w * p.TB : 0);    // this row's token of the unit
-      const bool live = x < p.TB && tx < u.ntok;
+      const bool live = x < p.TB && tx < u.ntok && !dry;
       // Warps without rows only keep step.
-      const bool active = __any_sync(0xffffffffu, live);
+      const bool active = dry || __any_sync(0xffffffffu, live);
       // Tiles from here on hold keys that some row of this query tile must not see.
       const int seen = !p.tree_mask && sh.pair && w ? min(u.base + p.TB + 1, u.lim) : sh.full;
       float m = -INFINITY, l = 0.0f;
@@ -872,12 +1037,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int c_first = (u.t0 + (NS == 1 || sh.pair ? j : 2 * j + w)) * KEYS;
         if (active) {
           const uint32_t s_addr = tmem + lane_addr + Shape::S_COL * sb;
-          if (c_first + KEYS > seen || p.negate) {
+          if (c_first + KEYS > seen || p.negate || dry) {
             // Masked keys, and a negative scale, in S itself.
 #pragma unroll 1
             for (int c0 = 0; c0 < KEYS; c0 += 32) {
               const uint32_t sees =
-                  live && !dry ? pt_sees(p, u.tok, u.base, u.lim, tx, c_first + c0) : 0u;
+                  live ? pt_sees(p, u.tok, u.base, u.lim, tx, c_first + c0) : 0u;
               float s[32];
               tmem_ld32(s_addr + c0, s);
               tmem_wait_ld();
@@ -976,7 +1141,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         m = top;
         l = y0.y * a0 + y1.y * a1;
       }
-      if (active && !dry) {
+      if (active) {
         const bool both = NS == 2 && merge && n1 > 0;
         const bool whole = u.slot < 0;
         const int c_begin = sh.pair ? 0 : w * (D / 2);
@@ -991,7 +1156,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const float inv = !whole ? 1.0f : empty ? 0.0f : 1.0f / l;
         a0 *= inv;
         a1 *= inv;
-        const bool any_odd = u.tiles > 0 && odd[unit_no & 3];
+        const bool any_odd = !dry && u.tiles > 0 && odd[unit_no & 3];
 #pragma unroll 1
         for (int c = c_begin; c < c_end; c += 32) {
           float o[32];
@@ -1063,12 +1228,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       }
     }
     // ------------------------------------------------- rows that were cut
-    const int n_splits = ok ? __ldcg(&p.head->splits) : 0;
+    const int n_splits = !ok ? 0 : p.small ? cut_count[0] : __ldcg(&p.head->splits);
     if (n_splits > 0) {
       // All slots of all items: the last units are about to end anyway.
-      unsigned want = 0;
-      for (int i = lane; i < n_splits; i += 32) want += __ldcg(&p.splits[i].splits);
-      want = __reduce_add_sync(0xffffffffu, want) * 8u * p.Hkv;
+      const unsigned want = (p.small ? cut_count[1] : __ldcg(&p.head->parts)) * 8u * p.Hkv;
       const uint64_t since = global_timer_ns();
       while (ok && *reinterpret_cast<volatile unsigned*>(&p.head->done) != want)
         ok = static_cast<long long>(global_timer_ns() - since) < p.timeout_ns;
@@ -1079,7 +1242,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 #pragma unroll 1
       for (int t = blockIdx.x; t < tasks; t += gridDim.x) {
         const int pos = t % kPer, ih = t / kPer, i = ih / p.Hkv, h = ih - i * p.Hkv;
-        const int4 raw = __ldcg(reinterpret_cast<const int4*>(p.splits + i));
+        const int4 raw = p.small ? *reinterpret_cast<const int4*>(cut_list + i)
+                                 : __ldcg(reinterpret_cast<const int4*>(p.splits + i));
         const int tok = raw.x, slot = raw.z, splits = raw.w;
         const int rows = raw.y * p.G, at = pos * 256 + threadIdx.x;
         if (at >= rows * (D / 4)) continue;

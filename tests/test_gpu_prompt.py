@@ -152,6 +152,17 @@ def test_trees_match_the_oracle(gq, case, vd):
     check(gq, make(np.random.default_rng(case[0] + case[2]), *case[:4], vd, *case[4:], tree=True))
 
 
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("case", PROMPTS, ids=IDS)
+def test_room_for_more_tokens(gq, case, tree):
+    # A captured step's padding: above 32 query tiles one CTA makes the plan for all, below it
+    # every CTA its own.
+    tiles = sum(-(-n // (128 * case[1] // case[0])) for n in case[5])
+    x = make(np.random.default_rng(12), *case[:4], "bf16", *case[4:], tree=tree,
+             pad=3 if tiles > 32 else 33 * 128)
+    check(gq, x)
+
+
 @pytest.mark.parametrize("D,Hkv", [(64, 2), (128, 2), (256, 1)])
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("vd", ["bf16", "fp16"])
@@ -160,6 +171,12 @@ def test_long_caches_are_cut(gq, D, Hkv, tree, vd):
     x = make(np.random.default_rng(D), 4 * Hkv, Hkv, D, 16, vd, [9000, 20, 4000], [40, 3, 1], tree=tree)
     a = check(gq, x)
     assert torch.equal(a, call(gq, x)), "not bitwise reproducible"
+    T = x["q"].shape[0]
+    more = torch.zeros((33 * 128, *x["q"].shape[1:]), dtype=x["q"].dtype)
+    y = dict(x, q=torch.cat([x["q"], more]))    # the other plan, with the same cuts
+    if tree:
+        y["mask"] = np.concatenate([x["mask"], np.zeros((len(more), x["mask"].shape[1]), np.int32)])
+    assert torch.equal(check(gq, y)[:T], a)
 
 
 def test_pairs_of_query_tiles(gq):
