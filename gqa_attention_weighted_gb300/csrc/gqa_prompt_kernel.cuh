@@ -36,7 +36,10 @@
 // streams take the two query tiles of a pair and share every K and V stage, or
 // the even and odd key tiles of a single query tile, merged at the unit's end.
 // D = 256: O fills half of the tensor memory, so there is one stream with two
-// S buffers and key tiles of 64.
+// S buffers and key tiles of 64; at that width the scores' product with both
+// operands in shared memory waits for it (48 cycles where it takes 32), so the
+// second warpgroup, which has no stream, copies the queries to tensor memory and
+// the product takes them from there.
 //
 // Masked places. A key that some row of a unit must not see can hold anything,
 // NaN and infinities too: its score is replaced, but a weight of 0 times such a
@@ -107,6 +110,7 @@ struct PtShape {
   static constexpr int SMEM = TILES_BYTES + MISC + 2048;
   static constexpr uint32_t S_COL = KEYS;              // tensor-memory columns of an S buffer
   static constexpr uint32_t O_COL0 = 256;
+  static constexpr uint32_t Q_COL = 128;               // queries in tensor memory (one stream)
 };
 
 // What a CTA works on at a time: key tiles t0 .. t0 + tiles - 1 for the rows of
@@ -376,19 +380,20 @@ struct PtSmallPlan {
       const int each = lane < total ? cost / cuts : -1;
       int rank = 0, src = 0;
 #pragma unroll 1
-      for (int i = 0; i < 32; ++i) {
+      for (int i = 0; i < total; ++i) {
         const int y = __shfl_sync(0xffffffffu, each, i);
         rank += y > each || (y == each && i < lane);
       }
 #pragma unroll 1
-      for (int i = 0; i < 32; ++i) src = __shfl_sync(0xffffffffu, rank, i) == lane ? i : src;
+      for (int i = 0; i < total; ++i) src = __shfl_sync(0xffffffffu, rank, i) == lane ? i : src;
       u.b = __shfl_sync(0xffffffffu, u.b, src);
       u.tok = __shfl_sync(0xffffffffu, u.tok, src);
       u.ntok = __shfl_sync(0xffffffffu, u.ntok, src);
       u.base = __shfl_sync(0xffffffffu, u.base, src);
       u.lim = __shfl_sync(0xffffffffu, u.lim, src);
       u.tiles = __shfl_sync(0xffffffffu, u.tiles, src);
-      cuts = __shfl_sync(0xffffffffu, cuts, src);
+      const int of = __shfl_sync(0xffffffffu, cuts, src);
+      cuts = lane < total ? of : 0;   // other lanes have no item
     }
     upto = warp_incl_sum(cuts);
     units = __shfl_sync(0xffffffffu, upto, 31) * p.Hkv;
@@ -617,8 +622,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   const uint32_t ofull0 = pfull0 + 16, ofree0 = ofull0 + 16, pvdone = ofree0 + 16;
   const uint32_t meet = pvdone + 8, drain = meet + 8, clean0 = drain + 8;
   const uint32_t issued0 = clean0 + 8 * kPtCleans;
-  const uint32_t ufull0 = issued0 + 8 * kPtCleans, uempty0 = ufull0 + 8 * kPtSegs;
-  constexpr int kBars = 2 * (KST + VST) + 15 + 2 * kPtCleans + 2 * kPtSegs;
+  const uint32_t tfull = issued0 + 8 * kPtCleans, tfree = tfull + 8;   // queries in tensor memory
+  const uint32_t ufull0 = tfree + 8, uempty0 = ufull0 + 8 * kPtSegs;
+  constexpr int kBars = 2 * (KST + VST) + 17 + 2 * kPtCleans + 2 * kPtSegs;
   struct Seg {
     PtUnit u;
     int kv;
@@ -650,13 +656,15 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     for (int i = 0; i < 2 * (KST + VST); ++i) mbar_init(kfull0 + 8 * i, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(qfull0 + 8 * i, 1);
-      mbar_init(qempty0 + 8 * i, 1);
+      mbar_init(qempty0 + 8 * i, NS == 1 ? 4 : 1);
       mbar_init(sfull0 + 8 * i, 1);
       mbar_init(pfull0 + 8 * i, 4);
       mbar_init(ofull0 + 8 * i, 1);
       mbar_init(ofree0 + 8 * i, 8);
     }
     mbar_init(pvdone, 1);
+    mbar_init(tfull, 4);
+    mbar_init(tfree, 1);
     mbar_init(meet, 8);
     mbar_init(drain, 1);
     for (int i = 0; i < 2 * kPtCleans; ++i) mbar_init(clean0 + 8 * i, 1);   // and issued0
@@ -901,8 +909,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         auto await_k = [&](int w, int j) {
           const int fill = fills + (pair ? w : 0);
           if (j == 0)
-            ok = ok && warp_poll(qfull0 + (NS == 2 ? 8 * (fill & 1) : 0),
-                                 (NS == 2 ? fill >> 1 : fill) & 1, p.timeout_ns);
+            ok = ok && (NS == 2 ? warp_poll(qfull0 + 8 * (fill & 1), fill >> 1 & 1, p.timeout_ns)
+                                : warp_poll(tfull, fill & 1, p.timeout_ns));
           if (pair && w && j < n0) return;           // the first stream's, too
           ok = ok && warp_poll(kfull0 + 8 * kst, kpar, p.timeout_ns);
         };
@@ -914,9 +922,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           const uint64_t b = k_desc + static_cast<uint64_t>(kst * (Shape::STAGE >> 4));
           const uint32_t s_tmem = tmem + Shape::S_COL * s_no;
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            mma_ss(leader, s_tmem, a + (uint64_t)((kk / 4 * 128 * 128 + kk % 4 * 32) >> 4),
-                   b + (uint64_t)((kk / 4 * KEYS * 128 + kk % 4 * 32) >> 4), qk_idesc, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint64_t b_kk = b + (uint64_t)((kk / 4 * KEYS * 128 + kk % 4 * 32) >> 4);
+            if (NS == 1)
+              mma_ts(leader, s_tmem, tmem + Shape::Q_COL + 8 * kk, b_kk, qk_idesc, kk > 0);
+            else
+              mma_ss(leader, s_tmem, a + (uint64_t)((kk / 4 * 128 * 128 + kk % 4 * 32) >> 4), b_kk,
+                     qk_idesc, kk > 0);
+          }
           commit_one(leader, sfull0 + 8 * s_no);
           // A pair's second stream is the last to use a stage: it has the more tiles.
           if (!pair || w) {
@@ -924,7 +937,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (++kst == KST) kst = 0, kpar ^= 1;
           }
           if (pair ? j == (w ? n1 : n0) - 1 : (NS == 2 ? 2 * j + w : j) == n - 1)
-            commit_one(leader, qempty0 + 8 * buf);
+            commit_one(leader, NS == 2 ? qempty0 + 8 * buf : tfree);
         };
         auto pv = [&](int w, int j, int s_no) {
           const int i = NS == 1 || pair ? j : 2 * j + w;
@@ -995,7 +1008,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const int w = warp >> 2;                  // stream
     const int r = threadIdx.x & 127;          // tensor-memory lane
     const uint32_t lane_addr = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    unsigned done = 0, ends0 = 0, ends1 = 0, meets = 0;
+    unsigned done = 0, ends0 = 0, ends1 = 0, meets = 0, copies = 0;
     bool ok = aligned;
     // Rows of a query tile are token after token, a token's heads together.
     const int x = r / p.G, g = r - x * p.G;
@@ -1027,6 +1040,33 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       const bool active = dry || __any_sync(0xffffffffu, live);
       // Tiles from here on hold keys that some row of this query tile must not see.
       const int seen = !p.tree_mask && sh.pair && w ? min(u.base + p.TB + 1, u.lim) : sh.full;
+      if (NS == 1 && w == 1 && u.tiles > 0 && !dry) {
+        // Queries from shared to tensor memory, once the last unit's scores are made.
+        // A row's 16-byte pieces lie where the swizzle has put them.
+        ok = warp_poll(qfull0, copies & 1, p.timeout_ns) &&
+             warp_poll(tfree, (copies & 1) ^ 1, p.timeout_ns);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll 1
+        for (int part = 0; part < PARTS; ++part) {
+          uint32_t q[32];
+          const uint4* src = reinterpret_cast<const uint4*>(smem + part * 128 * 128 + r * 128);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            const uint4 x = src[c ^ (r & 7)];
+            q[4 * c] = x.x; q[4 * c + 1] = x.y; q[4 * c + 2] = x.z; q[4 * c + 3] = x.w;
+          }
+          tmem_st32(tmem + lane_addr + Shape::Q_COL + 32 * part, q);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(tfull);
+          mbar_arrive(qempty0);
+        }
+        ++copies;
+      }
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < mine; ++j) {
         const unsigned no = done + j;
@@ -1237,16 +1277,26 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         ok = static_cast<long long>(global_timer_ns() - since) < p.timeout_ns;
       ok = __all_sync(0xffffffffu, ok);
       __threadfence();
-      constexpr int kPer = NS * 128 * (D / 4) / 256;   // tasks of an item and KV head
+      // A thread takes 8 columns of a row, 8 slots at a time: 16 loads of 16 bytes
+      // under way, and the next task's item before this one's sums.
+      constexpr int kPer = NS * 128 * (D / 8) / 256;   // tasks of an item and KV head
+      constexpr int U = 8;
       const int tasks = ok ? n_splits * p.Hkv * kPer : 0;
+      auto item_of = [&](int t) {
+        const int i = t / (kPer * p.Hkv);
+        return t >= tasks ? make_int4(0, 0, 0, 0)
+               : p.small  ? *reinterpret_cast<const int4*>(cut_list + i)
+                          : __ldcg(reinterpret_cast<const int4*>(p.splits + i));
+      };
+      int4 ahead = item_of(blockIdx.x);
 #pragma unroll 1
       for (int t = blockIdx.x; t < tasks; t += gridDim.x) {
-        const int pos = t % kPer, ih = t / kPer, i = ih / p.Hkv, h = ih - i * p.Hkv;
-        const int4 raw = p.small ? *reinterpret_cast<const int4*>(cut_list + i)
-                                 : __ldcg(reinterpret_cast<const int4*>(p.splits + i));
+        const int4 raw = ahead;
+        ahead = item_of(t + gridDim.x);
+        const int pos = t % kPer, h = t / kPer % p.Hkv;
         const int tok = raw.x, slot = raw.z, splits = raw.w;
         const int rows = raw.y * p.G, at = pos * 256 + threadIdx.x;
-        if (at >= rows * (D / 4)) continue;
+        if (at >= rows * (D / 8)) continue;
         const int c = at / rows, row = at - c * rows;
         const int tk = row / p.G, gh = row - tk * p.G;
         const int tile = NS == 2 && tk >= p.TB;
@@ -1254,21 +1304,21 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const size_t first = (static_cast<size_t>(slot) * p.Hkv + h) * NS + tile;
         const size_t step = static_cast<size_t>(p.Hkv) * NS;
         const float2* ms = p.part_ml + first * 128 + lane_row;
-        const float4* os = reinterpret_cast<const float4*>(p.part_o) + (first * (D / 4) + c) * 128 + lane_row;
-        constexpr int U = 4;
+        const float4* os = reinterpret_cast<const float4*>(p.part_o) + (first * (D / 4) + 2 * c) * 128 + lane_row;
         float top = -INFINITY, sum = 0.0f;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float acc[8] = {};
 #pragma unroll 1
         for (int s = 0; s < splits; s += U) {
           float2 mm[U];
-          float4 v[U];
+          float4 v[2 * U];
 #pragma unroll
           for (int k = 0; k < U; ++k) {
             mm[k] = make_float2(-INFINITY, 0.0f);
-            v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            v[2 * k] = v[2 * k + 1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             if (s + k < splits) {
               mm[k] = __ldcg(ms + (s + k) * step * 128);
-              v[k] = __ldcg(os + (s + k) * step * (D / 4) * 128);
+              v[2 * k] = __ldcg(os + (s + k) * step * (D / 4) * 128);
+              v[2 * k + 1] = __ldcg(os + (s + k) * step * (D / 4) * 128 + 128);
             }
           }
           float now = top;
@@ -1277,21 +1327,22 @@ __global__ void __launch_bounds__(kPtThreads, 1)
           const float old = ex2(top - now);
           top = now;
           sum *= old;
-          acc.x *= old; acc.y *= old; acc.z *= old; acc.w *= old;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) acc[e] *= old;
 #pragma unroll
           for (int k = 0; k < U; ++k) {
             const float a = ex2(mm[k].x - now);
             sum = fmaf(a, mm[k].y, sum);
-            acc.x = fmaf(a, v[k].x, acc.x);
-            acc.y = fmaf(a, v[k].y, acc.y);
-            acc.z = fmaf(a, v[k].z, acc.z);
-            acc.w = fmaf(a, v[k].w, acc.w);
+            const float* x = reinterpret_cast<const float*>(&v[2 * k]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(a, x[e], acc[e]);
           }
         }
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) +
-                                  (static_cast<size_t>(tok + tk) * p.Hq + h * p.G + gh) * D + 4 * c) =
-            make_uint2(pack2<Tag>(acc.x * inv, acc.y * inv), pack2<Tag>(acc.z * inv, acc.w * inv));
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                  (static_cast<size_t>(tok + tk) * p.Hq + h * p.G + gh) * D + 8 * c) =
+            make_uint4(pack2<Tag>(acc[0] * inv, acc[1] * inv), pack2<Tag>(acc[2] * inv, acc[3] * inv),
+                       pack2<Tag>(acc[4] * inv, acc[5] * inv), pack2<Tag>(acc[6] * inv, acc[7] * inv));
       }
     }
     if (!ok && lane == 0) atomicOr(&pt_status, kErrPtSoftmax);
