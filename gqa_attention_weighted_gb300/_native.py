@@ -425,6 +425,21 @@ def _int32(name: str, t, shape, dev: int) -> None:
         _refuse(name, t, dev, f"a contiguous CUDA int32 tensor of shape {tuple(shape)}")
 
 
+def _int32_at(name: str, t, shape, dev: int) -> int:
+    """The address of such a tensor."""
+    if (t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev
+            or not t.is_contiguous()):
+        _refuse(name, t, dev, f"a contiguous CUDA int32 tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _stream_on(stream, dev: int) -> Optional[int]:
+    """The handle of ``stream``, or of the stream that is current on ``dev``."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream_handle(stream)
+
+
 def _pools(k_pool: torch.Tensor, v_pool: torch.Tensor):
     shape, dtype = k_pool.shape, k_pool.dtype
     if len(shape) != 4 or v_pool.shape != shape:
@@ -569,19 +584,14 @@ def gqa_kv_fork(pools, parent, child, block_table, seq_lens, shares, free_list, 
         raise ValueError("block_table must be [B, max_blocks], free_list and parent of one dimension")
     B, max_blocks = block_table.shape
     N, n_free = parent.shape[0], free_list.shape[0]
-    _int32("block_table", block_table, (B, max_blocks), dev)
-    _int32("parent", parent, (N,), dev)
-    _int32("child", child, (N,), dev)
-    _int32("seq_lens", seq_lens, (B,), dev)
-    _int32("shares", shares, (pools.num_blocks,), dev)
-    _int32("free_list", free_list, (n_free,), dev)
-    _int32("free_count", free_count, (1,), dev)
-    _int32("fork_block", fork_block, (N,), dev)
-    _int32("free_left", free_left, (1,), dev)
-    _check_kv(lib.gqa_kv_fork(array, n_pools, row_bytes, _ptr(parent), _ptr(child),
-                              _ptr(block_table), _ptr(seq_lens), _ptr(shares), _ptr(free_list),
-                              _ptr(free_count), _ptr(fork_block), _ptr(free_left), N, B, max_blocks,
-                              n_free, pools.block_size, pools.num_blocks, _stream_handle(stream)))
+    at = _int32_at
+    _check_kv(lib.gqa_kv_fork(
+        array, n_pools, row_bytes, at("parent", parent, (N,), dev), at("child", child, (N,), dev),
+        at("block_table", block_table, (B, max_blocks), dev), at("seq_lens", seq_lens, (B,), dev),
+        at("shares", shares, (pools.num_blocks,), dev), at("free_list", free_list, (n_free,), dev),
+        at("free_count", free_count, (1,), dev), at("fork_block", fork_block, (N,), dev),
+        at("free_left", free_left, (1,), dev), N, B, max_blocks, n_free, pools.block_size,
+        pools.num_blocks, _stream_on(stream, dev)))
 
 
 def gqa_kv_keep(pools, cached_lens, accepted, accepted_count, block_table, seq_lens, kept_lens,
@@ -598,16 +608,13 @@ def gqa_kv_keep(pools, cached_lens, accepted, accepted_count, block_table, seq_l
         raise ValueError("block_table must be [B, max_blocks], accepted [B, W]")
     B, max_blocks = block_table.shape
     W = accepted.shape[1]
-    _int32("block_table", block_table, (B, max_blocks), dev)
-    _int32("cached_lens", cached_lens, (B,), dev)
-    _int32("accepted", accepted, (B, W), dev)
-    _int32("accepted_count", accepted_count, (B,), dev)
-    _int32("seq_lens", seq_lens, (B,), dev)
-    _int32("kept_lens", kept_lens, (B,), dev)
-    _check_kv(lib.gqa_kv_keep(array, n_pools, row_bytes, _ptr(cached_lens), _ptr(accepted),
-                              _ptr(accepted_count), _ptr(block_table), _ptr(seq_lens),
-                              _ptr(kept_lens), B, W, max_blocks, pools.block_size,
-                              pools.num_blocks, _stream_handle(stream)))
+    at = _int32_at
+    _check_kv(lib.gqa_kv_keep(
+        array, n_pools, row_bytes, at("cached_lens", cached_lens, (B,), dev),
+        at("accepted", accepted, (B, W), dev), at("accepted_count", accepted_count, (B,), dev),
+        at("block_table", block_table, (B, max_blocks), dev), at("seq_lens", seq_lens, (B,), dev),
+        at("kept_lens", kept_lens, (B,), dev), B, W, max_blocks, pools.block_size,
+        pools.num_blocks, _stream_on(stream, dev)))
     return kept_lens
 
 
@@ -625,17 +632,14 @@ def gqa_kv_release(block_table, old_lens, new_lens, shares, free_list, free_coun
     n_free = free_list.shape[0]
     num_blocks = int(shares.shape[0] if num_blocks is None else num_blocks)
     dev = _device("block_table", block_table)
-    _int32("block_table", block_table, (B, max_blocks), dev)
-    _int32("old_lens", old_lens, (B,), dev)
-    _int32("new_lens", new_lens, (B,), dev)
-    if shares is not None:
-        _int32("shares", shares, (num_blocks,), dev)
-    _int32("free_list", free_list, (n_free,), dev)
-    _int32("free_count", free_count, (1,), dev)
-    _int32("free_left", free_left, (1,), dev)
-    _check_kv(lib.gqa_kv_release(_ptr(block_table), _ptr(old_lens), _ptr(new_lens), _ptr(shares),
-                                 _ptr(free_list), _ptr(free_count), _ptr(free_left), B, max_blocks,
-                                 n_free, int(block_size), num_blocks, _stream_handle(stream)))
+    at = _int32_at
+    _check_kv(lib.gqa_kv_release(
+        at("block_table", block_table, (B, max_blocks), dev), at("old_lens", old_lens, (B,), dev),
+        at("new_lens", new_lens, (B,), dev),
+        None if shares is None else at("shares", shares, (num_blocks,), dev),
+        at("free_list", free_list, (n_free,), dev), at("free_count", free_count, (1,), dev),
+        at("free_left", free_left, (1,), dev), B, max_blocks, n_free, int(block_size), num_blocks,
+        _stream_on(stream, dev)))
 
 
 # ------------------------------------------- attention with shared prefixes
@@ -725,15 +729,13 @@ def _packed_attn(q, k_pool, v_pool, token_start, cached_lens, block_table, seq_l
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_blocks]")
     B, max_blocks = block_table.shape
-    _int32("block_table", block_table, (B, max_blocks), dev)
-    _int32("token_start", token_start, (B + 1,), dev)
-    if cached_lens is not None:
-        _int32("cached_lens", cached_lens, (B,), dev)
-    if seq_lens is not None:
-        _int32("seq_lens", seq_lens, (B,), dev)
-    return (dev, (_ptr(q), st[0], _ptr(k_pool), _ptr(v_pool), _ptr(token_start), _ptr(cached_lens)),
-            (_ptr(block_table), _ptr(seq_lens), _ptr(out), B, T, Hq, Hkv, D, _V_DTYPE[dtype],
-             block_size, num_blocks, max_blocks))
+    at = _int32_at
+    return (dev, (q.data_ptr(), st[0], k_pool.data_ptr(), v_pool.data_ptr(),
+                  at("token_start", token_start, (B + 1,), dev),
+                  None if cached_lens is None else at("cached_lens", cached_lens, (B,), dev)),
+            (at("block_table", block_table, (B, max_blocks), dev),
+             None if seq_lens is None else at("seq_lens", seq_lens, (B,), dev),
+             out.data_ptr(), B, T, Hq, Hkv, D, _V_DTYPE[dtype], block_size, num_blocks, max_blocks))
 
 
 def gqa_prompt_attn(q, k_pool, v_pool, token_start, cached_lens, block_table, seq_lens, out,
@@ -747,7 +749,7 @@ def gqa_prompt_attn(q, k_pool, v_pool, token_start, cached_lens, block_table, se
     dev, before, after = _packed_attn(q, k_pool, v_pool, token_start, cached_lens, block_table,
                                       seq_lens, out)
     sc = float(q.shape[2]) ** -0.5 if scale is None else float(scale)
-    _check_prompt(lib.gqa_prompt_attn(*before, *after, sc, _stream_handle(stream)))
+    _check_prompt(lib.gqa_prompt_attn(*before, *after, sc, _stream_on(stream, dev)))
     return out
 
 
@@ -765,10 +767,10 @@ def gqa_tree_attn(q, k_pool, v_pool, token_start, cached_lens, tree_mask, block_
     if tree_mask.dim() != 2:
         raise ValueError("tree_mask must be [T, words]")
     words = tree_mask.shape[1]
-    _int32("tree_mask", tree_mask, (q.shape[0], words), dev)
+    mask = _int32_at("tree_mask", tree_mask, (q.shape[0], words), dev)
     sc = float(q.shape[2]) ** -0.5 if scale is None else float(scale)
-    _check_prompt(lib.gqa_tree_attn(*before, _ptr(tree_mask), words, *after, sc,
-                                    _stream_handle(stream)))
+    _check_prompt(lib.gqa_tree_attn(*before, mask, words, *after, sc,
+                                    _stream_on(stream, dev)))
     return out
 
 

@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(32 * kKeepWarps)
 // Release
 // ---------------------------------------------------------------------------
 constexpr int kReleaseThreads = 1024;
+constexpr int kReleaseEach = 4;        // entries that a thread has under way
 constexpr int kReleaseCluster = 8;     // CTAs of one cluster where there are many entries
 constexpr int kReleaseCache = 16384;   // block numbers that a CTA keeps in shared memory
 
@@ -316,6 +317,7 @@ __global__ void __launch_bounds__(kReleaseThreads, 1)
   int32_t* cache = held + p.B;                 // [kReleaseCache]
   __shared__ int part[32];
   __shared__ int winners;                      // of this CTA, read by the others
+  __shared__ int sums[kReleaseEach][32];
   const int tid = threadIdx.x;
   const int rank = cluster_rank(), ctas = cluster_size();
   grid_dependency_wait();
@@ -344,6 +346,7 @@ __global__ void __launch_bounds__(kReleaseThreads, 1)
   const int per = (M + ctas - 1) / ctas;
   const int begin = min(rank * per, M), end = min(begin + per, M);
   auto lookup = [&](int e) {                   // entry e's block, -1: none
+    if (e >= end) return -1;
     int lo = 0, hi = p.B;                      // the last row with start[b] <= e
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -353,54 +356,99 @@ __global__ void __launch_bounds__(kReleaseThreads, 1)
     const int x = p.table[static_cast<size_t>(lo) * p.max_blocks + held[lo] + e - start[lo]];
     return x >= 0 && x < p.num_blocks ? x : -1;
   };
-  auto block_of = [&](int e) {
-    return e - begin < kReleaseCache ? cache[e - begin] : lookup(e);
-  };
   auto code = [&](int e) { return -0x40000000 - (M - e); };
+  // Four entries a thread at a time, so that their loads are under way together:
+  // e0, e0 + 1024, ...
+  auto blocks_of = [&](int e0, int (&x)[kReleaseEach]) {
+#pragma unroll
+    for (int k = 0; k < kReleaseEach; ++k) {
+      const int e = e0 + k * kReleaseThreads;
+      x[k] = e >= end ? -1 : e - begin < kReleaseCache ? cache[e - begin] : lookup(e);
+    }
+  };
+  auto counts_of = [&](const int (&x)[kReleaseEach], int (&v)[kReleaseEach]) {
+#pragma unroll
+    for (int k = 0; k < kReleaseEach; ++k) v[k] = x[k] >= 0 ? __ldcg(&p.shares[x[k]]) : 0;
+  };
+  constexpr int kWave = kReleaseEach * kReleaseThreads;
   // 1.
-  for (int e = begin + tid; e < end; e += kReleaseThreads) {
-    const int x = lookup(e);
-    if (e - begin < kReleaseCache) cache[e - begin] = x;
-    if (x >= 0 && p.shares) atomicSub(&p.shares[x], 1);
+  for (int e0 = begin + tid; e0 < end; e0 += kWave) {
+    int x[kReleaseEach];
+#pragma unroll
+    for (int k = 0; k < kReleaseEach; ++k) x[k] = lookup(e0 + k * kReleaseThreads);
+#pragma unroll
+    for (int k = 0; k < kReleaseEach; ++k) {
+      const int e = e0 + k * kReleaseThreads;
+      if (e < end && e - begin < kReleaseCache) cache[e - begin] = x[k];
+      if (x[k] >= 0 && p.shares) atomicSub(&p.shares[x[k]], 1);
+    }
   }
   if (p.shares) {
     __threadfence();
     cluster_barrier();
     // 2.
-    for (int e = begin + tid; e < end; e += kReleaseThreads) {
-      const int x = block_of(e);
-      if (x >= 0 && __ldcg(&p.shares[x]) < 0) atomicMin(&p.shares[x], code(e));
+    for (int e0 = begin + tid; e0 < end; e0 += kWave) {
+      int x[kReleaseEach], v[kReleaseEach];
+      blocks_of(e0, x);
+      counts_of(x, v);
+#pragma unroll
+      for (int k = 0; k < kReleaseEach; ++k)
+        if (v[k] < 0) atomicMin(&p.shares[x[k]], code(e0 + k * kReleaseThreads));
     }
     __threadfence();
     cluster_barrier();
   }
-  // 3.
-  auto goes = [&](int e) {
-    const int x = block_of(e);
-    return x >= 0 && (!p.shares || __ldcg(&p.shares[x]) == code(e));
+  // 3. Bit k: the thread's k-th entry from e0 on is the one.
+  auto goes = [&](int e0) {
+    int x[kReleaseEach], v[kReleaseEach];
+    blocks_of(e0, x);
+    if (p.shares) counts_of(x, v);
+    unsigned bits = 0;
+#pragma unroll
+    for (int k = 0; k < kReleaseEach; ++k)
+      if (x[k] >= 0 && (!p.shares || v[k] == code(e0 + k * kReleaseThreads))) bits |= 1u << k;
+    return bits;
   };
   int count = 0;
-  for (int e = begin + tid; e < end; e += kReleaseThreads) count += goes(e);
+  unsigned bits = 0;
+  for (int e0 = begin + tid; e0 < end; e0 += kWave) {
+    bits = goes(e0);
+    count += __popc(bits);
+  }
   carry = 0;
   release_scan(count, &carry, part);
   if (tid == 0) winners = carry;
   cluster_barrier();
-  int at = n_free, all = n_free;
-  for (int r = 0; r < ctas; ++r) {
-    const int n = cluster_read(&winners, r);
-    if (r < rank) at += n;
-    all += n;
-  }
-  // A count that becomes 0 is the code of no entry: nobody else is misled.
-  for (int e0 = begin; e0 < end; e0 += kReleaseThreads) {
-    const int e = e0 + tid;
-    const bool go = e < end && goes(e);
-    const int upto = release_scan(go, &at, part);
-    if (go) {
-      const int x = block_of(e);
-      if (upto <= p.n_free) p.free_list[upto - 1] = x;
-      if (p.shares) p.shares[x] = 0;
+  const int lane = tid & 31, warp = tid >> 5;
+  const int n = lane < ctas ? cluster_read(&winners, lane) : 0;   // at most 32 CTAs
+  int at = n_free + __reduce_add_sync(0xffffffffu, lane < rank ? n : 0);
+  const int all = n_free + __reduce_add_sync(0xffffffffu, n);
+  // Places: all entries of the first 1024, of the second, ... A count that becomes 0
+  // is the code of no entry: nobody else is misled.
+  const bool once = end - begin <= kWave;      // the bits are still at hand
+  for (int e0 = begin; e0 < end; e0 += kWave) {
+    if (!once) bits = goes(e0 + tid);
+    unsigned votes[kReleaseEach];
+#pragma unroll
+    for (int k = 0; k < kReleaseEach; ++k) {
+      votes[k] = __ballot_sync(0xffffffffu, bits >> k & 1);
+      if (lane == 0) sums[k][warp] = __popc(votes[k]);
     }
+    __syncthreads();
+    int x[kReleaseEach];
+    blocks_of(e0 + tid, x);
+#pragma unroll
+    for (int k = 0; k < kReleaseEach; ++k) {
+      const int s = sums[k][lane];
+      const int to = at + __reduce_add_sync(0xffffffffu, lane < warp ? s : 0) +
+                     __popc(votes[k] & ((1u << lane) - 1u));
+      at += __reduce_add_sync(0xffffffffu, s);
+      if (bits >> k & 1) {
+        if (to < p.n_free) p.free_list[to] = x[k];
+        if (p.shares) p.shares[x[k]] = 0;
+      }
+    }
+    __syncthreads();
   }
   if (rank == 0 && tid == 0) *p.free_left = min(all, p.n_free);
   cluster_barrier();   // nobody leaves while its count may be read

@@ -7,6 +7,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <map>
 #include <memory>
 #include <mutex>
@@ -189,6 +190,16 @@ inline cudaError_t launch_pdl(const void* fn, int grid, int block, size_t smem, 
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory, once a device (`done`: a
+// bit each, the kernel's own).
+inline cudaError_t allow_smem(const void* fn, int bytes, int dev, std::atomic<unsigned long long>* done) {
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev < 64 && (done->load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev < 64) done->fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 inline size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }

@@ -177,7 +177,9 @@ int attend(const Call& c, bool tree, long long wait_ns, unsigned withhold_from,
 
   const void* k = reinterpret_cast<const void*>(
       c.kv_dtype == GQA_AV_BF16 ? pick<Bf16Tag>(c.D) : pick<Fp16Tag>(c.D));
-  e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(c.D));
+  static std::atomic<unsigned long long> allowed[6];   // of each kernel
+  e = allow_smem(k, smem_bytes(c.D), dev,
+                 &allowed[(c.D == 64 ? 0 : c.D == 128 ? 2 : 4) + (c.kv_dtype == GQA_AV_FP16)]);
   if (e != cudaSuccess) return ptfail_cuda(e, "cudaFuncSetAttribute");
   void* args[] = {&p};
   e = launch_pdl(k, sms, kPtThreads, smem_bytes(c.D), stream, args);

@@ -3,7 +3,7 @@ current device before any library call (CPU only: tensors that say where they ar
 import pytest
 import torch
 
-from test_binding_devices import native, on  # noqa: F401  (native: the fixture)
+from test_binding_devices import native as binding, on  # noqa: F401  (binding: the fixture)
 
 B, T, MB, H, D, N, bf = 2, 3, 4, 2, 64, 2, torch.bfloat16
 PROMPT = dict(q=(T, H, D), k_pool=(4, 16, H, D), v_pool=(4, 16, H, D), token_start=(B + 1,),
@@ -18,6 +18,12 @@ CALLS = {"gqa_prompt_attn": PROMPT, "gqa_tree_attn": dict(PROMPT, tree_mask=(T, 
          "gqa_kv_fork": FORK, "gqa_kv_keep": KEEP, "gqa_kv_release": RELEASE}
 
 
+@pytest.fixture
+def native(binding, monkeypatch):  # noqa: F811
+    monkeypatch.setattr(binding, "_raw_stream", lambda dev: 0)
+    return binding
+
+
 def arguments(name, elsewhere=None, pools=0):
     args = {n: on(1 if n == elsewhere else 0, *shape,
                   dtype=bf if n in ("q", "out", "k_pool", "v_pool") else torch.int32)
@@ -30,20 +36,20 @@ def arguments(name, elsewhere=None, pools=0):
 
 
 @pytest.mark.parametrize("name", CALLS)
-def test_one_device_is_accepted(native, name):  # noqa: F811
+def test_one_device_is_accepted(native, name):
     getattr(native, name)(**arguments(name))
     assert native.lib.calls == 1
 
 
 @pytest.mark.parametrize("name,elsewhere", [(n, t) for n, c in CALLS.items() for t in c])
-def test_a_tensor_on_another_device_is_refused(native, name, elsewhere):  # noqa: F811
+def test_a_tensor_on_another_device_is_refused(native, name, elsewhere):
     with pytest.raises(ValueError, match=f"{elsewhere} is on cuda:1"):
         getattr(native, name)(**arguments(name, elsewhere))
     assert native.lib.calls == 0
 
 
 @pytest.mark.parametrize("name,wrong", [(n, t) for n, c in CALLS.items() for t in c])
-def test_a_tensor_of_another_shape_is_refused(native, name, wrong):  # noqa: F811
+def test_a_tensor_of_another_shape_is_refused(native, name, wrong):
     args = arguments(name)
     t = args[wrong]
     args[wrong] = on(0, *t.shape[:-1], t.shape[-1] + 1, dtype=t.dtype)
@@ -54,7 +60,7 @@ def test_a_tensor_of_another_shape_is_refused(native, name, wrong):  # noqa: F81
     assert native.lib.calls == 0
 
 
-def test_pools_are_of_one_kind_and_device(native, monkeypatch):  # noqa: F811
+def test_pools_are_of_one_kind_and_device(native, monkeypatch):
     for name in ("gqa_kv_fork", "gqa_kv_keep"):
         with pytest.raises(ValueError, match=r"pools\[1\] is on cuda:1"):
             getattr(native, name)(**arguments(name, pools=1))
@@ -69,7 +75,7 @@ def test_pools_are_of_one_kind_and_device(native, monkeypatch):  # noqa: F811
     assert native.lib.calls == 0
 
 
-def test_a_released_table_needs_shares_or_the_number_of_blocks(native):  # noqa: F811
+def test_a_released_table_needs_shares_or_the_number_of_blocks(native):
     args = dict(arguments("gqa_kv_release"), shares=None)
     with pytest.raises(ValueError, match="num_blocks"):
         native.gqa_kv_release(**args)
