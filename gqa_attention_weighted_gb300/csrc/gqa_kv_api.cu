@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -104,6 +105,32 @@ int check_rows(int B, int max_blocks, int block_size) {
   if (block_size > 0 && static_cast<long long>(max_blocks) * block_size > 0x7fffffffLL)
     return kfail(GQA_AV_ERR_UNSUPPORTED, "a table row of 2^31 or more cache rows");
   return GQA_AV_OK;
+}
+
+// The largest cluster that the release kernel can have on a device: 16 where it
+// allows that many, 8 is within every device's. Found once a device.
+int release_cluster(const void* fn, int dev) {
+  static std::atomic<int> known[64];
+  int n = dev < 64 ? known[dev].load(std::memory_order_relaxed) : 0;
+  if (n) return n;
+  n = kReleasePortable;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(kReleaseCluster);
+    cfg.blockDim = dim3(kReleaseThreads);
+    cfg.dynamicSmemBytes = 4 * (2 * kPageMaxB + 1 + kReleaseCache);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kReleaseCluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int fit = 0;
+    if (cudaOccupancyMaxActiveClusters(&fit, fn, &cfg) == cudaSuccess && fit > 0) n = kReleaseCluster;
+  }
+  cudaGetLastError();   // of a query that was refused
+  if (dev < 64) known[dev].store(n, std::memory_order_relaxed);
+  return n;
 }
 
 using RopeKernel = void (*)(RopeParams);
@@ -430,7 +457,11 @@ extern "C" int gqa_kv_release(const int32_t* block_table, const int32_t* old_len
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        4 * (2 * kPageMaxB + 1 + kReleaseCache));
   if (e != cudaSuccess) return kfail_cuda(e, "cudaFuncSetAttribute");
-  const int ctas = most > 4 * kReleaseThreads ? kReleaseCluster : 1;
+  int dev = 0, ctas = 1;
+  if (most > kReleaseEach * kReleaseThreads) {   // more than one CTA's entries at a time
+    if ((e = cudaGetDevice(&dev)) != cudaSuccess) return kfail_cuda(e, "cudaGetDevice");
+    ctas = release_cluster(fn, dev);
+  }
   void* args[] = {&p};
   e = launch(fn, ctas, kReleaseThreads, smem, static_cast<cudaStream_t>(stream), args, ctas);
   if (e != cudaSuccess) return kfail_cuda(e, "release kernel launch");

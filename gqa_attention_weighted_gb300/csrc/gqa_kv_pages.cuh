@@ -238,7 +238,9 @@ __global__ void __launch_bounds__(32 * kKeepWarps)
 // ---------------------------------------------------------------------------
 constexpr int kReleaseThreads = 1024;
 constexpr int kReleaseEach = 4;        // entries that a thread has under way
-constexpr int kReleaseCluster = 8;     // CTAs of one cluster where there are many entries
+// CTAs of one cluster where there are many entries: each gathers four bytes here
+// and there, about one a cycle and SM (256 requests, 22 thousand entries: see below).
+constexpr int kReleaseCluster = 16, kReleasePortable = 8;
 constexpr int kReleaseCache = 16384;   // block numbers that a CTA keeps in shared memory
 
 struct ReleaseParams {
