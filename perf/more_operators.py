@@ -338,7 +338,8 @@ def _plain_fork(s):
     need = (lens % bs > 0).long()
     at = s["free_count"].long() - need.cumsum(0)
     served = (need == 0) | (at >= 0)
-    block = torch.where(need > 0, s["free_list"][at.clamp(min=0)], -1)
+    # Before the first fork that needs a block, `at` lies one past the list.
+    block = torch.where(need > 0, s["free_list"][at.clamp(0, s["free_list"].numel() - 1)], -1)
     s["fork_block"].copy_(torch.where(served, block, -2))
     rows = s["table"][parent]
     j = torch.arange(rows.shape[1], device="cuda")
