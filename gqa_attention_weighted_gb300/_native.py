@@ -135,6 +135,24 @@ def _load() -> ctypes.CDLL:
 lib = _load()
 
 
+def _load_fastcall():
+    """The C++ side of the calls that check their tensors there."""
+    try:
+        from . import _fastcall
+    except ImportError as e:
+        raise ImportError(f"{_PKG}/_fastcall is missing: build the CUDA library first "
+                          "(python -c 'import __graft_entry__ as g; g.build()')") from e
+    _fastcall.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
+                     ("gqa_prompt_attn", "gqa_tree_attn", "gqa_kv_fork", "gqa_kv_keep",
+                      "gqa_kv_release")])
+    return _fastcall
+
+
+# Its calls return the library's status, or None where something is not as it should be: the
+# checks below then say what.
+_fast = _load_fastcall()
+
+
 def _check(status: int) -> None:
     if status != GQA_AV_OK:
         name = lib.gqa_av_status_string(status).decode()
@@ -425,6 +443,11 @@ def _int32(name: str, t, shape, dev: int) -> None:
         _refuse(name, t, dev, f"a contiguous CUDA int32 tensor of shape {tuple(shape)}")
 
 
+def _fast_stream(stream):
+    """None, for the current stream, or a stream's handle."""
+    return None if stream is None else _stream_handle(stream)
+
+
 def _int32_at(name: str, t, shape, dev: int) -> int:
     """The address of such a tensor."""
     if (t.dtype is not torch.int32 or t.shape != shape or t.get_device() != dev
@@ -560,7 +583,9 @@ class KvPools:
         for n in shape[2:]:
             row *= n
         self.row_bytes = row * pools[0].element_size()
-        self.array = (ctypes.c_void_p * len(pools))(*[t.data_ptr() for t in pools])
+        at = tuple(t.data_ptr() for t in pools)
+        self.array = (ctypes.c_void_p * len(pools))(*at)
+        self.fast = _fast.pools(at, self.device, self.row_bytes, self.num_blocks, self.block_size)
 
     def args(self):
         if self.device != torch.cuda.current_device():
@@ -578,6 +603,10 @@ def gqa_kv_fork(pools, parent, child, block_table, seq_lens, shares, free_list, 
     written."""
     if not isinstance(pools, KvPools):
         pools = KvPools(pools)
+    rc = _fast.fork(pools.fast, parent, child, block_table, seq_lens, shares, free_list, free_count,
+                    fork_block, free_left, _fast_stream(stream))
+    if rc is not None:
+        return _check_kv(rc)
     array, n_pools, row_bytes = pools.args()
     dev = pools.device
     if block_table.dim() != 2 or free_list.dim() != 1 or parent.dim() != 1:
@@ -602,6 +631,11 @@ def gqa_kv_keep(pools, cached_lens, accepted, accepted_count, block_table, seq_l
     Writes and returns ``kept_lens``: the cached rows and the kept ones."""
     if not isinstance(pools, KvPools):
         pools = KvPools(pools)
+    rc = _fast.keep(pools.fast, cached_lens, accepted, accepted_count, block_table, seq_lens,
+                    kept_lens, _fast_stream(stream))
+    if rc is not None:
+        _check_kv(rc)
+        return kept_lens
     array, n_pools, row_bytes = pools.args()
     dev = pools.device
     if block_table.dim() != 2 or accepted.dim() != 2:
@@ -624,6 +658,10 @@ def gqa_kv_release(block_table, old_lens, new_lens, shares, free_list, free_coun
     Its blocks past the new end lose an owner (``shares`` -= 1); those whose last owner let go are
     appended to ``free_list[:free_count]``, and ``free_left`` gets the new count. ``shares`` [
     num_blocks] may be None where no block is shared; ``num_blocks`` is needed then."""
+    rc = _fast.release(block_table, old_lens, new_lens, shares, free_list, free_count, free_left,
+                       block_size, num_blocks, _fast_stream(stream))
+    if rc is not None:
+        return _check_kv(rc)
     if block_table.dim() != 2 or free_list.dim() != 1:
         raise ValueError("block_table must be [B, max_blocks], free_list of one dimension")
     if shares is None and num_blocks is None:
@@ -746,6 +784,11 @@ def gqa_prompt_attn(q, k_pool, v_pool, token_start, cached_lens, block_table, se
     ``block_table[b]``. q is [T,Hq,D] of the pools' type, a view of a packed projection or not
     (scale defaults to 1/sqrt(D)); writes and returns ``out``, whose rows past the last sequence
     are left as they are. Calls on different streams and replays of different graphs may overlap."""
+    rc = _fast.attend(q, k_pool, v_pool, token_start, cached_lens, None, block_table, seq_lens, out,
+                      scale, _fast_stream(stream))
+    if rc is not None:
+        _check_prompt(rc)
+        return out
     dev, before, after = _packed_attn(q, k_pool, v_pool, token_start, cached_lens, block_table,
                                       seq_lens, out)
     sc = float(q.shape[2]) ** -0.5 if scale is None else float(scale)
@@ -760,6 +803,12 @@ def gqa_tree_attn(q, k_pool, v_pool, token_start, cached_lens, tree_mask, block_
     drafted rows behind them, row j where bit j % 32 of ``tree_mask[t, j // 32]`` is set (itself
     among them), all below ``seq_lens[b]`` (None: all). tree_mask is [T,words] int32; the rest as
     for gqa_prompt_attn."""
+    if tree_mask is not None:
+        rc = _fast.attend(q, k_pool, v_pool, token_start, cached_lens, tree_mask, block_table,
+                          seq_lens, out, scale, _fast_stream(stream))
+        if rc is not None:
+            _check_prompt(rc)
+            return out
     if cached_lens is None:
         raise ValueError("gqa_tree_attn needs cached_lens")
     dev, before, after = _packed_attn(q, k_pool, v_pool, token_start, cached_lens, block_table,

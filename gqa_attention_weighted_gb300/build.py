@@ -1,7 +1,8 @@
-"""In-tree build of libgqa_av.so (sm_103a) with nvcc.
+"""In-tree build of libgqa_av.so (sm_103a) with nvcc, and of the Python calls around
+it that need the tensors' C++ side (_fastcall, with the host compiler).
 
-The translation units compile in parallel; the library lands next to this
-file so that the Python binding loads it from the source tree. Nothing is
+The translation units compile in parallel; both land next to this file so that
+the Python binding loads them from the source tree. Nothing is
 installed into site-packages.
 """
 from __future__ import annotations
@@ -9,6 +10,7 @@ from __future__ import annotations
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -17,6 +19,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIBRARY = os.path.join(PKG, "libgqa_av.so")
+FASTCALL = os.path.join(PKG, "_fastcall" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 
 SOURCES = ["gqa_av_api.cu", "gqa_av_bf16.cu", "gqa_av_fp16.cu", "gqa_av_noalloc.cu", "gqa_qk_api.cu",
            "gqa_attn_api.cu", "gqa_kv_api.cu", "gqa_prefix_api.cu", "gqa_prompt_api.cu"]
@@ -38,14 +41,29 @@ def _inputs():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIBRARY):
+    if not os.path.exists(LIBRARY) or not os.path.exists(FASTCALL):
         return False
-    t = os.path.getmtime(LIBRARY)
+    t = min(os.path.getmtime(LIBRARY), os.path.getmtime(FASTCALL))
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def fastcall_command(out: str) -> list:
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc())) or "/usr/local/cuda"
+    include = [INCLUDE, os.path.join(home, "include"),
+               os.path.join(home, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[x for path in include for x in ("-I", path)],
+            os.path.join(CSRC, "gqa_fastcall.cpp"), "-o", out, "-L", os.path.join(home, "lib"),
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
-    """Compile and link libgqa_av.so; returns its path."""
+    """Compile and link libgqa_av.so and _fastcall; returns the library's path."""
     if not force and up_to_date():
         return LIBRARY
     os.makedirs(BUILD_DIR, exist_ok=True)
@@ -61,14 +79,25 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    def compile_fastcall():
+        cmd = fastcall_command(FASTCALL + ".tmp")
+        if verbose:
+            print(" ".join(cmd), file=sys.stderr)
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on gqa_fastcall.cpp:\n{r.stdout}\n{r.stderr}")
+
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        fast = ex.submit(compile_fastcall)
         objs = list(ex.map(compile_one, SOURCES))
+        fast.result()
     tmp = LIBRARY + ".tmp"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIBRARY)
+    os.replace(FASTCALL + ".tmp", FASTCALL)
     return LIBRARY
 
 
