@@ -84,6 +84,17 @@ int check(const Call& c, bool tree) {
   if (c.T > 1 && (c.q_stride & 7 || c.q_stride >= 1LL << 38))
     return ptfail(GQA_AV_ERR_UNSUPPORTED, "q_stride=%lld must be a multiple of 8 below 2^38",
                   static_cast<long long>(c.q_stride));
+  // Units write their rows while others still read.
+  const unsigned long long row = 2ull * c.Hq * c.D, pool = 2ull * c.num_blocks * c.block_size * c.Hkv * c.D;
+  const unsigned long long q = c.T > 1 ? 2ull * c.q_stride * (c.T - 1) + row : row, b4 = 4ull * c.B;
+  const struct { const char* name; const void* at; unsigned long long n; } ins[] = {
+      {"q", c.q, q}, {"k_pool", c.k_pool, pool}, {"v_pool", c.v_pool, pool},
+      {"token_start", c.token_start, b4 + 4}, {"cached_lens", c.cached_lens, b4},
+      {"tree_mask", c.tree_mask, 4ull * c.T * c.words}, {"seq_lens", c.seq_lens, b4},
+      {"block_table", c.block_table, b4 * c.max_blocks}};
+  for (const auto& i : ins)
+    if (c.T && i.at && addr(i.at) < addr(c.out) + row * c.T && addr(c.out) < addr(i.at) + i.n)
+      return ptfail(GQA_AV_ERR_INVALID, "out overlaps %s", i.name);
   return GQA_AV_OK;
 }
 

@@ -37,7 +37,7 @@
  * block_size]. Row c is in block table[c / block_size] at c % block_size; a
  * table entry outside [0, num_blocks) reads rows of zeros. Entries of blocks
  * past a length, and rows past a length inside a block, may hold anything. out
- * must not overlap an input.
+ * must not overlap an input (refused).
  *
  * Numerics: products on the tensor cores with fp32 accumulation; the running
  * maximum and sum of the softmax and the output sums are fp32; the weights

@@ -294,3 +294,82 @@ def test_single_token_of_any_stride(gq):
     x = make(np.random.default_rng(11), 8, 2, 64, 16, "bf16", [70], [1], pad=0)
     q = torch.as_strided(x["q"].cuda(), (1, 8, 64), (3, 64, 1))
     check(gq, x, q=q)
+
+
+# Hq, Hkv, D, block, cached lengths, new lengths: pairs of query tiles, at their edges and in
+# batches of few items whose keys are many (mean above 4096 rows), and plain heads of 256.
+PAIRS = [
+    (64, 64, 64, 64, [0, 100], [700, 650]),
+    (32, 4, 128, 32, [4500], [33]),                               # TB = 16: 2 pairs and a single tile
+    (8, 2, 64, 16, [5000, 4700], [64, 31]),
+    (3, 3, 256, 16, [70, 0], [200, 129]),
+    (160, 160, 128, 16, [3, 0, 200], [129, 256, 300]),
+]
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("case", PAIRS, ids=[f"Hq{c[0]}-Hkv{c[1]}-D{c[2]}" for c in PAIRS])
+def test_pairs_match_the_oracle(gq, case, tree):
+    check(gq, make(np.random.default_rng(13), *case[:4], "bf16", *case[4:], tree=tree))
+
+
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("case", PAIRS[:4], ids=[f"Hq{c[0]}-Hkv{c[1]}-D{c[2]}" for c in PAIRS[:4]])
+def test_pairs_with_values_that_are_not_finite(gq, case, tree):
+    # New tokens' values: seen by some rows of a pair, of both of its tiles, of cut items.
+    x = make(np.random.default_rng(14), *case[:4], "fp16", *case[4:], tree=tree)
+    bs, D = case[3], case[2]
+    for b, (a, n) in enumerate(zip(*case[4:])):
+        for i, value in ((0, "inf"), (n // 2, "nan"), (n - 1, "-inf"), (n // 3, "inf")):
+            c = a + i
+            x["v"][x["tab"][b, c // bs], c % bs, i % case[1], (7 * i) % D] = float(value)
+    check(gq, x)
+
+
+def test_rows_that_pass_the_plan_s_numbers(gq):
+    # One token behind 2^26 - 1 rows, the longest table row: its entries name three blocks in
+    # turn, so the softmax is over many copies of the same 384 rows (and one or two blocks more).
+    rng = np.random.default_rng(15)
+    bs, Hkv, D = 128, 1, 64
+    k, v = (torch.tensor(rng.standard_normal((3, bs, Hkv, D)), dtype=torch.float32).half() for _ in "kv")
+    n = 2 ** 26 // bs
+    tab = torch.arange(n, dtype=torch.int32, device="cuda")[None] % 3
+    q = torch.tensor(2 * rng.standard_normal((1, 2, D)), dtype=torch.float32).half()
+    counts = np.array([n // 3 + (i < n % 3) for i in range(3)], dtype=np.float64).repeat(bs)
+    counts[(n - 1) % 3 * bs + bs - 1] -= 1           # of 2^26 rows the last is not the token's own
+    own = (2 ** 26 - 2) // bs % 3 * bs + (2 ** 26 - 2) % bs
+    assert counts.sum() == 2 ** 26 - 1 and own == (n - 1) % 3 * bs + bs - 2
+    kd, vd, qd = (x.double().numpy() for x in (k, v, q))
+    s = qd[0] @ kd.reshape(-1, D).T * D ** -0.5
+    w = np.exp(s) * counts
+    ref = (w / w.sum(1, keepdims=True)) @ vd.reshape(-1, D)
+    for tree in (False, True):
+        args = (q.cuda(), k.cuda(), v.cuda(), i32([0, 1]), i32([2 ** 26 - 2]))
+        rest = (tab, None, torch.empty_like(q, device="cuda"))
+        got = gq.gqa_tree_attn(*args, i32([[1]]), *rest) if tree else gq.gqa_prompt_attn(*args, *rest)
+        gq.gqa_prompt_device_status()
+        # fp32 sums of 2^26 / (2 streams, 152 SMs and more) terms a partial, with 2^-24 a step of
+        # random sign, and half a step of the weights and of the output.
+        size = (w / w.sum(1, keepdims=True)) @ np.abs(vd.reshape(-1, D))
+        assert (np.abs(got.double().cpu().numpy()[0] - ref) <= 2.0 ** -11 * (np.abs(ref) + 2 * size)).all()
+
+
+def test_a_million_tokens(gq):
+    # 8192 sequences of 128 tokens whose tables name the same two blocks: each has the outputs
+    # of the first.
+    rng = np.random.default_rng(16)
+    x = make(rng, 1, 1, 64, 128, "bf16", [100], [128], pad=0)
+    want = check(gq, x)
+    B = 8192
+    q = x["q"].cuda().repeat(B, 1, 1)
+    out = torch.full_like(q, 7.0)
+    start = torch.arange(B + 1, dtype=torch.int32, device="cuda") * 128
+    tab = i32(x["tab"]).repeat(B, 1)
+    gq.gqa_prompt_attn(q, x["k"].cuda(), x["v"].cuda(), start, i32([100] * B), tab, None, out)
+    gq.gqa_prompt_device_status()
+    # Other units than the single call's, so other roundings: each is within half a step of the
+    # output and of the weights (at most the largest value) of the same sums.
+    first = out[:128]
+    assert (out.view(B, 128, 64) == first.view(1, 128, 64)).all()
+    diff, top = (first.double() - want.double()).abs(), x["v"][~x["v"].isnan()].abs().max().item()
+    assert (diff <= 2 * 2.0 ** -8 * (want.double().abs() * (1 + 2.0 ** -8) + top)).all()

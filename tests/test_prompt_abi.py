@@ -13,6 +13,7 @@ from oracle import gqa_prefix, gqa_prompt
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 HEADER = os.path.join(ROOT, "include", "gqa_prompt.h")
 FAKE = 1 << 20  # a non-NULL 16-byte-aligned address that no rejected call touches
+OUT = 1 << 40   # out lies elsewhere than the inputs
 
 
 @pytest.fixture(scope="module")
@@ -31,10 +32,10 @@ def test_library_exports_every_declared_symbol(native):
     assert [n for n in sorted(names) if not hasattr(lib, n)] == []
 
 
-PROMPT = dict(q=FAKE, qs=512, k=FAKE, v=FAKE, ts=FAKE, cached=FAKE, tab=FAKE, lens=FAKE, out=FAKE,
+PROMPT = dict(q=FAKE, qs=512, k=FAKE, v=FAKE, ts=FAKE, cached=FAKE, tab=FAKE, lens=FAKE, out=OUT,
               B=2, T=9, Hq=8, Hkv=2, D=64, dt=0, bs=16, nb=8, mb=4, scale=0.125)
 TREE = dict(q=FAKE, qs=512, k=FAKE, v=FAKE, ts=FAKE, cached=FAKE, mask=FAKE, words=1, tab=FAKE,
-            lens=FAKE, out=FAKE, B=2, T=9, Hq=8, Hkv=2, D=64, dt=0, bs=16, nb=8, mb=4, scale=0.125)
+            lens=FAKE, out=OUT, B=2, T=9, Hq=8, Hkv=2, D=64, dt=0, bs=16, nb=8, mb=4, scale=0.125)
 BAD = [
     (dict(B=0), 1), (dict(T=-1), 1), (dict(Hq=0), 1), (dict(Hkv=-2), 1), (dict(D=0), 1),
     (dict(bs=0), 1), (dict(nb=0), 1), (dict(mb=0), 1), (dict(Hkv=3), 1), (dict(dt=2), 1),
@@ -46,6 +47,11 @@ BAD = [
     (dict(T=(1 << 20) + 1), 2), (dict(Hkv=1025, Hq=1025, qs=1025 * 64), 2), (dict(nb=1 << 27), 2),
     (dict(mb=(1 << 22) + 1), 2), (dict(q=FAKE + 8), 2), (dict(v=FAKE + 2), 2), (dict(out=FAKE + 2), 2),
     (dict(qs=516), 2), (dict(qs=1 << 38), 2),
+    # out in the last query row, over the first and the last bytes of the pools, and of tables
+    (dict(q=OUT - 8 * 512 * 2 - 1008), 1), (dict(out=FAKE + 16 * 8 * 2 * 64 * 2 - 16), 1),
+    (dict(k=OUT + 9 * 512 * 2 - 16), 1), (dict(v=OUT - 16 * 8 * 2 * 64 * 2 + 16), 1),
+    (dict(tab=OUT + 9 * 512 * 2 - 4), 1), (dict(ts=OUT - 8), 1), (dict(lens=OUT - 4), 1),
+    (dict(cached=OUT), 1),
 ]
 
 
@@ -58,7 +64,7 @@ def test_prompt_host_checks(native, change, status):
 
 @pytest.mark.parametrize("change,status", BAD + [
     (dict(cached=None), 1), (dict(mask=None), 1), (dict(mask=FAKE + 2), 1), (dict(words=0), 1),
-    (dict(words=(1 << 15) + 1), 2)])
+    (dict(words=(1 << 15) + 1), 2), (dict(mask=OUT - 32), 1)])
 def test_tree_host_checks(native, change, status):
     rc = native.lib.gqa_tree_attn(*dict(TREE, **change).values(), None)
     assert rc == status, native.lib.gqa_prompt_last_error()
