@@ -26,10 +26,12 @@
 //                 log2 e; P goes back to tensor memory over S as 16 bits;
 //   O += P V      tcgen05.mma with P as the A operand from tensor memory and V
 //                 from shared memory (MN-major), O in tensor memory.
-// m moves only when a row's maximum has grown by more than 2^8 (then O and l
-// are rescaled), so O is rarely touched; weights stay below 2^8. They are rounded
-// to 16 bits for the one product that makes O (half a step each; the sum l takes
-// them unrounded).
+// m moves only when a row's maximum has grown by much (then O and l are rescaled),
+// so O is rarely touched. A tile without masks behind a first one is not searched
+// for its maximum at all: its weights are made with m as it is, and only if a row's
+// sum of them reaches 2^8 are they made again, with the tile's own maximum. So
+// weights stay below 2^8. They are rounded to 16 bits for the one product that makes
+// O (half a step each; the sum l takes them unrounded).
 //
 // D <= 128: two streams (S, O and a softmax warpgroup each) work in turn, so
 // the tensor core multiplies for one while the other makes weights. The
@@ -609,6 +611,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   // fp16 weights are scaled by 2^6 (at most 2^14 with the growth allowance), so
   // that small ones keep their bits; the sum carries the same factor.
   constexpr float kOff = std::is_same<Tag, Fp16Tag>::value ? 6.0f : 0.0f;
+  constexpr float kMostSum = std::is_same<Tag, Fp16Tag>::value ? 256.0f * 64.0f : 256.0f;
   extern __shared__ __align__(1024) uint8_t pt_smem[];
   uint8_t* smem = pt_smem;
   const uint32_t base_s = smem_addr(smem);
@@ -1131,77 +1134,116 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const int c_first = (u.t0 + (NS == 1 || sh.pair ? j : 2 * j + w)) * KEYS;
         if (active) {
           const uint32_t s_addr = tmem + lane_addr + Shape::S_COL * sb;
-          if (c_first + KEYS > seen || p.negate || dry) {
-            // Masked keys, and a negative scale, in S itself.
-#pragma unroll 1
-            for (int c0 = 0; c0 < KEYS; c0 += 32) {
-              const uint32_t sees =
-                  live ? pt_sees(p, u.tok, u.base, u.lim, tx, c_first + c0) : 0u;
-              float s[32];
+          const bool masked = c_first + KEYS > seen || p.negate || dry;
+          const bool tried = j > 0 && !masked;
+          bool done_with = false;
+          if (tried) {
+            // One pass over the scores, 64 at a time; the weights go back to tensor
+            // memory once their sums are known to be small. (A pass that found the
+            // maximum too was no faster than one for it and one for the weights.)
+            const float shift = kOff - m, qscale = p.qscale;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            uint32_t w16[KEYS / 2];
+            float s[64];
+#pragma unroll
+            for (int c0 = 0; c0 < KEYS; c0 += 64) {
               tmem_ld32(s_addr + c0, s);
+              tmem_ld32(s_addr + c0 + 32, s + 32);
               tmem_wait_ld();
-              hold<32>(s);
+              hold<64>(s);
 #pragma unroll
-              for (int c = 0; c < 32; ++c)
-                s[c] = (sees >> c) & 1u ? (p.negate ? -s[c] : s[c]) : -INFINITY;
-              tmem_st32(s_addr + c0, reinterpret_cast<const uint32_t*>(s));
+              for (int c = 0; c < 64; c += 2) {
+                float a, b;
+                fma2(s[c], s[c + 1], qscale, qscale, shift, shift, a, b);
+                a = ex2(a);
+                b = ex2(b);
+                add2(sum[c & 2], sum[(c & 2) + 1], a, b);
+                w16[(c0 + c) / 2] = pack2<Tag>(a, b);
+              }
             }
-            tmem_wait_st();
+            const float all = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            done_with = !__any_sync(0xffffffffu, live && !(all < kMostSum));
+            if (done_with) {
+#pragma unroll
+              for (int c0 = 0; c0 < KEYS / 2; c0 += 32) tmem_st32(s_addr + c0, w16 + c0);
+              l += all;
+            }
           }
-          float s[KEYS];
-#pragma unroll
-          for (int c0 = 0; c0 < KEYS; c0 += 32) tmem_ld32(s_addr + c0, s + c0);
-          tmem_wait_ld();
-          hold<KEYS>(s);
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-          for (int c = 0; c < KEYS; c += 8)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
-          if (j == 0) {
-            m = top == -INFINITY ? -1e30f : top;   // nothing finite yet: weights of 0
-          } else if (__any_sync(0xffffffffu, live && top > m + kPtGrow)) {
-            // Each row by itself: lanes without a row hold anything, and must
-            // not move the others' maxima.
-            // The previous tiles' products are done: S of this tile was
-            // multiplied after them, or (one stream) the wait below.
-            if (NS == 1) {
-              if (!(ok = warp_poll(pvdone, (no - 1) & 1, p.timeout_ns))) break;
-              tc_fence_after();
-            }
-            const float now = top > m + kPtGrow ? top : m, a = ex2(m - now);
-            m = now;
-            l *= a;
-            const uint32_t o_addr = tmem + lane_addr + Shape::O_COL0 + w * D;
+          if (!done_with) {
+            // Sums that were too large move the maximum however little it has grown.
+            const float grow = tried ? 0.0f : kPtGrow;
+            if (masked) {
+              // Masked keys, and a negative scale, in S itself.
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float o[32];
-              tmem_ld32(o_addr + c, o);
-              tmem_wait_ld();
-              hold<32>(o);
+              for (int c0 = 0; c0 < KEYS; c0 += 32) {
+                const uint32_t sees =
+                    live ? pt_sees(p, u.tok, u.base, u.lim, tx, c_first + c0) : 0u;
+                float s[32];
+                tmem_ld32(s_addr + c0, s);
+                tmem_wait_ld();
+                hold<32>(s);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= a;
-              tmem_st32(o_addr + c, reinterpret_cast<const uint32_t*>(o));
+                for (int c = 0; c < 32; ++c)
+                  s[c] = (sees >> c) & 1u ? (p.negate ? -s[c] : s[c]) : -INFINITY;
+                tmem_st32(s_addr + c0, reinterpret_cast<const uint32_t*>(s));
+              }
+              tmem_wait_st();
             }
-          }
-          const float shift = kOff - m, qscale = p.qscale;
-          float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            float s[KEYS];
 #pragma unroll
-          for (int c0 = 0; c0 < KEYS; c0 += 64) {
-            uint32_t w16[32];
+            for (int c0 = 0; c0 < KEYS; c0 += 32) tmem_ld32(s_addr + c0, s + c0);
+            tmem_wait_ld();
+            hold<KEYS>(s);
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < 64; c += 2) {
-              float a, b;
-              fma2(s[c0 + c], s[c0 + c + 1], qscale, qscale, shift, shift, a, b);
-              a = ex2(a);
-              b = ex2(b);
-              add2(sum[c & 2], sum[(c & 2) + 1], a, b);
-              w16[c / 2] = pack2<Tag>(a, b);
+            for (int c = 0; c < KEYS; c += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + e], s[c + 4 + e]);
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.qscale;
+            if (j == 0) {
+              m = top == -INFINITY ? -1e30f : top;   // nothing finite yet: weights of 0
+            } else if (__any_sync(0xffffffffu, live && top > m + grow)) {
+              // Each row by itself: lanes without a row hold anything, and must
+              // not move the others' maxima.
+              // The previous tiles' products are done: S of this tile was
+              // multiplied after them, or (one stream) the wait below.
+              if (NS == 1) {
+                if (!(ok = warp_poll(pvdone, (no - 1) & 1, p.timeout_ns))) break;
+                tc_fence_after();
+              }
+              const float now = top > m + grow ? top : m, a = ex2(m - now);
+              m = now;
+              l *= a;
+              const uint32_t o_addr = tmem + lane_addr + Shape::O_COL0 + w * D;
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                float o[32];
+                tmem_ld32(o_addr + c, o);
+                tmem_wait_ld();
+                hold<32>(o);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= a;
+                tmem_st32(o_addr + c, reinterpret_cast<const uint32_t*>(o));
+              }
             }
-            tmem_st32(s_addr + c0 / 2, w16);   // over scores that have been read
+            const float shift = kOff - m, qscale = p.qscale;
+            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int c0 = 0; c0 < KEYS; c0 += 64) {
+              uint32_t w16[32];
+#pragma unroll
+              for (int c = 0; c < 64; c += 2) {
+                float a, b;
+                fma2(s[c0 + c], s[c0 + c + 1], qscale, qscale, shift, shift, a, b);
+                a = ex2(a);
+                b = ex2(b);
+                add2(sum[c & 2], sum[(c & 2) + 1], a, b);
+                w16[c / 2] = pack2<Tag>(a, b);
+              }
+              tmem_st32(s_addr + c0 / 2, w16);   // over scores that have been read
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
           tmem_wait_st();
         }
         tc_fence_before();

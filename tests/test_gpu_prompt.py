@@ -373,3 +373,24 @@ def test_a_million_tokens(gq):
     assert (out.view(B, 128, 64) == first.view(1, 128, 64)).all()
     diff, top = (first.double() - want.double()).abs(), x["v"][~x["v"].isnan()].abs().max().item()
     assert (diff <= 2 * 2.0 ** -8 * (want.double().abs() * (1 + 2.0 ** -8) + top)).all()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("vd", ["bf16", "fp16"])
+def test_sums_that_cross_their_bound(gq, D, vd):
+    # Scores that step up by a little, by 2^7, by 2^40 and by 2^90 in the middle of a tile, down
+    # again, and equal ones many tiles long: weights made with an old maximum are kept, made
+    # again, or past what their type holds.
+    steps = [0.0, 0.1, 5.0, -3.0, 33.0, 33.1, 90.0, 90.0, 20.0, 170.0]
+
+    def key(c):
+        return steps[c // 70 % len(steps)] * 0.6931472 + (1e-3 * c if c % 7 == 0 else 0.0)
+
+    x = make(np.random.default_rng(17), 4, 1, D, 16, vd, [1500, 0], [9, 800], spread=0.0)
+    for b in range(2):
+        for c in range(x["cached"][b] + (9, 800)[b]):
+            x["k"][x["tab"][b, c // 16], c % 16] = 0
+            x["k"][x["tab"][b, c // 16], c % 16, 0, 0] = key(c)
+    x["q"][:, :, 0] = torch.tensor([1.0, 0.5, -1.0, 0.0])
+    check(gq, x, scale=1.0)
+    check(gq, x, scale=-1.0)
