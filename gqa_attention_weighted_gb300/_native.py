@@ -112,11 +112,14 @@ def _load() -> ctypes.CDLL:
     lib.gqa_prompt_release_graph_workspaces.argtypes = []
     lib.gqa_prompt_selftest_wait_timeout.argtypes = [P, L, *[P] * 7, *[I] * 9, F,
                                                      ctypes.c_longlong, I, P]
+    lib.gqa_prompt_selftest_late_start.argtypes = [P, L, *[P] * 7, *[I] * 9, F, ctypes.c_longlong, I,
+                                                   ctypes.c_longlong, P]
     lib.gqa_prompt_last_error.argtypes = []
     lib.gqa_prompt_last_error.restype = ctypes.c_char_p
     for f in ("gqa_kv_fork", "gqa_kv_keep", "gqa_kv_release",
               "gqa_prompt_attn", "gqa_tree_attn", "gqa_prompt_device_status",
-              "gqa_prompt_release_graph_workspaces", "gqa_prompt_selftest_wait_timeout"):
+              "gqa_prompt_release_graph_workspaces", "gqa_prompt_selftest_wait_timeout",
+              "gqa_prompt_selftest_late_start"):
         getattr(lib, f).restype = I
     for f in ("gqa_kv_tables", "gqa_kv_norm_rope_append", "gqa_prefix_attn_decode",
               "gqa_prefix_device_status", "gqa_prefix_release_graph_workspaces",

@@ -127,8 +127,14 @@ int encode_maps(PromptParams* p, const Call& c) {
   return rc;
 }
 
-int attend(const Call& c, bool tree, long long wait_ns, unsigned withhold_from,
-           cudaStream_t stream) try {
+// What the self-tests change.
+struct Trial {
+  long long wait_ns = kPtTimeoutNs;
+  unsigned withhold_from = ~0u, late_from = ~0u;
+  long long late_ns = 0;
+};
+
+int attend(const Call& c, bool tree, cudaStream_t stream, const Trial& trial = {}) try {
   int rc = check(c, tree);
   if (rc) return rc;
   if (c.T == 0) return GQA_AV_OK;
@@ -154,8 +160,10 @@ int attend(const Call& c, bool tree, long long wait_ns, unsigned withhold_from,
   if (s2 > FLT_MAX) return ptfail(GQA_AV_ERR_UNSUPPORTED, "scale=%g is too large", (double)c.scale);
   p.qscale = std::max(static_cast<float>(s2), FLT_MIN);
   p.negate = c.scale < 0.0f;
-  p.timeout_ns = wait_ns;
-  p.withhold_from = withhold_from;
+  p.timeout_ns = trial.wait_ns;
+  p.withhold_from = trial.withhold_from;
+  p.late_from = trial.late_from;
+  p.late_ns = trial.late_ns;
 
   // Items: query tiles, one more a sequence than its tokens fill. Slots: a chunk is
   // at least a quarter of an SM's share of the work, so all chunks are at most 4 an
@@ -215,7 +223,7 @@ extern "C" int gqa_prompt_attn(const void* q, int64_t q_stride, const void* k_po
   const Call c = {q, k_pool, v_pool, q_stride, token_start, cached_lens, nullptr, block_table,
                   seq_lens, out, 0, B, T, Hq, Hkv, D, kv_dtype, block_size, num_blocks, max_blocks,
                   scale};
-  return attend(c, false, kPtTimeoutNs, ~0u, static_cast<cudaStream_t>(stream));
+  return attend(c, false, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" int gqa_tree_attn(const void* q, int64_t q_stride, const void* k_pool,
@@ -228,7 +236,7 @@ extern "C" int gqa_tree_attn(const void* q, int64_t q_stride, const void* k_pool
   const Call c = {q, k_pool, v_pool, q_stride, token_start, cached_lens, tree_mask, block_table,
                   seq_lens, out, words, B, T, Hq, Hkv, D, kv_dtype, block_size, num_blocks,
                   max_blocks, scale};
-  return attend(c, true, kPtTimeoutNs, ~0u, static_cast<cudaStream_t>(stream));
+  return attend(c, true, static_cast<cudaStream_t>(stream));
 }
 
 // The K warp issues no query load from number `withhold_from` of each CTA on
@@ -247,8 +255,30 @@ extern "C" int gqa_prompt_selftest_wait_timeout(
   const Call c = {q, k_pool, v_pool, q_stride, token_start, cached_lens, nullptr, block_table,
                   seq_lens, out, 0, B, T, Hq, Hkv, D, kv_dtype, block_size, num_blocks, max_blocks,
                   scale};
-  return attend(c, false, wait_ns, static_cast<unsigned>(withhold_from),
-                static_cast<cudaStream_t>(stream));
+  Trial t;
+  t.wait_ns = wait_ns;
+  t.withhold_from = static_cast<unsigned>(withhold_from);
+  return attend(c, false, static_cast<cudaStream_t>(stream), t);
+}
+
+extern "C" int gqa_prompt_selftest_late_start(
+    const void* q, int64_t q_stride, const void* k_pool, const void* v_pool,
+    const int32_t* token_start, const int32_t* cached_lens, const int32_t* block_table,
+    const int32_t* seq_lens, void* out, int B, int T, int Hq, int Hkv, int D, int kv_dtype,
+    int block_size, int num_blocks, int max_blocks, float scale, long long wait_ns, int late_from,
+    long long late_ns, void* stream) {
+  g_pt_error[0] = 0;
+  if (wait_ns < 100000 || wait_ns > kPtTimeoutNs || late_from < 0 || late_ns < 0 || late_ns > kPtTimeoutNs)
+    return ptfail(GQA_AV_ERR_INVALID, "wait_ns=%lld must be in [100000, %lld], late_from=%d not negative "
+                  "and late_ns=%lld in [0, %lld]", wait_ns, kPtTimeoutNs, late_from, late_ns, kPtTimeoutNs);
+  const Call c = {q, k_pool, v_pool, q_stride, token_start, cached_lens, nullptr, block_table,
+                  seq_lens, out, 0, B, T, Hq, Hkv, D, kv_dtype, block_size, num_blocks, max_blocks,
+                  scale};
+  Trial t;
+  t.wait_ns = wait_ns;
+  t.late_from = static_cast<unsigned>(late_from);
+  t.late_ns = late_ns;
+  return attend(c, false, static_cast<cudaStream_t>(stream), t);
 }
 
 extern "C" int gqa_prompt_device_status(void* stream_, int clear) {

@@ -13,11 +13,16 @@
 // units of at most a chunk where that evens the SMs out; other items are one unit
 // each and write their output themselves. Units are handed out heaviest first, each for every KV head. The
 // lengths live on the device, so the first CTA to arrive makes the list while
-// the others set up; who was first shows in a ticket, so no CTA waits for one
-// that has not started. Where an item was cut, its units write their
-// unnormalised output, maximum and sum to slots, and when no unit is left the
-// CTAs join each row's slots in split order: who computed what does not matter
-// for the result.
+// the others set up; who was first shows in a ticket. Where an item was cut, its
+// units write their unnormalised output, maximum and sum to slots, and when no
+// unit is left the CTAs join each row's slots in split order: who computed what
+// does not matter for the result.
+//
+// CTAs that wait. The list and the slots are waited for by CTAs that hold an SM,
+// and nothing says that all CTAs of a launch are placed at once: other streams'
+// kernels may hold SMs, and wait likewise. So a CTA owns nothing before it runs:
+// the list's maker is whoever came first, and every unit, a CTA's first one too, is
+// claimed from one counter. What is waited for is then done by CTAs that run.
 //
 // A unit runs an online softmax over tiles of KEYS keys:
 //   S = Q K^T     tcgen05.mma, M = 128 rows, N = KEYS, both from shared memory
@@ -170,6 +175,8 @@ struct alignas(64) PromptParams {
   int small;                      // at most kPtSmall sequences and items: no list of units
   long long timeout_ns;
   unsigned withhold_from;         // self-test: query loads from this one of a CTA on are not issued
+  unsigned late_from;             // self-test: CTAs from this one on start late_ns later
+  long long late_ns;
 };
 
 __device__ __forceinline__ int pt_block_of(const PromptParams& p, int c) {
@@ -697,6 +704,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
   }
   grid_dependency_wait();
   grid_launch_dependents();
+  if (threadIdx.x == 0 && blockIdx.x >= p.late_from) {
+    const uint64_t since = global_timer_ns();
+    while (static_cast<long long>(global_timer_ns() - since) < p.late_ns) __nanosleep(1000);
+  }
   if (threadIdx.x == 0) *ticket = p.small ? 1u : atomicAdd(&p.head->ticket, 1u);
   tc_fence_before();
   __syncthreads();
@@ -734,8 +745,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
       // lane 16 + s: into query buffer s.
       unsigned held = 0;
       bool ok = true;
-      int next = blockIdx.x, total = 0;
+      int next = 0, total = 0;
       PtSmallPlan<D> plan;
+      // The first unit is claimed like the others, while the plan is made.
+      if (is_k && lane == 0) next = atomicAdd(&p.head->next, 1u);
       if (is_k && p.small) {
         plan.make(p);
         plan.publish(cut_list, cut_count);
@@ -750,6 +763,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         total = __ldcg(&p.head->units);
         if (!ok && lane == 0) atomicOr(&pt_status, kErrPtPlan);
       }
+      next = __shfl_sync(0xffffffffu, next, 0);
       for (unsigned unit_no = 0; ok; ++unit_no) {
         const int seg = unit_no % kPtSegs;
         Seg& s = segs[seg];
@@ -777,7 +791,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         // The next unit is taken late, so that who is ahead takes more (at the head of
         // the current one: trees of 64 sequences of 1 to 8192 rows end 25 us apart).
         const int claim_at = max(n - 2, 0);
-        if (is_k && lane == 0 && n == 0) claim = atomicAdd(&p.head->next, 1u) + gridDim.x;
+        if (is_k && lane == 0 && n == 0) claim = atomicAdd(&p.head->next, 1u);
         const int32_t* table = p.block_table + static_cast<size_t>(u.b) * p.max_blocks;
         // The pool row of this lane's box of tile i; rows past the last visible
         // one and entries outside the pool read zeros.
@@ -809,7 +823,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const CUtensorMap* map = is_k ? &p.k_map : &p.v_map;
         const int first_clean = uniform(pt_share<D>(p, u).full) / KEYS - uniform(u.t0);
         for (int i = 0; i < n && ok; ++i) {
-          if (is_k && lane == 0 && i == claim_at) claim = atomicAdd(&p.head->next, 1u) + gridDim.x;
+          if (is_k && lane == 0 && i == claim_at) claim = atomicAdd(&p.head->next, 1u);
           const int ahead = row_of(i + 1);
           if (!(ok = warp_poll(empty0 + 8 * stage, parity ^ 1, p.timeout_ns))) break;
           const uint32_t bar = full0 + 8 * stage, dst = ring_s + stage * Shape::STAGE;
@@ -1380,7 +1394,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     // ------------------------------------------------- rows that were cut
     const int n_splits = !ok ? 0 : p.small ? cut_count[0] : __ldcg(&p.head->splits);
     if (n_splits > 0) {
-      // All slots of all items: the last units are about to end anyway.
+      // All slots of all items: no unit is unclaimed, so CTAs that run are about to
+      // end the last ones.
       const unsigned want = (p.small ? cut_count[1] : __ldcg(&p.head->parts)) * 8u * p.Hkv;
       const uint64_t since = global_timer_ns();
       while (ok && *reinterpret_cast<volatile unsigned*>(&p.head->done) != want)

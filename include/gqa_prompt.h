@@ -115,6 +115,21 @@ int gqa_prompt_selftest_wait_timeout(const void *q, int64_t q_stride, const void
                                      int max_blocks, float scale, long long wait_ns,
                                      int withhold_from, void *stream);
 
+/*
+ * Self-test of calls whose CTAs are not all placed at once (other kernels hold
+ * SMs): gqa_prompt_attn with bounded waits of wait_ns (100 us to 2 s) and with the
+ * CTAs from number late_from on starting late_ns (at most 2 s) after the others. No
+ * CTA waits for one that has not started, so `out` is what gqa_prompt_attn gives
+ * and no wait runs out, however late they are.
+ */
+int gqa_prompt_selftest_late_start(const void *q, int64_t q_stride, const void *k_pool,
+                                   const void *v_pool, const int32_t *token_start,
+                                   const int32_t *cached_lens, const int32_t *block_table,
+                                   const int32_t *seq_lens, void *out, int B, int T, int Hq, int Hkv,
+                                   int D, int kv_dtype, int block_size, int num_blocks,
+                                   int max_blocks, float scale, long long wait_ns, int late_from,
+                                   long long late_ns, void *stream);
+
 /* Message of the calling thread's last error of these calls ("" if none). */
 const char *gqa_prompt_last_error(void);
 
