@@ -486,7 +486,8 @@ def gqa_kv_tables(cached_lens, new_lens, free_list, free_count, block_table, seq
     """Block-table entries, slots and positions of a step's new tokens: blocks come off the end
     of ``free_list[:free_count]`` in request order and ``block_table`` is updated in place;
     ``seq_lens``, ``token_start``, ``slots``, ``positions`` and ``free_left`` are written.
-    Requests that find no blocks keep their length and get slots of -1."""
+    Requests that find no blocks keep their length and get slots of -1. Where ``cached_lens[b]``
+    ends inside a block, new rows go into it: it must be the request's own (gqa_kv_release)."""
     if block_table.dim() != 2 or free_list.dim() != 1 or slots.dim() != 1:
         raise ValueError("block_table must be [B, max_blocks], free_list and slots of one "
                          "dimension")
@@ -631,7 +632,8 @@ def gqa_kv_keep(pools, cached_lens, accepted, accepted_count, block_table, seq_l
     """Moves the rows of accepted drafts together in all ``pools`` (a KvPools, or the tensors): row
     ``cached_lens[b] + i`` gets what row ``cached_lens[b] + accepted[b, i]`` held, for the leading
     numbers of ``accepted[b, :accepted_count[b]]`` that ascend and lie below ``seq_lens[b]``.
-    Writes and returns ``kept_lens``: the cached rows and the kept ones."""
+    Writes and returns ``kept_lens``: the cached rows and the kept ones. Blocks that hold drafted
+    rows must be the request's own (gqa_kv_release)."""
     if not isinstance(pools, KvPools):
         pools = KvPools(pools)
     rc = _fast.keep(pools.fast, cached_lens, accepted, accepted_count, block_table, seq_lens,
@@ -660,7 +662,12 @@ def gqa_kv_release(block_table, old_lens, new_lens, shares, free_list, free_coun
     """Cuts row b of ``block_table`` from ``old_lens[b]`` rows to ``new_lens[b]`` (0: it has ended).
     Its blocks past the new end lose an owner (``shares`` -= 1); those whose last owner let go are
     appended to ``free_list[:free_count]``, and ``free_left`` gets the new count. ``shares`` [
-    num_blocks] may be None where no block is shared; ``num_blocks`` is needed then."""
+    num_blocks] may be None where no block is shared; ``num_blocks`` is needed then.
+
+    A row whose ``new_lens[b]`` ends inside a block that other rows own as well must not get new
+    rows: they would overwrite the others'. To go back behind a fork and on from there, gqa_kv_fork
+    row b into an unused row, with ``seq_lens[b]`` set to the rows to keep, and release row b
+    whole."""
     rc = _fast.release(block_table, old_lens, new_lens, shares, free_list, free_count, free_left,
                        block_size, num_blocks, _fast_stream(stream))
     if rc is not None:

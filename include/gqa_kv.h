@@ -54,7 +54,9 @@ extern "C" {
  * outside [0, num_blocks); tokens t >= token_start[B] are padding, with slot
  * -1 and position 0. seq_lens[b] = cached_lens[b] + new_lens[b] for served
  * requests and cached_lens[b] for others. free_left[0] = free_count[0] - the
- * served needs. Entries of block_table outside the new columns are kept.
+ * served needs. Entries of block_table outside the new columns are kept. Where
+ * cached_lens[b] ends inside a block, the request's next rows go into that block:
+ * no other request may own it (gqa_kv_release says when one can, and what to do).
  *
  *     cached_lens, new_lens, pos_base  [B] int32 (pos_base may be NULL)
  *     free_list [n_free], free_count [1]  int32; free_count is clamped to [0, n_free]
@@ -183,7 +185,8 @@ int gqa_kv_fork(void *const *pools, int n_pools, int64_t row_bytes, const int32_
  * W and the table's row). Rows from kept_lens[b] on are left as they are;
  * gqa_kv_release takes their blocks. A row whose table entry lies outside
  * [0, num_blocks) is neither read nor written. No two requests may share a block
- * that holds drafted rows (a fork copies partial blocks, so none do).
+ * that holds drafted rows: a fork copies partial blocks, so none do as long as no
+ * row is cut inside a shared block and then extended (gqa_kv_release).
  *
  *     cached_lens, accepted_count, seq_lens [B], accepted [B, W], block_table [B, max_blocks] int32
  *     kept_lens [B] int32; must not overlap an input
@@ -210,6 +213,15 @@ int gqa_kv_keep(void *const *pools, int n_pools, int64_t row_bytes, const int32_
  * (those past n_free are dropped, and free_left is at most n_free). Entries outside
  * [0, num_blocks) are skipped. shares NULL: no block is shared, every entry goes
  * back, and no two entries may name one block. The block table itself is kept.
+ *
+ * A row that is cut keeps the block that new_lens[b] ends in. If that block has
+ * other owners (a request that goes back behind its fork), the row can be read and
+ * forked, but must not get new rows: gqa_kv_tables, gqa_kv_norm_rope_append and
+ * gqa_kv_keep would write them over the other owners'. To go on from there, take
+ * a copy of the row instead of a cut: gqa_kv_fork with parent[f] = b, an unused row as
+ * child[f] and, in the seq_lens it is given, n for seq_lens[b], n being the rows to
+ * keep. The child shares the full blocks and owns a copy of the last n % block_size
+ * rows. Then release row b whole, from the length that it had.
  *
  *     block_table [B, max_blocks], old_lens, new_lens [B] int32 (new_lens is clamped to [0, old_lens])
  *     shares [num_blocks] int32 (not negative) and free_list [n_free] int32, updated in place
