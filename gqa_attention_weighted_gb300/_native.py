@@ -8,9 +8,12 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 from typing import Optional
 
 import torch
+
+from . import build
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIBRARY = os.path.join(_PKG, "libgqa_av.so")
@@ -138,13 +141,24 @@ def _load() -> ctypes.CDLL:
 lib = _load()
 
 
+class _NoFastcall:
+    """In the place of _fastcall where it cannot be loaded: no call is taken there, so the checks
+    below are made in Python (the kernels are the same, a call costs some microseconds more)."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _load_fastcall():
     """The C++ side of the calls that check their tensors there."""
     try:
+        if not build.fastcall_fits():
+            raise ImportError("_fastcall is missing or was built against another torch")
         from . import _fastcall
     except ImportError as e:
-        raise ImportError(f"{_PKG}/_fastcall is missing: build the CUDA library first "
-                          "(python -c 'import __graft_entry__ as g; g.build()')") from e
+        warnings.warn(f"the calls for prompts, drafts and pages check their tensors in Python: {e} "
+                      "(python -c 'import __graft_entry__ as g; g.build()' builds _fastcall)")
+        return _NoFastcall()
     _fastcall.bind(*[ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
                      ("gqa_prompt_attn", "gqa_tree_attn", "gqa_kv_fork", "gqa_kv_keep",
                       "gqa_kv_release")])
