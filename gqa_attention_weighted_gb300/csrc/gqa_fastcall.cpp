@@ -14,6 +14,8 @@
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
+#include <memory>
+#include <new>
 #include <vector>
 
 #include "gqa_kv.h"
@@ -164,19 +166,21 @@ const char* const kPoolsName = "gqa_pools";
 void free_pools(PyObject* x) { delete static_cast<Pools*>(PyCapsule_GetPointer(x, kPoolsName)); }
 
 // addresses (a tuple of ints), device, bytes of a row, num_blocks, block_size
-PyObject* make_pools(PyObject*, PyObject* args) {
+PyObject* make_pools(PyObject*, PyObject* args) try {
   PyObject* list;
   long long dev, row, nb, bs;
   if (!PyArg_ParseTuple(args, "O!LLLL", &PyTuple_Type, &list, &dev, &row, &nb, &bs)) return nullptr;
   if (nb > 0x7fffffff || bs > 0x7fffffff) Py_RETURN_NONE;
-  auto* p = new Pools{{}, dev, row, static_cast<int>(nb), static_cast<int>(bs)};
+  std::unique_ptr<Pools> p(new Pools{{}, dev, row, static_cast<int>(nb), static_cast<int>(bs)});
+  p->at.reserve(static_cast<size_t>(PyTuple_GET_SIZE(list)));
   for (Py_ssize_t i = 0; i < PyTuple_GET_SIZE(list); ++i)
     p->at.push_back(PyLong_AsVoidPtr(PyTuple_GET_ITEM(list, i)));
-  if (PyErr_Occurred()) {
-    delete p;
-    return nullptr;
-  }
-  return PyCapsule_New(p, kPoolsName, free_pools);
+  if (PyErr_Occurred()) return nullptr;
+  PyObject* capsule = PyCapsule_New(p.get(), kPoolsName, free_pools);
+  if (capsule) p.release();   // the capsule's from here on
+  return capsule;
+} catch (const std::bad_alloc&) {
+  return PyErr_NoMemory();
 }
 const Pools* pools_of(PyObject* x, Call* c) {
   if (!PyCapsule_IsValid(x, kPoolsName)) {

@@ -66,3 +66,21 @@ def test_a_compiler_that_fails_leaves_the_library(monkeypatch, tmp_path):
     with pytest.warns(UserWarning, match="no headers"):
         assert build.build() == build.LIBRARY
     assert os.path.exists(build.LIBRARY) and not os.path.exists(build.FASTCALL)
+
+
+def test_no_memory_for_pools_is_an_error_and_not_the_end():
+    # 2^26 addresses (one int, named 2^26 times) in a list of their own, where there is room for
+    # no more than half of it.
+    code = """
+import resource
+from gqa_attention_weighted_gb300 import _native
+many = (1 << 20,) * (1 << 26)
+size = int(open("/proc/self/statm").read().split()[0]) * resource.getpagesize()
+resource.setrlimit(resource.RLIMIT_AS, (size + (1 << 28), size + (1 << 28)))
+try:
+    _native._fast.pools(many, 0, 16, 1, 8)
+except MemoryError:
+    print("refused")
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout == "refused\n", (r.returncode, r.stderr)
