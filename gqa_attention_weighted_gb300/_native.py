@@ -827,12 +827,13 @@ def gqa_tree_attn(q, k_pool, v_pool, token_start, cached_lens, tree_mask, block_
     drafted rows behind them, row j where bit j % 32 of ``tree_mask[t, j // 32]`` is set (itself
     among them), all below ``seq_lens[b]`` (None: all). tree_mask is [T,words] int32; the rest as
     for gqa_prompt_attn."""
-    if tree_mask is not None:
-        rc = _fast.attend(q, k_pool, v_pool, token_start, cached_lens, tree_mask, block_table,
-                          seq_lens, out, scale, _fast_stream(stream))
-        if rc is not None:
-            _check_prompt(rc)
-            return out
+    if tree_mask is None:
+        raise ValueError("gqa_tree_attn needs tree_mask")
+    rc = _fast.attend(q, k_pool, v_pool, token_start, cached_lens, tree_mask, block_table, seq_lens,
+                      out, scale, _fast_stream(stream))
+    if rc is not None:
+        _check_prompt(rc)
+        return out
     if cached_lens is None:
         raise ValueError("gqa_tree_attn needs cached_lens")
     dev, before, after = _packed_attn(q, k_pool, v_pool, token_start, cached_lens, block_table,
