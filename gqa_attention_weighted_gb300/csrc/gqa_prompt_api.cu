@@ -167,25 +167,35 @@ int attend(const Call& c, bool tree, cudaStream_t stream, const Trial& trial = {
 
   // Items: query tiles, one more a sequence than its tokens fill. Slots: a chunk is
   // at least a quarter of an SM's share of the work, so all chunks are at most 4 an
-  // SM, and an item that is cut has more than one and takes less than one more.
+  // SM, and an item that is cut has more than one and takes less than one more. A
+  // chunk is also at least kPtMinChunk key tiles, so a query tile of t key tiles has at
+  // most ceil(t / kPtMinChunk) slots, and a pair, which counts 2 t, at most twice that.
   const int ns = c.D == 256 ? 1 : 2;
   const long long items = (c.T + p.TB - 1) / p.TB + std::min(c.B, c.T);
   p.small = c.B <= kPtSmall && items <= kPtSmall;
   const long long slots = std::min(8LL * sms, 4LL * sms + items * c.Hkv);
+  const long long tiles = (static_cast<long long>(c.max_blocks) * c.block_size + keys - 1) / keys;
+  const long long few = std::min(slots, items * c.Hkv * ((tiles + kPtMinChunk - 1) / kPtMinChunk));
   if ((items + 8LL * sms) * c.Hkv > 0x7fffffffLL)
     return ptfail(GQA_AV_ERR_UNSUPPORTED, "T=%d tokens of %d KV heads are too many for one call",
                   c.T, c.Hkv);
   const size_t at_splits = up256(sizeof(PtHeader));
   const size_t at_units = at_splits + up256(8 * static_cast<size_t>(sms) * sizeof(PtSplit));
   const size_t at_ml = at_units + up256(static_cast<size_t>(items + 8 * sms) * sizeof(PtUnit));
-  const size_t at_o = at_ml + static_cast<size_t>(slots) * ns * 128 * 8;
   bool capturing = false;
   Workspace* ws = nullptr;
   if ((rc = PromptWorkspaces::find(dev, stream, &capturing, &ws))) return rc;
   std::lock_guard<std::mutex> lk(ws->mu);
-  if ((rc = PromptWorkspaces::grow(ws, capturing, at_o + static_cast<size_t>(slots) * ns * 128 * c.D * 4,
-                                   stream)))
-    return rc;
+  // A stream's workspace, of which there are few, is made large enough for any
+  // lengths at once. A capture's holds what its calls can need (7 drafts of 2 heads of
+  // 64 over tables of 512 rows: 0.3 MB where a stream's has 41): a server keeps one a
+  // graph. If a later call of the capture needs more, it at least doubles, because
+  // what was outgrown stays, up to what a stream would have.
+  const size_t slot = static_cast<size_t>(ns) * 128 * (c.D + 2) * 4, all = at_ml + slots * slot;
+  size_t need = capturing ? at_ml + few * slot : all;
+  if (ws->bytes < need && ws->bytes) need = std::max(need, std::min(all, 2 * ws->bytes));
+  if ((rc = PromptWorkspaces::grow(ws, capturing, need, stream))) return rc;
+  const size_t at_o = at_ml + static_cast<size_t>(capturing ? few : slots) * ns * 128 * 8;
   char* base = ws->base;
   p.head = reinterpret_cast<PtHeader*>(base);
   p.splits = reinterpret_cast<PtSplit*>(base + at_splits);

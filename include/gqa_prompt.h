@@ -58,9 +58,11 @@
  * waits for the calls under way on the stream; nothing else synchronises). Calls
  * on different streams and replays of different graphs may overlap; two
  * executable copies of one captured graph must not. A capture's workspace is
- * kept until gqa_prompt_release_graph_workspaces. Its size: up to 8 * SMs slots
- * of 128 * (D + 2) floats (twice that for D below 256) for rows whose keys were
- * cut, and 32 bytes an item of 128 / G tokens. Errors: a status code from
+ * kept until gqa_prompt_release_graph_workspaces. Its size: slots of 128 * (D + 2)
+ * floats (twice that for D below 256) for rows whose keys were cut, and 32 bytes an
+ * item of 128 / G tokens. A stream's has 4 to 8 slots an SM whatever the call (41 to
+ * 160 MB), a capture's no more than its calls can fill: for each KV head and item one
+ * slot for every 512 rows (D = 256: 256) that a table row can hold. Errors: a status code from
  * gqa_av.h; on error nothing is launched and gqa_prompt_last_error() holds a
  * message.
  */
