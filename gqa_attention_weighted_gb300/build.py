@@ -62,7 +62,7 @@ def fastcall_fits() -> bool:
     try:
         with open(FASTCALL_TORCH) as f:
             return os.path.exists(FASTCALL) and f.read() == torch_kind()
-    except OSError:
+    except (OSError, ImportError):
         return False
 
 

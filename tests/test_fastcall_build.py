@@ -84,3 +84,18 @@ except MemoryError:
 """
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout == "refused\n", (r.returncode, r.stderr)
+
+
+def test_a_library_without_torch(monkeypatch):
+    # Who has no torch wants the library alone.
+    def none():
+        raise ImportError("no torch")
+
+    done = []
+    monkeypatch.setattr(build, "torch_kind", none)
+    monkeypatch.setattr(build, "fastcall_command", lambda out: none())
+    monkeypatch.setattr(build, "build_library", lambda verbose: done.append("library"))
+    monkeypatch.setattr(build, "_newer", lambda path: path != build.LIBRARY)
+    with pytest.warns(UserWarning, match="no torch"):
+        assert build.build() == build.LIBRARY
+    assert done == ["library"]
