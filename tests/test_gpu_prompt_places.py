@@ -121,3 +121,13 @@ def test_random_batches(gq, seed):
              pad=int(rng.integers(0, 40)), words=None if seed % 4 else 5)
     got = check(gq, x)
     assert torch.equal(got, call(gq, x))
+
+
+@pytest.mark.parametrize("words,D", [(1, 64), (2, 128), (9, 256)])
+def test_masks_narrower_and_wider_than_the_drafts(gq, words, D):
+    # Bits past the mask's words count as 0; words past the drafts are not looked at.
+    x = make(np.random.default_rng(21), 8, 2, D, 16, "bf16", [50, 0, 300], [100, 33, 7], tree=True,
+             words=words)
+    if words == 9:
+        x["mask"][:, 5:] = -1
+    check(gq, x)
