@@ -156,8 +156,9 @@ __global__ void __launch_bounds__(kForkThreads)
 // Keep
 // ---------------------------------------------------------------------------
 constexpr int kKeepWarps = 8;
-// Rows read before they are written, and CTAs an SM: 64 paths in 48 pools are 1152
-// CTAs (4 and 4: 7.4 us; 8 and 3: 8.8; 4 and 6, 42 registers: 8.2).
+// Rows read before they are written, and CTAs an SM: 64 paths in 48 pools of 2 KB
+// rows are 1536 CTAs, two and a half waves (4 and 4: 7.4 us; 8 and 3: 8.8; 4 and 6,
+// 42 registers: 8.2).
 constexpr int kKeepRows = 4, kKeepCtas = 4;
 
 struct KeepParams {
@@ -311,7 +312,7 @@ __device__ __forceinline__ int release_scan(int x, int* carry, int* part) {
 // order does not depend on who was first:
 //   1. each entry takes one off its block's count;
 //   2. where that left less than 0, the block's smallest entry is found by a
-//      minimum over codes that fall with the entry's number (in the count itself:
+//      minimum over codes that rise with the entry's number (in the count itself:
 //      its value is no longer needed);
 //   3. the entry that finds its own code there is the one; their places are a sum
 //      over the cluster, and the count becomes 0.

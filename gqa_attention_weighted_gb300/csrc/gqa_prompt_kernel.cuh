@@ -56,19 +56,21 @@
 // to the rows that do see them when the unit ends (a slow path that only such
 // caches take).
 //
-// Bounds and figures (device time of a call in short runs, bf16, blocks of 16 if not
-// named). A whole prompt is the tensor cores': 16384 tokens, 32 + 8 heads of 128,
-// 1.30 ms, 1700 TFLOP/s (0.90 of a matrix product's measured rate; in seconds-long
-// runs the chip's 1400 W hold it at 1.42 ms). A pair's key tile takes about 2900
+// Bounds and figures (device time of a call, bf16, blocks of 16 if not named). A
+// whole prompt is the tensor cores': 16384 tokens, 32 + 8 heads of 128, 1.42 ms in
+// loops of calls, 1550 TFLOP/s, where the chip's 1400 W hold it (0.82 of a matrix
+// product's measured burst rate, 0.92 of its sustained one), and 1.30 ms in runs of
+// five calls. The figures below are of short runs. A pair's key tile takes about 2900
 // cycles for 2048 of products: of a stream's own chain, 1024 are products, about
 // 1150 softmax and the rest hand-overs. D = 64 (32 + 4 heads, 4 x 4096 tokens)
-// 318 us, 865 TFLOP/s: the weights' 2 x 128 x 128 exponentials a pair tile outweigh its
-// products; D = 256 (8 + 4 heads, 4 x 4096) 231 us, 1190: one stream. Trees over a
-// cache are HBM's: 64 sequences of 1 to 8192 rows, up to 13 drafts, 182 us, 5.9 TB/s, of
-// which 10 us pass before the first keys arrive. The smallest calls are chains of
-// latencies: 61 tokens of 8 + 2 heads of 64 11 us, 7 drafts over 500 rows 13 us: plan 2,
-// a record 1, table and first keys 2.5, a masked tile 1.5, cleared V 1.5, the unit's
-// end 1.5.
+// 318 us, 865 TFLOP/s: a pair tile has the same 2 x 128 x 128 weights to make for half
+// of the products (which of their instructions bounds it was not measured); D = 256
+// (8 + 4 heads, 4 x 4096) 231 us, 1190: one stream. Trees over a cache are HBM's: 64
+// sequences of 1 to 8192 rows, up to 13 drafts, 182 us (186 in loops of calls), 5.9
+// TB/s, of which 10 us pass before the first keys arrive. The smallest calls are
+// chains of latencies: 61 tokens of 8 + 2 heads of 64 11 us, 7 drafts over 500 rows
+// 13 us: plan 2, a record 1, table and first keys 2.5, a masked tile 1.5, cleared V
+// 1.5, the unit's end 1.5.
 //
 // Warps: 0-3 and 4-7 softmax warpgroups (and the units' ends), 8 issues the
 // MMAs from one thread, 9 hands out units and loads queries and K, 10 loads V,
@@ -101,7 +103,8 @@ constexpr int kPtMinChunk = 4;         // key tiles
 constexpr int kPtCosts = 16384;        // items whose costs the plan keeps
 // Chunks that the plan tries: 1.1 of an SM's share times 2^(-0.0929 i), i < 24, so
 // down to a quarter of it. In key tiles (0.75 us): a unit's start and end; 8 rows
-// of a partial result, written and read; the step that joins them.
+// of a partial result, written and read; the step that joins them. Measured at
+// D = 128 and used for all: a tile of the other widths takes another time.
 constexpr float kPtTopChunk = 1.1f, kPtChunkStep = 0.0929f;
 constexpr float kPtUnitCost = 3.0f, kPtRowCost = 0.14f, kPtJoinCost = 4.0f;
 constexpr int kPtDeep = 4096;          // mean rows that make a batch deep

@@ -56,15 +56,16 @@
  * one for each stream of a capture, which the calls of that capture share; they
  * are allocated with cudaMalloc when first needed or too small (the host then
  * waits for the calls under way on the stream; nothing else synchronises). Calls
- * on different streams and replays of different graphs may overlap; two
+ * on different streams, of any priority, and replays of different graphs may
+ * overlap (the kernel never waits for a block that has not started); two
  * executable copies of one captured graph must not. A capture's workspace is
  * kept until gqa_prompt_release_graph_workspaces. Its size: slots of 128 * (D + 2)
  * floats (twice that for D below 256) for rows whose keys were cut, and 32 bytes an
  * item of 128 / G tokens. A stream's has 4 to 8 slots an SM whatever the call (41 to
  * 160 MB), a capture's no more than its calls can fill: for each KV head and item one
- * slot for every 512 rows (D = 256: 256) that a table row can hold. Errors: a status code from
- * gqa_av.h; on error nothing is launched and gqa_prompt_last_error() holds a
- * message.
+ * slot for every 512 rows (D = 256: 256) that a table row can hold. Errors: a
+ * status code from gqa_av.h; on error nothing is launched and
+ * gqa_prompt_last_error() holds a message.
  */
 #ifndef GQA_PROMPT_H
 #define GQA_PROMPT_H
